@@ -23,6 +23,8 @@
  *   mx_grouped_gemm       the same per MoE expert over row groups
  *   mx_moe_dispatch       rows sorted by expert, gathered and quantized
  *   mx_moe_combine        expert outputs weighted and summed per token
+ * Expert routing, the combine's gradient and the MXFP4 forms are declared in
+ * mxfp8_moe_fp4.h, which this header includes.
  *
  * Number format (OCP Microscaling Formats (MX) v1.0, MXFP8 E4M3):
  *   element  E4M3 ("E4M3FN"): bias 7, largest finite 448 (0x7E), NaN 0x7F/0xFF,
@@ -671,5 +673,8 @@ mx_status mx_grouped_gemm_wgrad(int64_t num_groups, int64_t M, int64_t N, int64_
 #ifdef __cplusplus
 }
 #endif
+
+/* expert routing, the combine's gradient and MXFP4 */
+#include "mxfp8_moe_fp4.h"
 
 #endif /* MXFP8_H */

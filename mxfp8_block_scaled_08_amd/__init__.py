@@ -30,6 +30,9 @@ __all__ = [
     "mx_quantize_dual_grouped", "mx_swiglu_quantize_dual_grouped", "mx_gemm_workspace_bytes", "mx_moe_dispatch_workspace_bytes",
     "mx_grouped_gemm_wgrad_workspace_bytes", "mx_moe_dispatch_noalloc", "MX_OK", "MX_ERR_INVALID_ARG", "MX_ERR_SHAPE", "MX_ERR_ALIGN",
     "MX_ERR_OVERLAP", "MX_ERR_UNSUPPORTED", "MX_ERR_HIP", "MX_BF16", "MX_F32",
+    "mx_moe_route", "mx_moe_route_bwd", "mx_moe_combine_bwd", "mx_quantize_rowwise_fp4", "mx_quantize_colwise_fp4",
+    "mx_dequantize_fp4", "mx_moe_dispatch_fp4", "mx_swiglu_quantize_fp4", "mx_gemm_fp4", "mx_gemm_fp4_workspace_bytes",
+    "mx_grouped_gemm_fp4", "MX_SCORE_SOFTMAX", "MX_SCORE_SIGMOID",
 ]
 
 MX_OK, MX_ERR_INVALID_ARG, MX_ERR_SHAPE, MX_ERR_ALIGN = 0, 1, 2, 3
@@ -775,3 +778,10 @@ def mx_swiglu_quantize_dual_grouped(gu: torch.Tensor, group_offsets: torch.Tenso
                                                 _dev(st_swz, "st_swz", torch.uint8), _stream(stream))
     _check("mx_swiglu_quantize_dual_grouped", st)
     return q, s_swz, qt, st_swz, pad_offsets
+
+
+# expert routing, the combine's gradient and MXFP4 (include/mxfp8_moe_fp4.h)
+from .moe_fp4 import (MX_SCORE_SIGMOID, MX_SCORE_SOFTMAX, mx_dequantize_fp4, mx_gemm_fp4,  # noqa: E402
+                      mx_gemm_fp4_workspace_bytes, mx_grouped_gemm_fp4, mx_moe_combine_bwd, mx_moe_dispatch_fp4,
+                      mx_moe_route, mx_moe_route_bwd, mx_quantize_colwise_fp4, mx_quantize_rowwise_fp4,
+                      mx_swiglu_quantize_fp4)

@@ -161,6 +161,52 @@ hipError_t launch_grouped_gemm_wgrad(int64_t G, int64_t M, int64_t N, int64_t K,
 hipError_t launch_swiglu_quantize(const void *gu, int64_t rows, int64_t F, int64_t ld_gu, void *h,
                                   int64_t ld_h, void *q, int64_t ld_q, void *s_swz, hipStream_t stream);
 
+// Routing (mx_route.hip): softmax or sigmoid scores, logits' dtype 0 = BF16,
+// 1 = FP32; experts <= MOE_MAX_EXPERTS, topk <= ROUTE_MAX_TOPK, groups <=
+// ROUTE_MAX_GROUPS.
+constexpr int ROUTE_MAX_TOPK = 32;
+constexpr int ROUTE_MAX_GROUPS = 64;
+hipError_t launch_moe_route(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t ld,
+                            const float *bias, bool softmax, int64_t groups, int64_t keep_groups, int64_t group_top,
+                            int64_t topk, bool renorm, float scale, const uint8_t *mask, int32_t *ids, float *weights,
+                            hipStream_t stream);
+hipError_t launch_moe_route_bwd(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t ld,
+                                bool softmax, int64_t topk, bool renorm, float scale, const int32_t *ids,
+                                const float *dw, void *dx, int64_t ld_d, hipStream_t stream);
+
+// Gradient of the combine: dy and dw may each be null (y too without dw).
+hipError_t launch_moe_combine_bwd(const void *d_out, int64_t tokens, int64_t hidden, int64_t ld_dout, const void *y,
+                                  int64_t ld_y, const int32_t *slot, const float *weights, int64_t topk, void *dy,
+                                  int64_t ld_dy, float *dw, hipStream_t stream);
+
+// MXFP4 (mx_fp4.hip): E2M1 leading dimensions in bytes, scales rearranged.
+hipError_t launch_quantize_rowwise_fp4(const void *x, int64_t rows, int64_t cols, int64_t ld_x, void *q, int64_t ld_q,
+                                       void *s_swz, int64_t s_tiles, hipStream_t stream);
+hipError_t launch_quantize_colwise_fp4(const void *x, int64_t count, int64_t rows, int64_t cols, int64_t ld_x,
+                                       void *qt, int64_t ld_qt, void *st_swz, hipStream_t stream);
+hipError_t launch_dequantize_fp4(const void *q, int64_t rows, int64_t cols, int64_t ld_q, const void *s_swz,
+                                 int64_t s_tiles, void *y, int64_t ld_y, int y_dtype, hipStream_t stream);
+hipError_t launch_moe_dispatch_fp4(const void *x, int64_t tokens, int64_t hidden, int64_t ld_x,
+                                   const int32_t *topk_ids, int64_t topk, int64_t experts, int64_t *offsets,
+                                   int32_t *src_token, int32_t *slot, void *q, int64_t ld_q, void *s_swz, void *ws,
+                                   hipStream_t stream);
+hipError_t launch_swiglu_quantize_fp4(const void *gu, int64_t rows, int64_t F, int64_t ld_gu, void *h, int64_t ld_h,
+                                      void *q, int64_t ld_q, void *s_swz, hipStream_t stream);
+// The dispatch's ordering alone: offsets, src_token and slot (mx_moe.hip).
+void launch_dispatch_order(const int32_t *topk_ids, int64_t tokens, int64_t topk, int64_t experts, int64_t *offsets,
+                           int32_t *src_token, int32_t *slot, void *ws, hipStream_t stream);
+
+// MXFP4 products (mx_gemm_fp4.hip): ld_a, ld_b in bytes, K % 256 == 0.  ws: at
+// least gemm_fp4_workspace_bytes(...) bytes, 16-byte aligned (may be null when
+// that is 0).
+int64_t gemm_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int c_dtype, bool vec16);
+hipError_t launch_gemm_fp4(int64_t M, int64_t N, int64_t K, const void *a_q, int64_t ld_a, const void *a_s,
+                           const void *b_q, int64_t ld_b, const void *b_s, void *c, int64_t ld_c, int c_dtype,
+                           void *ws, hipStream_t stream);
+hipError_t launch_grouped_gemm_fp4(int64_t G, int64_t M_total, int64_t N, int64_t K, const int64_t *offsets,
+                                   const void *a_q, int64_t ld_a, const void *a_s, const void *b_q, const void *b_s,
+                                   void *c, int64_t ld_c, int c_dtype, hipStream_t stream);
+
 // Debug check of device offsets off[0..G] (see mx_debug.hip): waits for the
 // stream (the one wait in the library, under MX_DEBUG only), then *first_bad = the first entry breaking the stated properties
 // (in [0, total], multiple of align, ranges at least min_len long,

@@ -228,9 +228,8 @@ hipError_t moe_noalloc_scratch(void **ptr)
 
 // The dispatch's ordering: offsets, src_token and slot (four small kernels,
 // the chunk counts in ws).
-static void launch_dispatch_order(const int32_t *topk_ids, int64_t tokens, int64_t topk, int64_t experts,
-                                  int64_t *offsets, int32_t *src_token, int32_t *slot, void *ws,
-                                  hipStream_t stream)
+void launch_dispatch_order(const int32_t *topk_ids, int64_t tokens, int64_t topk, int64_t experts, int64_t *offsets,
+                           int32_t *src_token, int32_t *slot, void *ws, hipStream_t stream)
 {
     const int64_t n = tokens * topk;
     const int64_t chunks = (n + MOE_CHUNK - 1) / MOE_CHUNK;

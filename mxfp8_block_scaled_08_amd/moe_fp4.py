@@ -1,0 +1,396 @@
+"""Binding of the ABI's second part (``include/mxfp8_moe_fp4.h``): routing of
+tokens to experts and its gradient, the gradient of the MoE combine, and MXFP4
+quantization and products.
+
+As in the package's other functions, outputs that are passed in are written in
+place and the rest are new tensors.  Every tensor of a call lives on one
+device; the call runs on that device, on its current stream or on ``stream``,
+and what it allocates belongs to that stream.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+import inspect
+from typing import Optional, Tuple
+
+import torch
+
+from . import (_OUT, MX_BF16, MX_F32, _check, _ld, _u8, load, mx_moe_dispatch_workspace_bytes,
+               mx_scale_swizzled_bytes)
+
+MX_SCORE_SOFTMAX, MX_SCORE_SIGMOID = 0, 1
+
+_SCORES = {"softmax": MX_SCORE_SOFTMAX, "sigmoid": MX_SCORE_SIGMOID}
+_i, _l, _f, _p = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
+_ARGS = {
+    "mx_moe_route": [_p, _i, _l, _l, _l, _p, _i, _l, _l, _l, _l, _i, _f, _p, _p, _p, _p],
+    "mx_moe_route_bwd": [_p, _i, _l, _l, _l, _i, _l, _i, _f, _p, _p, _p, _l, _p],
+    "mx_moe_combine_bwd": [_p, _l, _l, _l, _p, _l, _p, _p, _l, _p, _l, _p, _p],
+    "mx_quantize_rowwise_fp4": [_p, _l, _l, _l, _p, _l, _p, _l, _p],
+    "mx_quantize_colwise_fp4": [_p, _l, _l, _l, _l, _p, _l, _p, _p],
+    "mx_dequantize_fp4": [_p, _l, _l, _l, _p, _l, _p, _l, _i, _p],
+    "mx_moe_dispatch_fp4": [_p, _l, _l, _l, _p, _l, _l, _p, _p, _p, _p, _l, _p, _p, _l, _p],
+    "mx_swiglu_quantize_fp4": [_p, _l, _l, _l, _p, _l, _p, _l, _p, _p],
+    "mx_gemm_fp4": [_l, _l, _l, _p, _l, _p, _p, _l, _p, _p, _l, _i, _p, _l, _p],
+    "mx_grouped_gemm_fp4": [_l, _l, _l, _l, _p, _p, _l, _p, _p, _p, _p, _l, _i, _p],
+}
+_fns = {}
+
+
+def _fn(name: str):
+    """The library's entry point, its argument types set on first use."""
+    f = _fns.get(name)
+    if f is None:
+        f = getattr(load(), name)
+        f.restype = ctypes.c_int
+        f.argtypes = _ARGS[name]
+        _fns[name] = f
+    return f
+
+
+def _call(name: str, *args) -> None:
+    """The entry point on the current device's current stream."""
+    _check(name, _fn(name)(*args, torch.cuda.current_stream().cuda_stream))
+
+
+def _entry(fn):
+    """Run fn with its first tensor's device current and, where stream is
+    given, with that stream current, so that the work, and every tensor that
+    the call allocates, belongs to it."""
+    name = next(iter(inspect.signature(fn).parameters))
+
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else kw[name]
+        if not first.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        dev = first.device
+        if stream is None and dev.index == torch.cuda.current_device():
+            return fn(*args, **kw)
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        elif not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _at(t: Optional[torch.Tensor], name: str, dev, *dtypes, shape=None, least: int = 0) -> Optional[int]:
+    """Pointer of t (None stays None), which must lie on dev and have one of
+    the dtypes and, where given, the shape (contiguous) or at least so many
+    elements, contiguous."""
+    if t is None:
+        return None
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, is on {t.device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if shape is not None and (tuple(t.shape) != shape or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
+    if least and (t.numel() < least or not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous and hold {least} elements, holds {t.numel()}")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, dev, rows: int, cols: int, *dtypes) -> Tuple[int, int]:
+    """(pointer, leading dimension) of a [rows][cols] row-major view on dev."""
+    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}][{cols}], got {list(t.shape)}")
+    if rows > 1 and cols > 1:
+        ld = _ld(t, name)
+    elif rows > 1 and cols == 1:
+        ld = t.stride(0)
+    else:  # one row, or nothing: the stride says nothing (torch gives any value); a whole number of 16 bytes
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must be a 2-D row-major view")
+        per = max(1, 16 // t.element_size())
+        ld = (cols + per - 1) // per * per
+    return _at(t, name, dev, *dtypes), ld
+
+
+_U8 = torch.uint8
+_LOGITS = {torch.bfloat16: MX_BF16, torch.float32: MX_F32}
+
+
+def _score(score: str) -> int:
+    if score not in _SCORES:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    return _SCORES[score]
+
+
+@_entry
+def mx_moe_route(logits: torch.Tensor, topk: int, *, bias: Optional[torch.Tensor] = None, score: str = "softmax",
+                 num_groups: int = 1, topk_groups: int = 1, group_top: int = 1, renormalize: bool = True,
+                 scale: float = 1.0, mask: Optional[torch.Tensor] = None, topk_ids: Optional[torch.Tensor] = None,
+                 weights: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """logits [tokens][num_experts] (BF16 or FP32) -> (topk_ids int32, weights
+    float32, both [tokens][topk]): each token's experts by decreasing score and
+    their weights, what mx_moe_dispatch and mx_moe_combine take.
+
+    bias (float32 [num_experts]) is added for the selection only; with
+    num_groups > 1 only the topk_groups groups whose group_top best scores sum
+    highest are chosen from; mask (uint8 or bool [tokens]) keeps tokens with 0
+    unrouted (ids -1, weights 0), as experts with a logit of -inf are."""
+    tokens, experts = logits.shape
+    dev = logits.device
+    if topk_ids is None:
+        topk_ids = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((tokens, topk), dtype=torch.float32, device=dev)
+    x, ld = _rows(logits, "logits", dev, tokens, experts, *_LOGITS)
+    _call("mx_moe_route", x, _LOGITS[logits.dtype], tokens, experts, ld,
+          _at(bias, "bias", dev, torch.float32, shape=(experts,)), _score(score), num_groups, topk_groups, group_top,
+          topk, int(renormalize), scale, _at(mask, "mask", dev, _U8, torch.bool, shape=(tokens,)),
+          _at(topk_ids, "topk_ids", dev, torch.int32, shape=(tokens, topk)),
+          _at(weights, "weights", dev, torch.float32, shape=(tokens, topk)))
+    return topk_ids, weights
+
+
+@_entry
+def mx_moe_route_bwd(d_weights: torch.Tensor, logits: torch.Tensor, topk_ids: torch.Tensor, *, score: str = "softmax",
+                     renormalize: bool = True, scale: float = 1.0, d_logits: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """Gradient of mx_moe_route's weights with respect to the logits (the
+    choice topk_ids held fixed): [tokens][num_experts] of the logits' type."""
+    tokens, experts = logits.shape
+    topk = topk_ids.shape[1]
+    dev = d_weights.device
+    if d_logits is None:
+        d_logits = torch.empty((tokens, experts), dtype=logits.dtype, device=dev)
+    x, ld = _rows(logits, "logits", dev, tokens, experts, *_LOGITS)
+    d, ld_d = _rows(d_logits, "d_logits", dev, tokens, experts, logits.dtype)
+    _call("mx_moe_route_bwd", x, _LOGITS[logits.dtype], tokens, experts, ld, _score(score), topk, int(renormalize),
+          scale, _at(topk_ids, "topk_ids", dev, torch.int32, shape=(tokens, topk)),
+          _at(d_weights, "d_weights", dev, torch.float32, shape=(tokens, topk)), d, ld_d)
+    return d_logits
+
+
+@_entry
+def mx_moe_combine_bwd(d_out: torch.Tensor, y: Optional[torch.Tensor], slot: torch.Tensor, weights: torch.Tensor,
+                       dy: Optional[torch.Tensor] = None, d_weights: Optional[torch.Tensor] = None,
+                       want_dy: bool = True, want_d_weights: bool = True,
+                       stream=None) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """Gradients of mx_moe_combine: (dy BF16 [tokens*topk][hidden], d_weights
+    float32 [tokens][topk]); either can be left out (then y may be None without
+    d_weights).  Rows of dy that no slot names are not written (a new dy holds
+    zeros there)."""
+    tokens, topk = weights.shape
+    hidden = d_out.shape[1]
+    n = tokens * topk
+    dev = d_out.device
+    bf = torch.bfloat16
+    if want_dy and dy is None:
+        dy = torch.zeros((n, hidden), dtype=bf, device=dev)
+    if want_d_weights and d_weights is None:
+        d_weights = torch.empty((tokens, topk), dtype=torch.float32, device=dev)
+    if want_d_weights and y is None:
+        raise ValueError("d_weights needs y")
+    o, ld_o = _rows(d_out, "d_out", dev, tokens, hidden, bf)
+    py, ld_y = _rows(y, "y", dev, n, hidden, bf) if want_d_weights else (None, 0)
+    pd, ld_dy = _rows(dy, "dy", dev, n, hidden, bf) if want_dy else (None, 0)
+    if tuple(slot.shape) not in ((n,), (tokens, topk)):
+        raise ValueError(f"slot must hold {n} entries, got {list(slot.shape)}")
+    _call("mx_moe_combine_bwd", o, tokens, hidden, ld_o, py, ld_y,
+          _at(slot, "slot", dev, torch.int32, shape=tuple(slot.shape)),
+          _at(weights, "weights", dev, torch.float32, shape=(tokens, topk)), topk, pd, ld_dy,
+          _at(d_weights, "d_weights", dev, torch.float32, shape=(tokens, topk)) if want_d_weights else None)
+    return dy if want_dy else None, d_weights if want_d_weights else None
+
+
+def _swizzled(s: Optional[torch.Tensor], rows: int, tiles: int, cols: int, name: str, dev):
+    """(tensor, pointer) of rearranged scales with `tiles` tiles a tile row (a
+    new buffer if None)."""
+    need = max(0, ((rows + 31) // 32 - 1) * tiles + cols // 256) * 256 if rows and cols else 0
+    if s is None:
+        s = torch.empty(max(need, (rows + 31) // 32 * tiles * 256, 1), dtype=_U8, device=dev)
+    s = _u8(s)
+    return s, _at(s, name, dev, _U8, least=need)
+
+
+@_entry
+def mx_quantize_rowwise_fp4(x: torch.Tensor, q: Optional[torch.Tensor] = None, s_swz: Optional[torch.Tensor] = None,
+                            s_tiles: Optional[int] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """BF16 x[rows][cols] -> (q uint8 [rows][cols/2] E2M1, two codes a byte,
+    s_swz: its scales in the products' layout)."""
+    rows, cols = x.shape
+    dev = x.device
+    if q is None:
+        q = torch.empty((rows, cols // 2), dtype=_U8, device=dev)
+    if s_tiles is None:
+        s_tiles = cols // 256
+    s_swz, ps = _swizzled(s_swz, rows, s_tiles, cols, "s_swz", dev)
+    px, ld_x = _rows(x, "x", dev, rows, cols, torch.bfloat16)
+    pq, ld_q = _rows(q, "q", dev, rows, cols // 2, _U8)
+    _call("mx_quantize_rowwise_fp4", px, rows, cols, ld_x, pq, ld_q, ps, s_tiles)
+    return q, s_swz
+
+
+@_entry
+def mx_quantize_colwise_fp4(x: torch.Tensor, qt: Optional[torch.Tensor] = None, st_swz: Optional[torch.Tensor] = None,
+                            stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """BF16 x [rows][cols], or a stack [count][rows][cols] -> (qt uint8
+    [(count][)cols][rows/2], st_swz): each tensor quantized down its columns and
+    written transposed, the stack's scales back to back."""
+    if x.dim() == 3:
+        count, rows, cols = x.shape
+        if not x.is_contiguous():
+            raise ValueError("a stack must be contiguous [count][rows][cols]")
+        flat, shape = x.view(count * rows, cols), (count, cols, rows // 2)
+    else:
+        (rows, cols), count = x.shape, 1
+        flat, shape = x, (cols, rows // 2)
+    dev = x.device
+    if qt is None:
+        qt = torch.empty(shape, dtype=_U8, device=dev)
+    if tuple(qt.shape) != shape or (x.dim() == 3 and not qt.is_contiguous()):
+        raise ValueError(f"qt must be {list(shape)}, and contiguous for a stack, got {list(qt.shape)}")
+    need = count * mx_scale_swizzled_bytes(cols, rows // 32)
+    if st_swz is None:
+        st_swz = torch.empty(max(need, 1), dtype=_U8, device=dev)
+    st_swz = _u8(st_swz)
+    px, ld_x = _rows(flat, "x", dev, count * rows, cols, torch.bfloat16)
+    pq, ld_qt = _rows(qt.view(count * cols, rows // 2) if x.dim() == 3 else qt, "qt", dev, count * cols, rows // 2, _U8)
+    _call("mx_quantize_colwise_fp4", px, count, rows, cols, ld_x, pq, ld_qt,
+          _at(st_swz, "st_swz", dev, _U8, least=need))
+    return qt, st_swz
+
+
+@_entry
+def mx_dequantize_fp4(q: torch.Tensor, s_swz: torch.Tensor, y: Optional[torch.Tensor] = None,
+                      out_dtype: torch.dtype = torch.bfloat16, s_tiles: Optional[int] = None,
+                      stream=None) -> torch.Tensor:
+    """The values of an MXFP4 operand (q [rows][cols/2], rearranged scales) as
+    BF16 or FP32 [rows][cols]; exact in both."""
+    rows, half = q.shape
+    cols = 2 * half
+    dev = q.device
+    if y is None:
+        y = torch.empty((rows, cols), dtype=out_dtype, device=dev)
+    if s_tiles is None:
+        s_tiles = cols // 256
+    pq, ld_q = _rows(q, "q", dev, rows, half, _U8)
+    py, ld_y = _rows(y, "y", dev, rows, cols, *_OUT)
+    _, ps = _swizzled(s_swz, rows, s_tiles, cols, "s_swz", dev)
+    _call("mx_dequantize_fp4", pq, rows, cols, ld_q, ps, s_tiles, py, ld_y, _OUT[y.dtype])
+    return y
+
+
+@_entry
+def mx_moe_dispatch_fp4(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: int,
+                        offsets: Optional[torch.Tensor] = None, src: Optional[torch.Tensor] = None,
+                        slot: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                        s_swz: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """mx_moe_dispatch with MXFP4 rows: (offsets, src_token, slot, q uint8
+    [tokens*topk][hidden/2], s_swz)."""
+    tokens, hidden = x.shape
+    if topk_ids.dim() != 2 or topk_ids.shape[0] != tokens:
+        raise ValueError("topk_ids must be [tokens][topk]")
+    topk = topk_ids.shape[1]
+    n = tokens * topk
+    dev = x.device
+    i32 = torch.int32
+    if offsets is None:
+        offsets = torch.empty(num_experts + 1, dtype=torch.int64, device=dev)
+    if src is None:
+        src = torch.empty(n, dtype=i32, device=dev)
+    if slot is None:
+        slot = torch.empty(n, dtype=i32, device=dev)
+    if q is None:
+        q = torch.empty((n, hidden // 2), dtype=_U8, device=dev)
+    s_swz, ps = _swizzled(s_swz, n, hidden // 256, hidden, "s_swz", dev)
+    need = mx_moe_dispatch_workspace_bytes(tokens, topk, num_experts)
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=_U8, device=dev)
+    px, ld_x = _rows(x, "x", dev, tokens, hidden, torch.bfloat16)
+    pq, ld_q = _rows(q, "q", dev, n, hidden // 2, _U8)
+    _call("mx_moe_dispatch_fp4", px, tokens, hidden, ld_x, _at(topk_ids, "topk_ids", dev, i32, shape=(tokens, topk)),
+          topk, num_experts, _at(offsets, "offsets", dev, torch.int64, shape=(num_experts + 1,)),
+          _at(src, "src", dev, i32, shape=(n,)), _at(slot, "slot", dev, i32, shape=(n,)), pq, ld_q, ps,
+          *_scratch(workspace, dev))
+    return offsets, src, slot, q, s_swz
+
+
+def _scratch(workspace: Optional[torch.Tensor], dev) -> Tuple[Optional[int], int]:
+    if workspace is None:
+        return None, 0
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+@_entry
+def mx_swiglu_quantize_fp4(gu: torch.Tensor, q: Optional[torch.Tensor] = None, s_swz: Optional[torch.Tensor] = None,
+                           h: Optional[torch.Tensor] = None, want_h: bool = False, stream=None):
+    """gu [rows][2F] BF16 (gate | up) -> (q uint8 [rows][F/2], s_swz, h or
+    None): mx_swiglu_quantize with MXFP4 output."""
+    rows, F2 = gu.shape
+    F = F2 // 2
+    dev = gu.device
+    if q is None:
+        q = torch.empty((rows, F // 2), dtype=_U8, device=dev)
+    s_swz, ps = _swizzled(s_swz, rows, F // 256, F, "s_swz", dev)
+    if h is None and want_h:
+        h = torch.empty((rows, F), dtype=torch.bfloat16, device=dev)
+    pg, ld_gu = _rows(gu, "gu", dev, rows, F2, torch.bfloat16)
+    ph, ld_h = _rows(h, "h", dev, rows, F, torch.bfloat16) if h is not None else (None, 0)
+    pq, ld_q = _rows(q, "q", dev, rows, F // 2, _U8)
+    _call("mx_swiglu_quantize_fp4", pg, rows, F, ld_gu, ph, ld_h, pq, ld_q, ps)
+    return q, s_swz, h
+
+
+def mx_gemm_fp4_workspace_bytes(M: int, N: int, K: int, out_dtype: torch.dtype = torch.bfloat16) -> int:
+    """Device scratch mx_gemm_fp4 needs for this shape (0: none), host-only."""
+    f = _fns.get("mx_gemm_fp4_workspace_bytes")
+    if f is None:
+        f = load().mx_gemm_fp4_workspace_bytes
+        f.restype, f.argtypes = ctypes.c_int64, [_l, _l, _l, _i]
+        _fns["mx_gemm_fp4_workspace_bytes"] = f
+    return f(M, N, K, _OUT[out_dtype])
+
+
+@_entry
+def mx_gemm_fp4(a_q: torch.Tensor, a_s_swz: torch.Tensor, b_q: torch.Tensor, b_s_swz: torch.Tensor,
+                c: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """C[M][N] = deq(A) . deq(B)^T for MXFP4 operands A [M][K/2 bytes], B
+    [N][K/2 bytes].  workspace: device scratch of at least
+    mx_gemm_fp4_workspace_bytes bytes when that is nonzero (a new tensor if
+    None)."""
+    M, half = a_q.shape
+    N, K = b_q.shape[0], 2 * half
+    dev = a_q.device
+    if c is None:
+        c = torch.empty((M, N), dtype=out_dtype, device=dev)
+    pa, ld_a = _rows(a_q, "a_q", dev, M, half, _U8)
+    pb, ld_b = _rows(b_q, "b_q", dev, N, half, _U8)
+    pc, ld_c = _rows(c, "c", dev, M, N, *_OUT)
+    if workspace is None:
+        need = mx_gemm_fp4_workspace_bytes(M, N, K, c.dtype)
+        workspace = torch.empty(need, dtype=_U8, device=dev) if need else None
+    _call("mx_gemm_fp4", M, N, K, pa, ld_a, _swizzled(a_s_swz, M, K // 256, K, "a_s_swz", dev)[1], pb, ld_b,
+          _swizzled(b_s_swz, N, K // 256, K, "b_s_swz", dev)[1], pc, ld_c, _OUT[c.dtype], *_scratch(workspace, dev))
+    return c
+
+
+@_entry
+def mx_grouped_gemm_fp4(group_offsets: torch.Tensor, a_q: torch.Tensor, a_s_swz: torch.Tensor, b_q: torch.Tensor,
+                        b_s_swz: torch.Tensor, c: Optional[torch.Tensor] = None,
+                        out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """Per-expert C: rows [off[g], off[g+1]) of A times B_g^T, B as
+    [G][N][K/2 bytes], MXFP4.  Rows outside every group are not written."""
+    M, half = a_q.shape
+    G, N, _ = b_q.shape
+    K = 2 * half
+    dev = group_offsets.device
+    if c is None:
+        c = torch.empty((M, N), dtype=out_dtype, device=dev)
+    pa, ld_a = _rows(a_q, "a_q", dev, M, half, _U8)
+    pc, ld_c = _rows(c, "c", dev, M, N, *_OUT)
+    _call("mx_grouped_gemm_fp4", G, M, N, K, _at(group_offsets, "group_offsets", dev, torch.int64, shape=(G + 1,)),
+          pa, ld_a, _swizzled(a_s_swz, M, K // 256, K, "a_s_swz", dev)[1], _at(b_q, "b_q", dev, _U8, shape=(G, N, half)),
+          _at(b_s_swz, "b_s_swz", dev, _U8, least=G * mx_scale_swizzled_bytes(N, K // 32)), pc, ld_c, _OUT[c.dtype])
+    return c

@@ -31,9 +31,9 @@ static mx_status check_route(const char *fn, int dtype, int64_t tokens, int64_t 
                     (long long)experts);
     if (!std::isfinite(scale))
         return fail(MX_ERR_INVALID_ARG, "%s: scale is not finite", fn);
-    // (tokens and ld bound every byte offset below 2^63)
-    if (tokens >= ((int64_t)1 << 31) || ld >= ((int64_t)1 << 28))
-        return fail(MX_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 tokens or a leading dimension of 2^28", fn);
+    // (a launch has at most 2^32 - 1 threads, up to 64 a token)
+    if (tokens >= ((int64_t)1 << 26) || ld >= ((int64_t)1 << 28))
+        return fail(MX_ERR_UNSUPPORTED, "%s: 2^26 tokens or more, or a leading dimension of 2^28", fn);
     return MX_OK;
 }
 

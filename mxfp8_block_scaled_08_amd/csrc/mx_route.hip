@@ -1,39 +1,76 @@
 // Routing of tokens to experts, its gradient, and the gradient of the MoE
 // combine (gfx950).
 //
-// Routing.  Sixteen lanes (one DPP row) take a token, four tokens a wave;
-// lane l holds the selection keys of experts l*EPL .. +EPL-1 in registers.  A
-// key is a 64-bit integer: the order-preserving pattern of the selection
-// score (FP64) in its upper 54 bits and 1023 - expert in the low 10, so one
-// unsigned maximum finds the largest score and, among equal ones, the lowest
-// expert.  The top-k are taken one by one: a 16-lane maximum by four DPP row
-// rotations, then the owning lane drops the key.  Scores with a bias are
-// formed in FP64 because two experts' sums are compared, not approximated: in
-// FP32 about one row in ten thousand would swap two experts.  FP64 costs the
-// same issue slots as FP32 on CDNA4's vector unit.
+// Routing.  LANES lanes take a token (16 up to 128 experts, 32 up to 256, else
+// the wave), so a wave holds 4, 2 or 1 tokens; lane l holds the selection keys
+// of experts l*EPL .. +EPL-1 in registers, 4 to 16 of them.  A key is a double:
+// the selection score with its low 10 mantissa bits replaced by the expert's
+// number, in such a way that of two equal scores the lower expert's key is the
+// larger, so one v_max_f64 finds both the best score and the lowest expert that
+// has it.  The top-k are taken one by one: EPL - 1 maxima in the lane, four DPP
+// row rotations (and the two half-swaps for wider tokens) across the lanes, then
+// the owning lane drops the key.  Scores with a bias are formed in FP64 because
+// two experts' sums are compared, not approximated: in FP32 about one row in ten
+// thousand would swap two experts.  FP64 costs the same issue slots as FP32 on
+// CDNA4's vector unit.
 #include "mx_device.h"
 #include "mx_launch.h"
 
 #include <algorithm>
 #include <math.h>
+#include <type_traits>
 
 namespace mx {
 
-constexpr int RT_LANES = 16;            // lanes per token
-constexpr int RT_TOKENS = 64 / RT_LANES;  // tokens per wave
-static_assert(ROUTE_MAX_TOPK == 2 * RT_LANES, "each lane keeps two of the chosen");
+static_assert(ROUTE_MAX_TOPK <= 32, "a 16-lane token keeps two of the chosen a lane, a wider one one");
 static_assert(ROUTE_MAX_GROUPS == 64, "kept groups are a 64-bit mask");
+static_assert(MOE_MAX_EXPERTS == 1024, "keys hold 10 bits of expert number");
 
-__device__ __forceinline__ float bf16_f32(uint16_t v) { return __builtin_bit_cast(float, (uint32_t)v << 16); }
+typedef float f4_t __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ uint16_t f32_bf16(float v)
-{
-    return __builtin_bit_cast(uint16_t, (__bf16)v);
-}
+__device__ __forceinline__ float bf16_f32(uint32_t v) { return __builtin_bit_cast(float, v << 16); }
 
 template <int DT> __device__ __forceinline__ float logit_at(const void *p, int64_t i)
 {
     return DT == 0 ? bf16_f32(reinterpret_cast<const uint16_t *>(p)[i]) : reinterpret_cast<const float *>(p)[i];
+}
+
+// A lane's EPL consecutive logits from expert e0 of the row at element `row`;
+// -inf past the experts and where the token is not live.  vec: rows are aligned
+// to 16 bytes (8 for 4 BF16) and experts a multiple of EPL, so a lane's run is
+// whole and loads as vectors.
+template <int EPL, int DT>
+__device__ __forceinline__ void load_logits(const void *p, int64_t row, int e0, int experts, bool live, bool vec,
+                                            float *x)
+{
+    if (vec) {
+        const bool in = live && e0 < experts;
+        if (DT == 0) {
+#pragma unroll
+            for (int i = 0; i < EPL; i += 4) {
+                const uint2 w = in ? *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p) + row + e0 + i)
+                                   : make_uint2(0xFF80FF80u, 0xFF80FF80u);
+                x[i] = bf16_f32(w.x & 0xFFFFu);
+                x[i + 1] = bf16_f32(w.x >> 16);
+                x[i + 2] = bf16_f32(w.y & 0xFFFFu);
+                x[i + 3] = bf16_f32(w.y >> 16);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; i += 4) {
+                f4_t w = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if (in)
+                    w = *reinterpret_cast<const f4_t *>(reinterpret_cast<const float *>(p) + row + e0 + i);
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    x[i + k] = w[k];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL; i++)
+            x[i] = live && e0 + i < experts ? logit_at<DT>(p, row + e0 + i) : -INFINITY;
+    }
 }
 
 // Rotation by N within each row of 16 lanes.
@@ -41,70 +78,96 @@ template <int N> __device__ __forceinline__ uint32_t ror16(uint32_t v)
 {
     return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x120 + N, 0xF, 0xF, false);
 }
-template <int N> __device__ __forceinline__ float ror16(float v)
+// The value of this lane's partner rows: rows 0 and 1, 2 and 3 (ROWS 16) or
+// the wave's halves (ROWS 32) exchanged; lo holds the lower one's in both,
+// hi the upper one's.
+template <int ROWS> __device__ __forceinline__ void halves(uint32_t v, uint32_t &lo, uint32_t &hi)
 {
-    return __builtin_bit_cast(float, ror16<N>(__builtin_bit_cast(uint32_t, v)));
-}
-template <int N> __device__ __forceinline__ uint64_t ror16(uint64_t v)
-{
-    return ((uint64_t)ror16<N>((uint32_t)(v >> 32)) << 32) | ror16<N>((uint32_t)v);
-}
-template <int N> __device__ __forceinline__ double ror16(double v)
-{
-    return __builtin_bit_cast(double, ror16<N>(__builtin_bit_cast(uint64_t, v)));
+    const auto s = ROWS == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                              : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    lo = s[0];
+    hi = s[1];
 }
 
-// Reductions over a row of 16 lanes, the result in every lane.  The rotations
-// pair the lanes in a fixed way, so a sum's order is fixed; for the sums every
-// lane adds the same pairs in one order or the other (addition commutes).
-template <typename T, typename F> __device__ __forceinline__ T reduce16(T v, F f)
-{
-    v = f(v, ror16<8>(v));
-    v = f(v, ror16<4>(v));
-    v = f(v, ror16<2>(v));
-    v = f(v, ror16<1>(v));
-    return v;
-}
-template <typename T> __device__ __forceinline__ T sum16(T v)
-{
-    return reduce16(v, [](T a, T b) { return a + b; });
-}
-__device__ __forceinline__ uint64_t max16(uint64_t v)
-{
-    return reduce16(v, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
-}
-// FP64 patterns in value order as unsigned integers: -inf lowest, NaN (any)
-// highest, both zeros alike.
-__device__ __forceinline__ uint64_t sortable(double v)
-{
-    if (v != v)
-        return ~0ull;
-    const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);
-    return (b >> 63) ? ~b : b | (1ull << 63);
-}
-__device__ __forceinline__ double unsortable(uint64_t u)
-{
-    return __builtin_bit_cast(double, (u >> 63) ? u & ~(1ull << 63) : ~u);
-}
-
-struct RouteParams {
-    const void *logits;
-    int64_t tokens, ld;
-    int experts;
-    const float *bias;
-    int groups, group_size, keep_groups, group_top;
-    int topk, renorm;
-    float scale;
-    const uint8_t *mask;
-    int32_t *ids;
-    float *weights;
+template <typename T> struct Words {
+    uint32_t w[sizeof(T) / 4];
 };
 
+template <int N, typename T> __device__ __forceinline__ T rotated(T v)
+{
+    Words<T> u = __builtin_bit_cast(Words<T>, v);
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(T) / 4; i++)
+        u.w[i] = ror16<N>(u.w[i]);
+    return __builtin_bit_cast(T, u);
+}
+template <int ROWS, typename T, typename F> __device__ __forceinline__ T joined(T v, F f)
+{
+    const Words<T> u = __builtin_bit_cast(Words<T>, v);
+    Words<T> a, b;
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(T) / 4; i++)
+        halves<ROWS>(u.w[i], a.w[i], b.w[i]);
+    return f(__builtin_bit_cast(T, a), __builtin_bit_cast(T, b));
+}
+
+// Reduction over a token's LANES lanes, the result in every lane.  The lanes
+// are paired in a fixed way and every lane adds the same pairs in one order or
+// the other, so a sum is the same in all of them and on every call.
+template <int LANES, typename T, typename F> __device__ __forceinline__ T reduce(T v, F f)
+{
+    v = f(v, rotated<8>(v));
+    v = f(v, rotated<4>(v));
+    v = f(v, rotated<2>(v));
+    v = f(v, rotated<1>(v));
+    if (LANES >= 32)
+        v = joined<16>(v, f);
+    if (LANES >= 64)
+        v = joined<32>(v, f);
+    return v;
+}
+template <int LANES, typename T> __device__ __forceinline__ T sum_of(T v)
+{
+    return reduce<LANES>(v, [](T a, T b) { return a + b; });
+}
 // Maxima that keep a NaN.
 __device__ __forceinline__ float max_nan(float a, float b) { return (a != a || b != b) ? NAN : fmaxf(a, b); }
-__device__ __forceinline__ float max16_nan(float v)
+template <int LANES> __device__ __forceinline__ float max_of(float v)
 {
-    return reduce16(v, [](float a, float b) { return max_nan(a, b); });
+    return reduce<LANES>(v, [](float a, float b) { return max_nan(a, b); });
+}
+
+// Selection keys.  Scores are at most FLT_MAX in magnitude (or a few units);
+// NaN becomes DBL_MAX's pattern and +inf half of it, above every score.  For
+// positive scores the larger low bits win, for negative ones the smaller.  What
+// cannot be chosen is below KEY_NONE.
+constexpr double KEY_NONE = -1e300;
+constexpr uint32_t KEY_GONE_HI = 0xFFEFFFFFu;  // upper word of a key that was taken: about -DBL_MAX
+
+// (keys and scores are never NaN; one instruction)
+__device__ __forceinline__ double max_key(double a, double b) { return __builtin_fmax(a, b); }
+
+__device__ __forceinline__ double make_key(double v, int e)
+{
+    uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);  // (both zeros become +0)
+    if (v != v)
+        b = 0x7FEFFFFFFFFFFFFFull;
+    if (v == (double)INFINITY)
+        b = 0x7FDFFFFFFFFFFFFFull;
+    if (v == -(double)INFINITY)
+        return __builtin_bit_cast(double, (uint64_t)KEY_GONE_HI << 32);
+    return __builtin_bit_cast(double, (b & ~1023ull) | (uint64_t)((b >> 63) ? e : 1023 - e));
+}
+__device__ __forceinline__ int key_expert(double k)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, k);
+    return (b >> 63) ? (int)(b & 1023) : 1023 - (int)(b & 1023);
+}
+// The score in a key, to its 42 bits of mantissa (NaN and +inf as the large
+// numbers above, -inf for what cannot be chosen).
+__device__ __forceinline__ double key_score(double k)
+{
+    return k > KEY_NONE ? __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, k) & ~1023ull) : -(double)INFINITY;
 }
 
 // Shift of a row's exponentials by its largest logit; -inf rows (nothing to
@@ -123,47 +186,60 @@ template <bool SOFTMAX> __device__ __forceinline__ float scaled_score(float x, f
     return (x > 0.0f ? 1.0f : expf(x - fminf(m, 0.0f))) / (1.0f + t);
 }
 
+struct RouteParams {
+    const void *logits;
+    int64_t tokens, ld;
+    int experts, vec;
+    const float *bias;
+    int groups, group_size, keep_groups, group_top;
+    int topk, renorm;
+    float scale;
+    const uint8_t *mask;
+    int32_t *ids;
+    float *weights;
+};
+
 // DT: logits' type (0 BF16, 1 FP32); SOFTMAX: score; GROUPS: groups > 1.
-template <int EPL, int DT, bool SOFTMAX, bool GROUPS>
+template <int LANES, int EPL, int DT, bool SOFTMAX, bool GROUPS>
 __global__ __launch_bounds__(64) void route_kernel(RouteParams p)
 {
-    extern __shared__ uint64_t s_keys[];  // GROUPS: [tokens][experts] keys, then [tokens][groups] group scores
-    const int lane = threadIdx.x, l = lane & (RT_LANES - 1), sub = lane / RT_LANES;
-    const int64_t t = (int64_t)blockIdx.x * RT_TOKENS + sub;
+    constexpr int TOKENS = 64 / LANES;        // a wave's
+    constexpr int NSEL = LANES >= 32 ? 1 : 2;  // chosen experts a lane keeps
+    extern __shared__ double s_keys[];  // GROUPS: [TOKENS][experts] keys, then [TOKENS][groups] group scores
+    const int lane = threadIdx.x, l = lane & (LANES - 1), sub = lane / LANES;
+    const int64_t t = (int64_t)blockIdx.x * TOKENS + sub;
     const bool live = t < p.tokens && (p.mask == nullptr || p.mask[t] != 0);
-    const int E = p.experts;
     const int64_t row = live ? t * p.ld : 0;
     // (masked tokens and those past the end read nothing: every logit -inf)
     float x[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; i++) {
-        const int e = l * EPL + i;
-        x[i] = live && e < E ? logit_at<DT>(p.logits, row + e) : -INFINITY;
-    }
-    // softmax statistics: the weights' without renormalization, and the
-    // selection scores' when a bias (or a sum of two) is compared
+    load_logits<EPL, DT>(p.logits, row, l * EPL, p.experts, live, p.vec != 0, x);
+    // softmax statistics: for the weights without renormalization, and for the
+    // selection scores when a bias (or a sum of two) is compared
     const bool scored = p.bias != nullptr || p.group_top > 1;
-    float mx = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < EPL; i++)
-        mx = max_nan(mx, x[i]);
-    mx = shift_of(max16_nan(mx));
-    uint64_t key[EPL];
-    float fsum = 0.0f;
-    if (SOFTMAX && !p.renorm) {
-#pragma unroll
-        for (int i = 0; i < EPL; i++)
-            fsum += expf(x[i] - mx);
-        fsum = sum16(fsum);
-    }
+    float mx = 0.0f, fsum = 1.0f;
     double inv = 1.0;
-    if (SOFTMAX && scored) {
-        double s = 0.0;
+    if (SOFTMAX && (scored || !p.renorm)) {
+        mx = x[0];
 #pragma unroll
-        for (int i = 0; i < EPL; i++)
-            s += exp((double)x[i] - (double)mx);
-        inv = 1.0 / sum16(s);
+        for (int i = 1; i < EPL; i++)
+            mx = max_nan(mx, x[i]);
+        mx = shift_of(max_of<LANES>(mx));
+        if (!p.renorm) {
+            fsum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < EPL; i++)
+                fsum += expf(x[i] - mx);
+            fsum = sum_of<LANES>(fsum);
+        }
+        if (scored) {
+            double s = 0.0;
+#pragma unroll
+            for (int i = 0; i < EPL; i++)
+                s += exp((double)x[i] - (double)mx);
+            inv = 1.0 / sum_of<LANES>(s);
+        }
     }
+    double key[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; i++) {
         const int e = l * EPL + i;
@@ -174,89 +250,106 @@ __global__ __launch_bounds__(64) void route_kernel(RouteParams p)
                 v += (double)p.bias[e];
             v = v != v ? (double)x[i] : v;  // a NaN or +inf in the row: its experts rank by their logits, NaN first
         }
-        key[i] = x[i] == -INFINITY ? 0 : sortable(v);  // 0: never chosen
+        key[i] = make_key(v, e);
     }
     if (GROUPS) {
         // group scores: lane g of the token scans group g's keys (starting at
         // its own offset, so that the lanes' banks differ), then counts the
         // groups that rank before its own
-        uint64_t *keys = s_keys + sub * E, *score = s_keys + RT_TOKENS * E + sub * p.groups;
+        double *keys = s_keys + sub * p.experts, *score = s_keys + TOKENS * p.experts + sub * p.groups;
 #pragma unroll
         for (int i = 0; i < EPL; i++)
-            if (l * EPL + i < E)
+            if (l * EPL + i < p.experts)
                 keys[l * EPL + i] = key[i];
         __syncthreads();
-        for (int g = l; g < p.groups; g += RT_LANES) {
-            uint64_t a = 0, b = 0;  // largest, second
+        for (int g = l; g < p.groups; g += LANES) {
+            double a = -(double)INFINITY, b = a;  // largest, second
             int at = g % p.group_size;
+#pragma unroll 4
             for (int i = 0; i < p.group_size; i++) {
-                const uint64_t v = keys[g * p.group_size + at];
+                const double v = key_score(keys[g * p.group_size + at]);
                 at = at + 1 == p.group_size ? 0 : at + 1;
-                b = v > a ? a : (v > b ? v : b);
-                a = v > a ? v : a;
+                b = max_key(b, __builtin_fmin(v, a));
+                a = max_key(a, v);
             }
-            // (0 stands for an expert that cannot be chosen: -inf)
-            const double va = a ? unsortable(a) : -(double)INFINITY, vb = b ? unsortable(b) : -(double)INFINITY;
-            score[g] = sortable(p.group_top > 1 ? va + vb : va);
+            score[g] = p.group_top > 1 ? a + b : a;
         }
         __syncthreads();
         uint64_t kept = 0;
-        for (int g = l; g < p.groups; g += RT_LANES) {
-            const uint64_t mine = score[g];
+        for (int g = l; g < p.groups; g += LANES) {
+            const double mine = score[g];
             int rank = 0;
+#pragma unroll 4
             for (int h = 0; h < p.groups; h++)
                 rank += score[h] > mine || (score[h] == mine && h < g) ? 1 : 0;
             if (rank < p.keep_groups)
                 kept |= 1ull << g;
         }
-        kept = reduce16(kept, [](uint64_t a, uint64_t b) { return a | b; });
+        kept = reduce<LANES>(kept, [](uint64_t a, uint64_t b) { return a | b; });
+        int g = l * EPL / p.group_size, left = (g + 1) * p.group_size - l * EPL;
 #pragma unroll
         for (int i = 0; i < EPL; i++) {
-            const int e = l * EPL + i;
-            if (e < E && !((kept >> (e / p.group_size)) & 1))
-                key[i] = 0;
+            if (g < p.groups && !((kept >> g) & 1))
+                key[i] = make_key(-(double)INFINITY, 0);
+            if (--left == 0) {
+                g++;
+                left = p.group_size;
+            }
         }
     }
+    // top-k: chosen j stays in lane j % LANES, register j / LANES
+    int id[NSEL];
 #pragma unroll
-    for (int i = 0; i < EPL; i++)
-        key[i] = key[i] ? (key[i] & ~1023ull) | (uint64_t)(1023 - (l * EPL + i)) : 0;
-    // top-k: chosen j stays in lane j % 16, register j / 16
-    int id0 = -1, id1 = -1;
+    for (int k = 0; k < NSEL; k++)
+        id[k] = -1;
     for (int j = 0; j < p.topk; j++) {
-        uint64_t best = key[0];
-#pragma unroll
-        for (int i = 1; i < EPL; i++)
-            best = key[i] > best ? key[i] : best;
-        best = max16(best);
-        const int e = best ? 1023 - (int)(best & 1023) : -1;
-        if (j == l)
-            id0 = e;
-        if (j == l + RT_LANES)
-            id1 = e;
+        double m[EPL];
 #pragma unroll
         for (int i = 0; i < EPL; i++)
-            key[i] = key[i] == best ? 0 : key[i];
+            m[i] = key[i];
+#pragma unroll
+        for (int d = EPL / 2; d >= 1; d /= 2)
+#pragma unroll
+            for (int i = 0; i < d; i++)
+                m[i] = max_key(m[i], m[i + d]);
+        const double best = reduce<LANES>(m[0], [](double a, double b) { return max_key(a, b); });
+        const int e = best > KEY_NONE ? key_expert(best) : -1;
+#pragma unroll
+        for (int k = 0; k < NSEL; k++)
+            id[k] = j == l + k * LANES ? e : id[k];
+        const int mine = e - l * EPL;
+#pragma unroll
+        for (int i = 0; i < EPL; i++) {
+            uint64_t b = __builtin_bit_cast(uint64_t, key[i]);
+            const uint32_t hi = mine == i ? KEY_GONE_HI : (uint32_t)(b >> 32);
+            key[i] = __builtin_bit_cast(double, ((uint64_t)hi << 32) | (uint32_t)b);
+        }
     }
     // weights, in FP32 (scaled_score): softmax relative to the row's maximum, or
     // to the chosen ones' when they are renormalized
-    const int id[2] = {id0, id1};
-    float own_max = -INFINITY, xs[2], sc[2];
+    float xs[NSEL], sc[NSEL];
+    if (p.renorm)
+        mx = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < 2; k++) {
+    for (int k = 0; k < NSEL; k++) {
         xs[k] = id[k] >= 0 ? logit_at<DT>(p.logits, row + id[k]) : -INFINITY;
-        own_max = max_nan(own_max, xs[k]);
+        if (p.renorm)
+            mx = max_nan(mx, xs[k]);
     }
     if (p.renorm)
-        mx = shift_of(max16_nan(own_max));
+        mx = shift_of(max_of<LANES>(mx));
+    float total = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 2; k++)
-        sc[k] = id[k] < 0 ? 0.0f : scaled_score<SOFTMAX>(xs[k], SOFTMAX || p.renorm ? mx : 0.0f);
-    const float total = p.renorm ? sum16(sc[0] + sc[1]) : SOFTMAX ? fsum : 1.0f;
+    for (int k = 0; k < NSEL; k++) {
+        sc[k] = id[k] < 0 ? 0.0f : scaled_score<SOFTMAX>(xs[k], mx);
+        total += sc[k];
+    }
+    total = p.renorm ? sum_of<LANES>(total) : fsum;
     if (t >= p.tokens)
         return;
 #pragma unroll
-    for (int k = 0; k < 2; k++) {
-        const int j = l + k * RT_LANES;
+    for (int k = 0; k < NSEL; k++) {
+        const int j = l + k * LANES;
         if (j < p.topk) {
             p.ids[t * p.topk + j] = id[k];
             p.weights[t * p.topk + j] = id[k] < 0 ? 0.0f : p.scale * (sc[k] / total);
@@ -267,7 +360,7 @@ __global__ __launch_bounds__(64) void route_kernel(RouteParams p)
 struct RouteBwdParams {
     const void *logits;
     int64_t tokens, ld;
-    int experts, topk, renorm;
+    int experts, vec, topk, renorm;
     float scale;
     const int32_t *ids;
     const float *dw;
@@ -275,92 +368,94 @@ struct RouteBwdParams {
     int64_t ld_d;
 };
 
-// Gradient of the weights.  The same sixteen lanes a token; chosen j in lane
-// j % 16.  With r_j = s_j / S (a softmax over the chosen for softmax scores)
+// Gradient of the weights.  The same lanes a token; chosen j in lane j %
+// LANES.  With r_j = s_j / S (a softmax over the chosen for softmax scores)
 // and D = sum g_k r_k the renormalized gradients are
 //   softmax  dx_j = scale (g_j - D) r_j          (the sum over the chosen of
 //            ds_k s_k is zero, so nothing flows to the others)
 //   sigmoid  dx_j = scale (g_j - D) r_j (1 - s_j)
 // which need no division by a small S.  Each lane then gathers the chosen
 // ones' values for its own experts, in order j = 0, 1, ..
-template <int EPL, int DT, bool SOFTMAX>
+template <int LANES, int EPL, int DT, bool SOFTMAX>
 __global__ __launch_bounds__(64) void route_bwd_kernel(RouteBwdParams p)
 {
-    const int lane = threadIdx.x, l = lane & (RT_LANES - 1), sub = lane / RT_LANES;
-    const int64_t t = (int64_t)blockIdx.x * RT_TOKENS + sub;
+    constexpr int NSEL = LANES >= 32 ? 1 : 2;
+    const int lane = threadIdx.x, l = lane & (LANES - 1), sub = lane / LANES;
+    const int64_t t = (int64_t)blockIdx.x * (64 / LANES) + sub;
     const bool live = t < p.tokens;
-    const int E = p.experts;
     const int64_t row = live ? t * p.ld : 0;
-    int id[2];
-    float g[2], xs[2];
+    const bool full = SOFTMAX && !p.renorm;  // every expert's score takes part
+    int id[NSEL];
+    float g[NSEL], xs[NSEL];
     float mx = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < 2; k++) {
-        const int j = l + k * RT_LANES;
+    for (int k = 0; k < NSEL; k++) {
+        const int j = l + k * LANES;
         const bool has = live && j < p.topk;
         id[k] = has ? p.ids[t * p.topk + j] : -1;
-        if (id[k] < 0 || id[k] >= E)
+        g[k] = has ? p.dw[t * p.topk + j] : 0.0f;
+        if (id[k] < 0 || id[k] >= p.experts)
             id[k] = -1;
         xs[k] = id[k] >= 0 ? logit_at<DT>(p.logits, row + id[k]) : -INFINITY;
         if (xs[k] == -INFINITY)
             id[k] = -1;  // no score, no gradient
-        g[k] = id[k] >= 0 ? p.dw[t * p.topk + j] : 0.0f;
+        g[k] = id[k] >= 0 ? g[k] : 0.0f;
         mx = max_nan(mx, xs[k]);
     }
-    float pr[EPL];  // softmax without renormalization: every expert's score
+    float pr[EPL];
     float total = 1.0f;
-    const bool full = SOFTMAX && !p.renorm;
     if (full) {
-        mx = -INFINITY;
+        load_logits<EPL, DT>(p.logits, row, l * EPL, p.experts, live, p.vec != 0, pr);
 #pragma unroll
-        for (int i = 0; i < EPL; i++) {
-            const int e = l * EPL + i;
-            pr[i] = live && e < E ? logit_at<DT>(p.logits, row + e) : -INFINITY;
+        for (int i = 0; i < EPL; i++)
             mx = max_nan(mx, pr[i]);
-        }
     }
-    mx = shift_of(max16_nan(mx));
+    mx = shift_of(max_of<LANES>(mx));
     if (full) {
-        float s = 0.0f;
+        total = 0.0f;
 #pragma unroll
         for (int i = 0; i < EPL; i++) {
             pr[i] = expf(pr[i] - mx);
-            s += pr[i];
+            total += pr[i];
         }
-        total = sum16(s);
+        total = sum_of<LANES>(total);
         total = total == 0.0f ? 1.0f : total;  // a row of -inf: every score is zero
     }
     // r: the chosen scores (over their sum when renormalized); v: what flows
     // to the logits (softmax without renormalization: to the scores)
-    float r[2], v[2];
-    float dot = 0.0f;  // softmax without renormalization: sum ds_k s_k
+    float r[NSEL], v[NSEL];
+    float S = 0.0f, D = 0.0f, dot = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 2; k++)
+    for (int k = 0; k < NSEL; k++) {
         r[k] = id[k] < 0 ? 0.0f : scaled_score<SOFTMAX>(xs[k], SOFTMAX || p.renorm ? mx : 0.0f) / total;
-    float D = 0.0f;
+        S += r[k];
+    }
     if (p.renorm) {
-        const float S = sum16(r[0] + r[1]);
+        S = sum_of<LANES>(S);
 #pragma unroll
-        for (int k = 0; k < 2; k++)
+        for (int k = 0; k < NSEL; k++) {
             r[k] = S == 0.0f ? 0.0f : r[k] / S;  // (S is zero only where nothing was chosen)
-        D = sum16(g[0] * r[0] + g[1] * r[1]);
+            D += g[k] * r[k];
+        }
+        D = sum_of<LANES>(D);
     }
 #pragma unroll
-    for (int k = 0; k < 2; k++) {
-        const float t = expf(-fabsf(xs[k]));
-        const float not_s = SOFTMAX ? 1.0f : (xs[k] > 0.0f ? t : 1.0f) / (1.0f + t);
+    for (int k = 0; k < NSEL; k++) {
+        const float e = expf(-fabsf(xs[k]));
+        const float not_s = SOFTMAX ? 1.0f : (xs[k] > 0.0f ? e : 1.0f) / (1.0f + e);
         v[k] = id[k] < 0 ? 0.0f : full ? p.scale * g[k] : p.scale * (g[k] - D) * r[k] * not_s;
+        dot += v[k] * r[k];
     }
     if (full)
-        dot = sum16(v[0] * r[0] + v[1] * r[1]);
+        dot = sum_of<LANES>(dot);  // sum ds_k s_k
     float acc[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; i++)
         acc[i] = 0.0f;
     for (int j = 0; j < p.topk; j++) {
-        const int from = (lane & ~(RT_LANES - 1)) + (j & (RT_LANES - 1));
-        const int e = __shfl(j < RT_LANES ? id[0] : id[1], from, 64) - l * EPL;
-        const float w = __shfl(j < RT_LANES ? v[0] : v[1], from, 64);
+        const int from = (lane & ~(LANES - 1)) + (j & (LANES - 1));
+        const int e = __shfl(j < LANES ? id[0] : id[NSEL - 1], from, 64) - l * EPL;
+        const float w = __shfl(j < LANES ? v[0] : v[NSEL - 1], from, 64);
 #pragma unroll
         for (int i = 0; i < EPL; i++)
             acc[i] += e == i ? w : 0.0f;
@@ -368,41 +463,68 @@ __global__ __launch_bounds__(64) void route_bwd_kernel(RouteBwdParams p)
     if (!live)
         return;
 #pragma unroll
-    for (int i = 0; i < EPL; i++) {
-        const int e = l * EPL + i;
-        if (e < E) {
-            const float d = full ? pr[i] / total * (acc[i] - dot) : acc[i];
-            if (DT == 0)
-                reinterpret_cast<uint16_t *>(p.dx)[t * p.ld_d + e] = f32_bf16(d);
-            else
-                reinterpret_cast<float *>(p.dx)[t * p.ld_d + e] = d;
+    for (int i = 0; i < EPL; i++)
+        acc[i] = full ? pr[i] / total * (acc[i] - dot) : acc[i];
+    const int64_t out = t * p.ld_d + l * EPL;
+    if (p.vec) {
+        if (l * EPL >= p.experts)
+            return;
+#pragma unroll
+        for (int i = 0; i < EPL; i += 4) {
+            if (DT == 0) {
+                typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+                const f4_t a = {acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
+                *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(p.dx) + out + i) =
+                    __builtin_bit_cast(uint2, __builtin_convertvector(a, bf16x4_t));
+            } else {
+                *reinterpret_cast<f4_t *>(reinterpret_cast<float *>(p.dx) + out + i) =
+                    f4_t{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
+            }
         }
-    }
-}
-
-template <int EPL, int DT>
-static void launch_route_t(const RouteParams &p, bool softmax, unsigned grid, hipStream_t stream)
-{
-    const size_t lds = p.groups > 1 ? (size_t)RT_TOKENS * (p.experts + p.groups) * 8 : 0;
-    if (p.groups > 1) {
-        if (softmax)
-            hipLaunchKernelGGL((route_kernel<EPL, DT, true, true>), dim3(grid), dim3(64), lds, stream, p);
-        else
-            hipLaunchKernelGGL((route_kernel<EPL, DT, false, true>), dim3(grid), dim3(64), lds, stream, p);
-    } else if (softmax) {
-        hipLaunchKernelGGL((route_kernel<EPL, DT, true, false>), dim3(grid), dim3(64), lds, stream, p);
     } else {
-        hipLaunchKernelGGL((route_kernel<EPL, DT, false, false>), dim3(grid), dim3(64), lds, stream, p);
+#pragma unroll
+        for (int i = 0; i < EPL; i++)
+            if (l * EPL + i < p.experts) {
+                if (DT == 0)
+                    reinterpret_cast<uint16_t *>(p.dx)[out + i] = __builtin_bit_cast(uint16_t, (__bf16)acc[i]);
+                else
+                    reinterpret_cast<float *>(p.dx)[out + i] = acc[i];
+            }
     }
 }
 
-template <int EPL, int DT>
-static void launch_route_bwd_t(const RouteBwdParams &p, bool softmax, unsigned grid, hipStream_t stream)
+// Rows that a lane's run of EPL logits can be read from (written to) as
+// vectors of four: 8-byte aligned for BF16, 16-byte for FP32.
+static bool vec_rows(const void *p, int64_t ld, int dtype, int64_t experts, int epl)
 {
-    if (softmax)
-        hipLaunchKernelGGL((route_bwd_kernel<EPL, DT, true>), dim3(grid), dim3(64), 0, stream, p);
+    return experts % epl == 0 && ld % 4 == 0 && (uintptr_t)p % (dtype == 0 ? 8 : 16) == 0;
+}
+
+// The lanes a token and the experts a lane holds, by the number of experts.
+template <typename F> static void by_experts(int64_t experts, F f)
+{
+    if (experts <= 64)
+        f(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
+    else if (experts <= 128)
+        f(std::integral_constant<int, 16>{}, std::integral_constant<int, 8>{});
+    else if (experts <= 256)
+        f(std::integral_constant<int, 32>{}, std::integral_constant<int, 8>{});
+    else if (experts <= 512)
+        f(std::integral_constant<int, 64>{}, std::integral_constant<int, 8>{});
     else
-        hipLaunchKernelGGL((route_bwd_kernel<EPL, DT, false>), dim3(grid), dim3(64), 0, stream, p);
+        f(std::integral_constant<int, 64>{}, std::integral_constant<int, 16>{});
+}
+
+template <int LANES, int EPL, int DT, bool SOFTMAX>
+static void launch_route_t(const RouteParams &p, hipStream_t stream)
+{
+    constexpr int TOKENS = 64 / LANES;
+    const dim3 grid((unsigned)((p.tokens + TOKENS - 1) / TOKENS)), block(64);
+    if (p.groups > 1)
+        hipLaunchKernelGGL((route_kernel<LANES, EPL, DT, SOFTMAX, true>), grid, block,
+                           (size_t)TOKENS * (p.experts + p.groups) * 8, stream, p);
+    else
+        hipLaunchKernelGGL((route_kernel<LANES, EPL, DT, SOFTMAX, false>), grid, block, 0, stream, p);
 }
 
 hipError_t launch_moe_route(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t ld,
@@ -410,24 +532,16 @@ hipError_t launch_moe_route(const void *logits, int dtype, int64_t tokens, int64
                             int64_t topk, bool renorm, float scale, const uint8_t *mask, int32_t *ids, float *weights,
                             hipStream_t stream)
 {
-    static_assert(MOE_MAX_EXPERTS == RT_LANES * 64, "keys hold 10 bits of expert number");
-    const RouteParams p{logits, tokens, ld, (int)experts, bias, (int)groups, (int)(experts / groups),
-                        (int)keep_groups, (int)group_top, (int)topk, renorm ? 1 : 0, scale, mask, ids, weights};
-    const unsigned grid = (unsigned)((tokens + RT_TOKENS - 1) / RT_TOKENS);
-#define MX_ROUTE(EPL)                                                  \
-    (dtype == 0 ? launch_route_t<EPL, 0>(p, softmax, grid, stream)     \
-                : launch_route_t<EPL, 1>(p, softmax, grid, stream))
-    if (experts <= 4 * RT_LANES)
-        MX_ROUTE(4);
-    else if (experts <= 8 * RT_LANES)
-        MX_ROUTE(8);
-    else if (experts <= 16 * RT_LANES)
-        MX_ROUTE(16);
-    else if (experts <= 32 * RT_LANES)
-        MX_ROUTE(32);
-    else
-        MX_ROUTE(64);
-#undef MX_ROUTE
+    by_experts(experts, [&](auto lanes, auto epl) {
+        constexpr int L = decltype(lanes)::value, E = decltype(epl)::value;
+        const RouteParams p{logits, tokens, ld, (int)experts, vec_rows(logits, ld, dtype, experts, E) ? 1 : 0, bias,
+                            (int)groups, (int)(experts / groups), (int)keep_groups, (int)group_top, (int)topk,
+                            renorm ? 1 : 0, scale, mask, ids, weights};
+        if (dtype == 0)
+            softmax ? launch_route_t<L, E, 0, true>(p, stream) : launch_route_t<L, E, 0, false>(p, stream);
+        else
+            softmax ? launch_route_t<L, E, 1, true>(p, stream) : launch_route_t<L, E, 1, false>(p, stream);
+    });
     return hipGetLastError();
 }
 
@@ -435,22 +549,21 @@ hipError_t launch_moe_route_bwd(const void *logits, int dtype, int64_t tokens, i
                                 bool softmax, int64_t topk, bool renorm, float scale, const int32_t *ids,
                                 const float *dw, void *dx, int64_t ld_d, hipStream_t stream)
 {
-    const RouteBwdParams p{logits, tokens, ld, (int)experts, (int)topk, renorm ? 1 : 0, scale, ids, dw, dx, ld_d};
-    const unsigned grid = (unsigned)((tokens + RT_TOKENS - 1) / RT_TOKENS);
-#define MX_ROUTE(EPL)                                                      \
-    (dtype == 0 ? launch_route_bwd_t<EPL, 0>(p, softmax, grid, stream)     \
-                : launch_route_bwd_t<EPL, 1>(p, softmax, grid, stream))
-    if (experts <= 4 * RT_LANES)
-        MX_ROUTE(4);
-    else if (experts <= 8 * RT_LANES)
-        MX_ROUTE(8);
-    else if (experts <= 16 * RT_LANES)
-        MX_ROUTE(16);
-    else if (experts <= 32 * RT_LANES)
-        MX_ROUTE(32);
-    else
-        MX_ROUTE(64);
-#undef MX_ROUTE
+    by_experts(experts, [&](auto lanes, auto epl) {
+        constexpr int L = decltype(lanes)::value, E = decltype(epl)::value;
+        const bool vec = vec_rows(logits, ld, dtype, experts, E) && vec_rows(dx, ld_d, dtype, experts, E);
+        const RouteBwdParams p{logits, tokens, ld, (int)experts, vec ? 1 : 0, (int)topk, renorm ? 1 : 0, scale, ids,
+                               dw, dx, ld_d};
+        const dim3 grid((unsigned)((tokens * L + 63) / 64)), block(64);
+        if (dtype == 0 && softmax)
+            hipLaunchKernelGGL((route_bwd_kernel<L, E, 0, true>), grid, block, 0, stream, p);
+        else if (dtype == 0)
+            hipLaunchKernelGGL((route_bwd_kernel<L, E, 0, false>), grid, block, 0, stream, p);
+        else if (softmax)
+            hipLaunchKernelGGL((route_bwd_kernel<L, E, 1, true>), grid, block, 0, stream, p);
+        else
+            hipLaunchKernelGGL((route_bwd_kernel<L, E, 1, false>), grid, block, 0, stream, p);
+    });
     return hipGetLastError();
 }
 
@@ -516,9 +629,7 @@ __global__ __launch_bounds__(64 * WAVES) void combine_bwd_kernel(
                 continue;
 #pragma unroll
             for (int j = 0; j < CB_SLOTS; j++) {
-                float v = sum16(dot[j]);
-                v += __shfl_xor(v, 16, 64);
-                v += __shfl_xor(v, 32, 64);
+                const float v = sum_of<64>(dot[j]);
                 if (lane == 0)
                     part[wave][j] = v;
             }

@@ -49,9 +49,14 @@ def _fn(name: str):
     return f
 
 
-def _call(name: str, *args) -> None:
-    """The entry point on the current device's current stream."""
-    _check(name, _fn(name)(*args, torch.cuda.current_stream().cuda_stream))
+def _call(name: str, dev: torch.device, *args) -> None:
+    """The entry point on dev's current stream (dev is the current device).
+
+    The raw stream handle is asked for directly: a torch.cuda.Stream object
+    for it costs 2.8 us, more than the whole launch."""
+    st = _fn(name)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        _check(name, st)
 
 
 def _entry(fn):
@@ -89,7 +94,7 @@ def _at(t: Optional[torch.Tensor], name: str, dev, *dtypes, shape=None, least: i
         raise ValueError(f"{name} must be on {dev}, is on {t.device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if shape is not None and (tuple(t.shape) != shape or not t.is_contiguous()):
+    if shape is not None and (t.shape != shape or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
     if least and (t.numel() < least or not t.is_contiguous()):
         raise ValueError(f"{name} must be contiguous and hold {least} elements, holds {t.numel()}")
@@ -98,7 +103,7 @@ def _at(t: Optional[torch.Tensor], name: str, dev, *dtypes, shape=None, least: i
 
 def _rows(t: torch.Tensor, name: str, dev, rows: int, cols: int, *dtypes) -> Tuple[int, int]:
     """(pointer, leading dimension) of a [rows][cols] row-major view on dev."""
-    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}][{cols}], got {list(t.shape)}")
     if rows > 1 and cols > 1:
         ld = _ld(t, name)
@@ -142,7 +147,7 @@ def mx_moe_route(logits: torch.Tensor, topk: int, *, bias: Optional[torch.Tensor
     if weights is None:
         weights = torch.empty((tokens, topk), dtype=torch.float32, device=dev)
     x, ld = _rows(logits, "logits", dev, tokens, experts, *_LOGITS)
-    _call("mx_moe_route", x, _LOGITS[logits.dtype], tokens, experts, ld,
+    _call("mx_moe_route", dev, x, _LOGITS[logits.dtype], tokens, experts, ld,
           _at(bias, "bias", dev, torch.float32, shape=(experts,)), _score(score), num_groups, topk_groups, group_top,
           topk, int(renormalize), scale, _at(mask, "mask", dev, _U8, torch.bool, shape=(tokens,)),
           _at(topk_ids, "topk_ids", dev, torch.int32, shape=(tokens, topk)),
@@ -163,7 +168,7 @@ def mx_moe_route_bwd(d_weights: torch.Tensor, logits: torch.Tensor, topk_ids: to
         d_logits = torch.empty((tokens, experts), dtype=logits.dtype, device=dev)
     x, ld = _rows(logits, "logits", dev, tokens, experts, *_LOGITS)
     d, ld_d = _rows(d_logits, "d_logits", dev, tokens, experts, logits.dtype)
-    _call("mx_moe_route_bwd", x, _LOGITS[logits.dtype], tokens, experts, ld, _score(score), topk, int(renormalize),
+    _call("mx_moe_route_bwd", dev, x, _LOGITS[logits.dtype], tokens, experts, ld, _score(score), topk, int(renormalize),
           scale, _at(topk_ids, "topk_ids", dev, torch.int32, shape=(tokens, topk)),
           _at(d_weights, "d_weights", dev, torch.float32, shape=(tokens, topk)), d, ld_d)
     return d_logits
@@ -194,7 +199,7 @@ def mx_moe_combine_bwd(d_out: torch.Tensor, y: Optional[torch.Tensor], slot: tor
     pd, ld_dy = _rows(dy, "dy", dev, n, hidden, bf) if want_dy else (None, 0)
     if tuple(slot.shape) not in ((n,), (tokens, topk)):
         raise ValueError(f"slot must hold {n} entries, got {list(slot.shape)}")
-    _call("mx_moe_combine_bwd", o, tokens, hidden, ld_o, py, ld_y,
+    _call("mx_moe_combine_bwd", dev, o, tokens, hidden, ld_o, py, ld_y,
           _at(slot, "slot", dev, torch.int32, shape=tuple(slot.shape)),
           _at(weights, "weights", dev, torch.float32, shape=(tokens, topk)), topk, pd, ld_dy,
           _at(d_weights, "d_weights", dev, torch.float32, shape=(tokens, topk)) if want_d_weights else None)
@@ -225,7 +230,7 @@ def mx_quantize_rowwise_fp4(x: torch.Tensor, q: Optional[torch.Tensor] = None, s
     s_swz, ps = _swizzled(s_swz, rows, s_tiles, cols, "s_swz", dev)
     px, ld_x = _rows(x, "x", dev, rows, cols, torch.bfloat16)
     pq, ld_q = _rows(q, "q", dev, rows, cols // 2, _U8)
-    _call("mx_quantize_rowwise_fp4", px, rows, cols, ld_x, pq, ld_q, ps, s_tiles)
+    _call("mx_quantize_rowwise_fp4", dev, px, rows, cols, ld_x, pq, ld_q, ps, s_tiles)
     return q, s_swz
 
 
@@ -254,7 +259,7 @@ def mx_quantize_colwise_fp4(x: torch.Tensor, qt: Optional[torch.Tensor] = None, 
     st_swz = _u8(st_swz)
     px, ld_x = _rows(flat, "x", dev, count * rows, cols, torch.bfloat16)
     pq, ld_qt = _rows(qt.view(count * cols, rows // 2) if x.dim() == 3 else qt, "qt", dev, count * cols, rows // 2, _U8)
-    _call("mx_quantize_colwise_fp4", px, count, rows, cols, ld_x, pq, ld_qt,
+    _call("mx_quantize_colwise_fp4", dev, px, count, rows, cols, ld_x, pq, ld_qt,
           _at(st_swz, "st_swz", dev, _U8, least=need))
     return qt, st_swz
 
@@ -275,7 +280,7 @@ def mx_dequantize_fp4(q: torch.Tensor, s_swz: torch.Tensor, y: Optional[torch.Te
     pq, ld_q = _rows(q, "q", dev, rows, half, _U8)
     py, ld_y = _rows(y, "y", dev, rows, cols, *_OUT)
     _, ps = _swizzled(s_swz, rows, s_tiles, cols, "s_swz", dev)
-    _call("mx_dequantize_fp4", pq, rows, cols, ld_q, ps, s_tiles, py, ld_y, _OUT[y.dtype])
+    _call("mx_dequantize_fp4", dev, pq, rows, cols, ld_q, ps, s_tiles, py, ld_y, _OUT[y.dtype])
     return y
 
 
@@ -307,7 +312,7 @@ def mx_moe_dispatch_fp4(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: in
         workspace = torch.empty(max(need, 1), dtype=_U8, device=dev)
     px, ld_x = _rows(x, "x", dev, tokens, hidden, torch.bfloat16)
     pq, ld_q = _rows(q, "q", dev, n, hidden // 2, _U8)
-    _call("mx_moe_dispatch_fp4", px, tokens, hidden, ld_x, _at(topk_ids, "topk_ids", dev, i32, shape=(tokens, topk)),
+    _call("mx_moe_dispatch_fp4", dev, px, tokens, hidden, ld_x, _at(topk_ids, "topk_ids", dev, i32, shape=(tokens, topk)),
           topk, num_experts, _at(offsets, "offsets", dev, torch.int64, shape=(num_experts + 1,)),
           _at(src, "src", dev, i32, shape=(n,)), _at(slot, "slot", dev, i32, shape=(n,)), pq, ld_q, ps,
           *_scratch(workspace, dev))
@@ -338,7 +343,7 @@ def mx_swiglu_quantize_fp4(gu: torch.Tensor, q: Optional[torch.Tensor] = None, s
     pg, ld_gu = _rows(gu, "gu", dev, rows, F2, torch.bfloat16)
     ph, ld_h = _rows(h, "h", dev, rows, F, torch.bfloat16) if h is not None else (None, 0)
     pq, ld_q = _rows(q, "q", dev, rows, F // 2, _U8)
-    _call("mx_swiglu_quantize_fp4", pg, rows, F, ld_gu, ph, ld_h, pq, ld_q, ps)
+    _call("mx_swiglu_quantize_fp4", dev, pg, rows, F, ld_gu, ph, ld_h, pq, ld_q, ps)
     return q, s_swz, h
 
 
@@ -371,7 +376,7 @@ def mx_gemm_fp4(a_q: torch.Tensor, a_s_swz: torch.Tensor, b_q: torch.Tensor, b_s
     if workspace is None:
         need = mx_gemm_fp4_workspace_bytes(M, N, K, c.dtype)
         workspace = torch.empty(need, dtype=_U8, device=dev) if need else None
-    _call("mx_gemm_fp4", M, N, K, pa, ld_a, _swizzled(a_s_swz, M, K // 256, K, "a_s_swz", dev)[1], pb, ld_b,
+    _call("mx_gemm_fp4", dev, M, N, K, pa, ld_a, _swizzled(a_s_swz, M, K // 256, K, "a_s_swz", dev)[1], pb, ld_b,
           _swizzled(b_s_swz, N, K // 256, K, "b_s_swz", dev)[1], pc, ld_c, _OUT[c.dtype], *_scratch(workspace, dev))
     return c
 
@@ -390,7 +395,7 @@ def mx_grouped_gemm_fp4(group_offsets: torch.Tensor, a_q: torch.Tensor, a_s_swz:
         c = torch.empty((M, N), dtype=out_dtype, device=dev)
     pa, ld_a = _rows(a_q, "a_q", dev, M, half, _U8)
     pc, ld_c = _rows(c, "c", dev, M, N, *_OUT)
-    _call("mx_grouped_gemm_fp4", G, M, N, K, _at(group_offsets, "group_offsets", dev, torch.int64, shape=(G + 1,)),
+    _call("mx_grouped_gemm_fp4", dev, G, M, N, K, _at(group_offsets, "group_offsets", dev, torch.int64, shape=(G + 1,)),
           pa, ld_a, _swizzled(a_s_swz, M, K // 256, K, "a_s_swz", dev)[1], _at(b_q, "b_q", dev, _U8, shape=(G, N, half)),
           _at(b_s_swz, "b_s_swz", dev, _U8, least=G * mx_scale_swizzled_bytes(N, K // 32)), pc, ld_c, _OUT[c.dtype])
     return c

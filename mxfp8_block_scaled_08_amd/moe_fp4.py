@@ -71,7 +71,7 @@ def _entry(fn):
         if not first.is_cuda:
             raise ValueError(f"{name} must be a device tensor")
         dev = first.device
-        if stream is None and dev.index == torch.cuda.current_device():
+        if stream is None and dev.index == torch._C._cuda_getDevice():
             return fn(*args, **kw)
         if stream is None:
             stream = torch.cuda.current_stream(dev)
@@ -84,37 +84,39 @@ def _entry(fn):
     return call
 
 
-def _at(t: Optional[torch.Tensor], name: str, dev, *dtypes, shape=None, least: int = 0) -> Optional[int]:
-    """Pointer of t (None stays None), which must lie on dev and have one of
-    the dtypes and, where given, the shape (contiguous) or at least so many
-    elements, contiguous."""
+def _at(t: Optional[torch.Tensor], name: str, dev, dtype, shape) -> Optional[int]:
+    """Pointer of t (None stays None), a contiguous tensor of dtype and shape on dev."""
     if t is None:
         return None
+    if t.dtype is dtype and t.device == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}, is on {t.device}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if shape is not None and (t.shape != shape or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
-    if least and (t.numel() < least or not t.is_contiguous()):
-        raise ValueError(f"{name} must be contiguous and hold {least} elements, holds {t.numel()}")
-    return t.data_ptr()
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
 
 
-def _rows(t: torch.Tensor, name: str, dev, rows: int, cols: int, *dtypes) -> Tuple[int, int]:
-    """(pointer, leading dimension) of a [rows][cols] row-major view on dev."""
+def _rows(t: torch.Tensor, name: str, dev, rows: int, cols: int, dtype) -> Tuple[int, int]:
+    """(pointer, leading dimension) of a [rows][cols] row-major view of dtype on dev."""
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, is on {t.device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}][{cols}], got {list(t.shape)}")
-    if rows > 1 and cols > 1:
-        ld = _ld(t, name)
-    elif rows > 1 and cols == 1:
-        ld = t.stride(0)
-    else:  # one row, or nothing: the stride says nothing (torch gives any value); a whole number of 16 bytes
-        if cols > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name} must be a 2-D row-major view")
-        per = max(1, 16 // t.element_size())
-        ld = (cols + per - 1) // per * per
-    return _at(t, name, dev, *dtypes), ld
+    if t.is_contiguous():
+        return t.data_ptr(), cols
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be a 2-D row-major view")
+    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+
+
+def _one_of(t: torch.Tensor, name: str, dtypes):
+    """t's dtype, which must be among dtypes."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    return t.dtype
 
 
 _U8 = torch.uint8
@@ -146,12 +148,12 @@ def mx_moe_route(logits: torch.Tensor, topk: int, *, bias: Optional[torch.Tensor
         topk_ids = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
     if weights is None:
         weights = torch.empty((tokens, topk), dtype=torch.float32, device=dev)
-    x, ld = _rows(logits, "logits", dev, tokens, experts, *_LOGITS)
+    x, ld = _rows(logits, "logits", dev, tokens, experts, _one_of(logits, "logits", _LOGITS))
     _call("mx_moe_route", dev, x, _LOGITS[logits.dtype], tokens, experts, ld,
-          _at(bias, "bias", dev, torch.float32, shape=(experts,)), _score(score), num_groups, topk_groups, group_top,
-          topk, int(renormalize), scale, _at(mask, "mask", dev, _U8, torch.bool, shape=(tokens,)),
-          _at(topk_ids, "topk_ids", dev, torch.int32, shape=(tokens, topk)),
-          _at(weights, "weights", dev, torch.float32, shape=(tokens, topk)))
+          _at(bias, "bias", dev, torch.float32, (experts,)), _score(score), num_groups, topk_groups, group_top,
+          topk, int(renormalize), scale, _at(mask, "mask", dev, torch.bool if mask is not None and mask.dtype is torch.bool else _U8, (tokens,)),
+          _at(topk_ids, "topk_ids", dev, torch.int32, (tokens, topk)),
+          _at(weights, "weights", dev, torch.float32, (tokens, topk)))
     return topk_ids, weights
 
 
@@ -166,11 +168,11 @@ def mx_moe_route_bwd(d_weights: torch.Tensor, logits: torch.Tensor, topk_ids: to
     dev = d_weights.device
     if d_logits is None:
         d_logits = torch.empty((tokens, experts), dtype=logits.dtype, device=dev)
-    x, ld = _rows(logits, "logits", dev, tokens, experts, *_LOGITS)
+    x, ld = _rows(logits, "logits", dev, tokens, experts, _one_of(logits, "logits", _LOGITS))
     d, ld_d = _rows(d_logits, "d_logits", dev, tokens, experts, logits.dtype)
     _call("mx_moe_route_bwd", dev, x, _LOGITS[logits.dtype], tokens, experts, ld, _score(score), topk, int(renormalize),
-          scale, _at(topk_ids, "topk_ids", dev, torch.int32, shape=(tokens, topk)),
-          _at(d_weights, "d_weights", dev, torch.float32, shape=(tokens, topk)), d, ld_d)
+          scale, _at(topk_ids, "topk_ids", dev, torch.int32, (tokens, topk)),
+          _at(d_weights, "d_weights", dev, torch.float32, (tokens, topk)), d, ld_d)
     return d_logits
 
 
@@ -200,20 +202,32 @@ def mx_moe_combine_bwd(d_out: torch.Tensor, y: Optional[torch.Tensor], slot: tor
     if tuple(slot.shape) not in ((n,), (tokens, topk)):
         raise ValueError(f"slot must hold {n} entries, got {list(slot.shape)}")
     _call("mx_moe_combine_bwd", dev, o, tokens, hidden, ld_o, py, ld_y,
-          _at(slot, "slot", dev, torch.int32, shape=tuple(slot.shape)),
-          _at(weights, "weights", dev, torch.float32, shape=(tokens, topk)), topk, pd, ld_dy,
-          _at(d_weights, "d_weights", dev, torch.float32, shape=(tokens, topk)) if want_d_weights else None)
+          _at(slot, "slot", dev, torch.int32, tuple(slot.shape)),
+          _at(weights, "weights", dev, torch.float32, (tokens, topk)), topk, pd, ld_dy,
+          _at(d_weights, "d_weights", dev, torch.float32, (tokens, topk)) if want_d_weights else None)
     return dy if want_dy else None, d_weights if want_d_weights else None
 
 
-def _swizzled(s: Optional[torch.Tensor], rows: int, tiles: int, cols: int, name: str, dev):
-    """(tensor, pointer) of rearranged scales with `tiles` tiles a tile row (a
-    new buffer if None)."""
-    need = max(0, ((rows + 31) // 32 - 1) * tiles + cols // 256) * 256 if rows and cols else 0
+def _scale_ptr(s: torch.Tensor, name: str, dev, need: int) -> int:
+    """Pointer of a rearranged scale buffer on dev of at least need bytes."""
+    if s.dtype is not _U8:
+        s = _u8(s)
+    if s.dtype is _U8 and s.device == dev and s.numel() >= need and s.is_contiguous():
+        return s.data_ptr()
+    raise ValueError(f"{name} must be a contiguous uint8 tensor of at least {need} bytes on {dev}, got {s.numel()} of "
+                     f"{s.dtype} on {s.device}")
+
+
+def _scale_bytes(rows: int, cols: int, tiles: int) -> int:
+    """Bytes from the first to the last tile of [rows][cols/32] scales, `tiles` tiles a tile row."""
+    return ((rows + 31) // 32 * tiles - tiles + cols // 256) * 256 if rows and cols else 0
+
+
+def _scales(s: Optional[torch.Tensor], rows: int, cols: int, tiles: int, name: str, dev):
+    """(tensor, pointer) of rearranged scales to write (a new buffer if None)."""
     if s is None:
-        s = torch.empty(max(need, (rows + 31) // 32 * tiles * 256, 1), dtype=_U8, device=dev)
-    s = _u8(s)
-    return s, _at(s, name, dev, _U8, least=need)
+        s = torch.empty(max((rows + 31) // 32 * tiles * 256, 1), dtype=_U8, device=dev)
+    return s, _scale_ptr(s, name, dev, _scale_bytes(rows, cols, tiles))
 
 
 @_entry
@@ -227,7 +241,7 @@ def mx_quantize_rowwise_fp4(x: torch.Tensor, q: Optional[torch.Tensor] = None, s
         q = torch.empty((rows, cols // 2), dtype=_U8, device=dev)
     if s_tiles is None:
         s_tiles = cols // 256
-    s_swz, ps = _swizzled(s_swz, rows, s_tiles, cols, "s_swz", dev)
+    s_swz, ps = _scales(s_swz, rows, cols, s_tiles, "s_swz", dev)
     px, ld_x = _rows(x, "x", dev, rows, cols, torch.bfloat16)
     pq, ld_q = _rows(q, "q", dev, rows, cols // 2, _U8)
     _call("mx_quantize_rowwise_fp4", dev, px, rows, cols, ld_x, pq, ld_q, ps, s_tiles)
@@ -256,11 +270,10 @@ def mx_quantize_colwise_fp4(x: torch.Tensor, qt: Optional[torch.Tensor] = None, 
     need = count * mx_scale_swizzled_bytes(cols, rows // 32)
     if st_swz is None:
         st_swz = torch.empty(max(need, 1), dtype=_U8, device=dev)
-    st_swz = _u8(st_swz)
     px, ld_x = _rows(flat, "x", dev, count * rows, cols, torch.bfloat16)
     pq, ld_qt = _rows(qt.view(count * cols, rows // 2) if x.dim() == 3 else qt, "qt", dev, count * cols, rows // 2, _U8)
     _call("mx_quantize_colwise_fp4", dev, px, count, rows, cols, ld_x, pq, ld_qt,
-          _at(st_swz, "st_swz", dev, _U8, least=need))
+          _scale_ptr(st_swz, "st_swz", dev, need))
     return qt, st_swz
 
 
@@ -278,8 +291,8 @@ def mx_dequantize_fp4(q: torch.Tensor, s_swz: torch.Tensor, y: Optional[torch.Te
     if s_tiles is None:
         s_tiles = cols // 256
     pq, ld_q = _rows(q, "q", dev, rows, half, _U8)
-    py, ld_y = _rows(y, "y", dev, rows, cols, *_OUT)
-    _, ps = _swizzled(s_swz, rows, s_tiles, cols, "s_swz", dev)
+    py, ld_y = _rows(y, "y", dev, rows, cols, _one_of(y, "y", _OUT))
+    ps = _scale_ptr(s_swz, "s_swz", dev, _scale_bytes(rows, cols, s_tiles))
     _call("mx_dequantize_fp4", dev, pq, rows, cols, ld_q, ps, s_tiles, py, ld_y, _OUT[y.dtype])
     return y
 
@@ -306,15 +319,15 @@ def mx_moe_dispatch_fp4(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: in
         slot = torch.empty(n, dtype=i32, device=dev)
     if q is None:
         q = torch.empty((n, hidden // 2), dtype=_U8, device=dev)
-    s_swz, ps = _swizzled(s_swz, n, hidden // 256, hidden, "s_swz", dev)
+    s_swz, ps = _scales(s_swz, n, hidden, hidden // 256, "s_swz", dev)
     need = mx_moe_dispatch_workspace_bytes(tokens, topk, num_experts)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=_U8, device=dev)
     px, ld_x = _rows(x, "x", dev, tokens, hidden, torch.bfloat16)
     pq, ld_q = _rows(q, "q", dev, n, hidden // 2, _U8)
-    _call("mx_moe_dispatch_fp4", dev, px, tokens, hidden, ld_x, _at(topk_ids, "topk_ids", dev, i32, shape=(tokens, topk)),
-          topk, num_experts, _at(offsets, "offsets", dev, torch.int64, shape=(num_experts + 1,)),
-          _at(src, "src", dev, i32, shape=(n,)), _at(slot, "slot", dev, i32, shape=(n,)), pq, ld_q, ps,
+    _call("mx_moe_dispatch_fp4", dev, px, tokens, hidden, ld_x, _at(topk_ids, "topk_ids", dev, i32, (tokens, topk)),
+          topk, num_experts, _at(offsets, "offsets", dev, torch.int64, (num_experts + 1,)),
+          _at(src, "src", dev, i32, (n,)), _at(slot, "slot", dev, i32, (n,)), pq, ld_q, ps,
           *_scratch(workspace, dev))
     return offsets, src, slot, q, s_swz
 
@@ -337,7 +350,7 @@ def mx_swiglu_quantize_fp4(gu: torch.Tensor, q: Optional[torch.Tensor] = None, s
     dev = gu.device
     if q is None:
         q = torch.empty((rows, F // 2), dtype=_U8, device=dev)
-    s_swz, ps = _swizzled(s_swz, rows, F // 256, F, "s_swz", dev)
+    s_swz, ps = _scales(s_swz, rows, F, F // 256, "s_swz", dev)
     if h is None and want_h:
         h = torch.empty((rows, F), dtype=torch.bfloat16, device=dev)
     pg, ld_gu = _rows(gu, "gu", dev, rows, F2, torch.bfloat16)
@@ -357,6 +370,13 @@ def mx_gemm_fp4_workspace_bytes(M: int, N: int, K: int, out_dtype: torch.dtype =
     return f(M, N, K, _OUT[out_dtype])
 
 
+@functools.lru_cache(maxsize=1024)
+def _gemm_workspace(device: int, M: int, N: int, K: int, dtype: torch.dtype) -> int:
+    """mx_gemm_fp4_workspace_bytes on the current device, which is `device`: a
+    function of the shape and the device alone."""
+    return mx_gemm_fp4_workspace_bytes(M, N, K, dtype)
+
+
 @_entry
 def mx_gemm_fp4(a_q: torch.Tensor, a_s_swz: torch.Tensor, b_q: torch.Tensor, b_s_swz: torch.Tensor,
                 c: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
@@ -372,12 +392,13 @@ def mx_gemm_fp4(a_q: torch.Tensor, a_s_swz: torch.Tensor, b_q: torch.Tensor, b_s
         c = torch.empty((M, N), dtype=out_dtype, device=dev)
     pa, ld_a = _rows(a_q, "a_q", dev, M, half, _U8)
     pb, ld_b = _rows(b_q, "b_q", dev, N, half, _U8)
-    pc, ld_c = _rows(c, "c", dev, M, N, *_OUT)
+    pc, ld_c = _rows(c, "c", dev, M, N, _one_of(c, "c", _OUT))
     if workspace is None:
-        need = mx_gemm_fp4_workspace_bytes(M, N, K, c.dtype)
-        workspace = torch.empty(need, dtype=_U8, device=dev) if need else None
-    _call("mx_gemm_fp4", dev, M, N, K, pa, ld_a, _swizzled(a_s_swz, M, K // 256, K, "a_s_swz", dev)[1], pb, ld_b,
-          _swizzled(b_s_swz, N, K // 256, K, "b_s_swz", dev)[1], pc, ld_c, _OUT[c.dtype], *_scratch(workspace, dev))
+        need = _gemm_workspace(dev.index, M, N, K, c.dtype)
+        if need:
+            workspace = torch.empty(need, dtype=_U8, device=dev)
+    _call("mx_gemm_fp4", dev, M, N, K, pa, ld_a, _scale_ptr(a_s_swz, "a_s_swz", dev, _scale_bytes(M, K, K // 256)), pb, ld_b,
+          _scale_ptr(b_s_swz, "b_s_swz", dev, _scale_bytes(N, K, K // 256)), pc, ld_c, _OUT[c.dtype], *_scratch(workspace, dev))
     return c
 
 
@@ -394,8 +415,8 @@ def mx_grouped_gemm_fp4(group_offsets: torch.Tensor, a_q: torch.Tensor, a_s_swz:
     if c is None:
         c = torch.empty((M, N), dtype=out_dtype, device=dev)
     pa, ld_a = _rows(a_q, "a_q", dev, M, half, _U8)
-    pc, ld_c = _rows(c, "c", dev, M, N, *_OUT)
-    _call("mx_grouped_gemm_fp4", dev, G, M, N, K, _at(group_offsets, "group_offsets", dev, torch.int64, shape=(G + 1,)),
-          pa, ld_a, _swizzled(a_s_swz, M, K // 256, K, "a_s_swz", dev)[1], _at(b_q, "b_q", dev, _U8, shape=(G, N, half)),
-          _at(b_s_swz, "b_s_swz", dev, _U8, least=G * mx_scale_swizzled_bytes(N, K // 32)), pc, ld_c, _OUT[c.dtype])
+    pc, ld_c = _rows(c, "c", dev, M, N, _one_of(c, "c", _OUT))
+    _call("mx_grouped_gemm_fp4", dev, G, M, N, K, _at(group_offsets, "group_offsets", dev, torch.int64, (G + 1,)),
+          pa, ld_a, _scale_ptr(a_s_swz, "a_s_swz", dev, _scale_bytes(M, K, K // 256)), _at(b_q, "b_q", dev, _U8, (G, N, half)),
+          _scale_ptr(b_s_swz, "b_s_swz", dev, G * ((N + 31) // 32) * K), pc, ld_c, _OUT[c.dtype])
     return c

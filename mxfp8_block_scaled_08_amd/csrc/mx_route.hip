@@ -2,7 +2,7 @@
 // combine (gfx950).
 //
 // Routing.  LANES lanes take a token (16 up to 128 experts, 32 up to 256, else
-// the wave), so a wave holds 4, 2 or 1 tokens; lane l holds the selection keys
+// the wave), so a wave holds 4, 2 or 1 tokens, and four waves make a workgroup; lane l holds the selection keys
 // of experts l*EPL .. +EPL-1 in registers, 4 to 16 of them.  A key is a double:
 // the selection score with its low 10 mantissa bits replaced by the expert's
 // number, in such a way that of two equal scores the lower expert's key is the
@@ -25,6 +25,8 @@ namespace mx {
 static_assert(ROUTE_MAX_TOPK <= 32, "a 16-lane token keeps two of the chosen a lane, a wider one one");
 static_assert(ROUTE_MAX_GROUPS == 64, "kept groups are a 64-bit mask");
 static_assert(MOE_MAX_EXPERTS == 1024, "keys hold 10 bits of expert number");
+
+constexpr int RT_THREADS = 256;  // four waves a workgroup, no token in two of them
 
 typedef float f4_t __attribute__((ext_vector_type(4)));
 
@@ -201,12 +203,12 @@ struct RouteParams {
 
 // DT: logits' type (0 BF16, 1 FP32); SOFTMAX: score; GROUPS: groups > 1.
 template <int LANES, int EPL, int DT, bool SOFTMAX, bool GROUPS>
-__global__ __launch_bounds__(64) void route_kernel(RouteParams p)
+__global__ __launch_bounds__(RT_THREADS) void route_kernel(RouteParams p)
 {
-    constexpr int TOKENS = 64 / LANES;        // a wave's
+    constexpr int TOKENS = RT_THREADS / LANES;  // a workgroup's
     constexpr int NSEL = LANES >= 32 ? 1 : 2;  // chosen experts a lane keeps
     extern __shared__ double s_keys[];  // GROUPS: [TOKENS][experts] keys, then [TOKENS][groups] group scores
-    const int lane = threadIdx.x, l = lane & (LANES - 1), sub = lane / LANES;
+    const int l = threadIdx.x & (LANES - 1), sub = threadIdx.x / LANES;
     const int64_t t = (int64_t)blockIdx.x * TOKENS + sub;
     const bool live = t < p.tokens && (p.mask == nullptr || p.mask[t] != 0);
     const int64_t row = live ? t * p.ld : 0;
@@ -377,11 +379,11 @@ struct RouteBwdParams {
 // which need no division by a small S.  Each lane then gathers the chosen
 // ones' values for its own experts, in order j = 0, 1, ..
 template <int LANES, int EPL, int DT, bool SOFTMAX>
-__global__ __launch_bounds__(64) void route_bwd_kernel(RouteBwdParams p)
+__global__ __launch_bounds__(RT_THREADS) void route_bwd_kernel(RouteBwdParams p)
 {
     constexpr int NSEL = LANES >= 32 ? 1 : 2;
-    const int lane = threadIdx.x, l = lane & (LANES - 1), sub = lane / LANES;
-    const int64_t t = (int64_t)blockIdx.x * (64 / LANES) + sub;
+    const int lane = threadIdx.x & 63, l = lane & (LANES - 1);
+    const int64_t t = (int64_t)blockIdx.x * (RT_THREADS / LANES) + threadIdx.x / LANES;
     const bool live = t < p.tokens;
     const int64_t row = live ? t * p.ld : 0;
     const bool full = SOFTMAX && !p.renorm;  // every expert's score takes part
@@ -518,8 +520,8 @@ template <typename F> static void by_experts(int64_t experts, F f)
 template <int LANES, int EPL, int DT, bool SOFTMAX>
 static void launch_route_t(const RouteParams &p, hipStream_t stream)
 {
-    constexpr int TOKENS = 64 / LANES;
-    const dim3 grid((unsigned)((p.tokens + TOKENS - 1) / TOKENS)), block(64);
+    constexpr int TOKENS = RT_THREADS / LANES;
+    const dim3 grid((unsigned)((p.tokens + TOKENS - 1) / TOKENS)), block(RT_THREADS);
     if (p.groups > 1)
         hipLaunchKernelGGL((route_kernel<LANES, EPL, DT, SOFTMAX, true>), grid, block,
                            (size_t)TOKENS * (p.experts + p.groups) * 8, stream, p);
@@ -554,7 +556,7 @@ hipError_t launch_moe_route_bwd(const void *logits, int dtype, int64_t tokens, i
         const bool vec = vec_rows(logits, ld, dtype, experts, E) && vec_rows(dx, ld_d, dtype, experts, E);
         const RouteBwdParams p{logits, tokens, ld, (int)experts, vec ? 1 : 0, (int)topk, renorm ? 1 : 0, scale, ids,
                                dw, dx, ld_d};
-        const dim3 grid((unsigned)((tokens * L + 63) / 64)), block(64);
+        const dim3 grid((unsigned)((tokens * L + RT_THREADS - 1) / RT_THREADS)), block(RT_THREADS);
         if (dtype == 0 && softmax)
             hipLaunchKernelGGL((route_bwd_kernel<L, E, 0, true>), grid, block, 0, stream, p);
         else if (dtype == 0)

@@ -1,24 +1,33 @@
 // MXFP4 products for gfx950 (CDNA4): dense and grouped per expert.
 //
-// C[m][n] = sum_k deq(A)[m][k] deq(B)[n][k] on v_mfma_scale_f32_16x16x128:
-// lane l = 16g + r holds the 32 E2M1 (16 bytes) of block g of row r, and that
-// block's E8M0 scale.  In the rearranged scale layout block 2t + h of a 256-K
-// group is byte t of word 32h + row, so the word of lane l is 32(g & 1) + row
-// and step s (128 K) takes its byte 2s + (g >> 1).
+// C[m][n] = sum_k deq(A)[m][k] deq(B)[n][k] on CDNA4's scaled matrix cores with
+// FP32 accumulation.  Two kernels: one for a few rows, bound by reading B, and
+// one on LDS tiles for the rest, bound by the matrix cores (and, with every
+// unit busy, by the power they draw) and the LDS traffic that feeds them.
+//
+// Operands (layouts measured on gfx950): of v_mfma_scale_f32_16x16x128, lane
+// 16g + r holds the 32 E2M1 codes (16 bytes) of block g of row r; of
+// 32x32x64, lane 32h + r those of block h of row r.  The lane also gives that
+// block's E8M0 scale: the byte of a 4-byte register that the instruction's
+// byte select names.  In the rearranged scale layout block 2t + h of a 256-K
+// group is byte t of word 32h + row, so a lane's word serves four steps of
+// 32x32x64 (h, byte t) and two of 16x16x128 (word 32(g & 1) + row, byte
+// 2s + (g >> 1) at step s).
+//
+// E2M1 products are multiples of 1/4 up to 36, so a 32-block's sum is exact;
+// the blocks' sums are added in FP32.
 //
 // B's rows feed the first operand and A's the second, so a lane ends up with
 // four consecutive columns of one row of C.
 #include "mx_device.h"
+#include "mx_gemm_util.h"
 #include "mx_launch.h"
-#include "mx_plan.h"
 
 #include <algorithm>
 #include <type_traits>
 
 namespace mx {
 
-typedef int v4i __attribute__((ext_vector_type(4)));
-typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 struct Gemm4Params {
@@ -39,7 +48,9 @@ struct Gemm4Params {
     uint32_t as_bytes, bs_bytes;  // rearranged scale bytes of A (all rows) and of one B
     int vec_store;  // C rows allow 4-element vector stores
     int vec16;      // BF16 C: rows allow 16-byte stores (8 elements)
-    // split tail (dense only), as mx_gemm's
+    // split tail (dense only): tiles dp_tiles .. dp_tiles + split_tiles - 1 are
+    // each cut into split_s K ranges of whole 512-K groups, one workgroup per
+    // range, whose FP32 partial tiles go to ws
     int64_t dp_tiles;
     int split_tiles, split_s;
     float *ws;
@@ -61,12 +72,14 @@ constexpr int ROWS_CHUNK = 64;  // few rows: rows of one workgroup
 constexpr int FMT_E2M1 = 4;  // the instruction's operand format code
 
 // Few rows.  A wave takes 16 columns of C and a range of 256-K groups, of up to
-// 16 * MT rows at a time; ksplit waves of a workgroup share the columns,
-// each with its own range of K, and their sums meet in LDS, added in K order.
-// B, which is most of what there is to read, goes straight to registers in the
-// matrix cores' layout, up to MAXG groups (2 KiB each) in flight
-// a wave, and stays there while the rows of A pass (a group of 16 * MT rows
-// after another); A comes out of L2.
+// 16 * MT rows at a time; ksplit waves of a workgroup share the columns, each
+// with its own range of K, and their sums meet in LDS, added in K order.  B,
+// which is most of what there is to read, goes straight to registers in the
+// matrix cores' layout, up to MAXG groups (2 KiB each) in flight a wave, and
+// stays there while the rows of A pass, 16 * MT after another; A comes out of
+// L2.  Bound by reading B: one row x 24576x4096 (53 MB) takes 12.4 us, 4.3 TB/s;
+// x 6144x4096 5.0 us, of which an empty launch is 2.4.  With four waves a tile
+// and one group in flight, as at first, x 4096x12288 took 16.7 us instead of 7.4.
 template <bool GROUPED, int CT, int MT, int MAXG>
 __global__ __launch_bounds__(1024) void gemm4_rows_kernel(Gemm4Params p)
 {
@@ -236,94 +249,9 @@ __global__ __launch_bounds__(1024) void gemm4_rows_kernel(Gemm4Params p)
 
 // ---------------------------------------------------------------------------
 
-typedef float v16f __attribute__((ext_vector_type(16)));
-
 constexpr int BK = 64;             // bytes of K (128 codes) per stage: two matrix-core steps
 constexpr int NBUF = 4;            // stages in the LDS ring (one 512-K group)
 constexpr int GM_THREADS = 256;    // 4 waves, one per SIMD, 2x2 over the tile
-constexpr int GROUP_M = 4;         // tile-rows walked together for L2 reuse
-
-// The 16-byte slot of a 64-byte LDS row that holds chunk c is c ^ chunk_perm(row).
-__device__ __forceinline__ int chunk_perm(int row) { return (row >> 2) & 3; }
-
-// Two FP32 -> packed BF16 (low half first), round to nearest even: one
-// v_cvt_pk_bf16_f32 on this target (NaN stays NaN).
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
-{
-    typedef float f2_t __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2_t{lo, hi}), bf16x2_t));
-}
-
-
-// Values every lane holds alike, moved to scalar registers.
-__device__ __forceinline__ int64_t uniform(int64_t x)
-{
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)x >> 32));
-    return (int64_t)(((uint64_t)hi << 32) | lo);
-}
-template <typename T> __device__ __forceinline__ const T *uniform(const T *x)
-{
-    return reinterpret_cast<const T *>(uniform((int64_t)(uintptr_t)x));
-}
-
-// A wave-uniform value the compiler must take as unknown at this point, so
-// that what it derives from it (a divisor's reciprocal) is formed where it is
-// used and not kept in vector registers across the main loop.
-__device__ __forceinline__ int64_t opaque(int64_t x)
-{
-    asm volatile("" : "+s"(x));
-    return x;
-}
-
-// Tile t of a GROUP_M-row band walk over tiles_m x tiles_n tiles -> (m, n):
-// the bands of GROUP_M tile-rows are taken in turn, and within a band the
-// tiles column by column.  t < GROUP_M * tiles_n * ceil(tiles_m / GROUP_M)
-// and tiles_n < 2^21, so the in-band index fits 32 bits; the band height
-// (GROUP_M, less for the last band) is 1 to 4, divided by shifts or by the
-// exact multiply-high for 3.
-__device__ __forceinline__ void band_walk(int64_t t, int64_t tiles_m, int64_t tiles_n, int64_t &m,
-                                          int64_t &n)
-{
-    static_assert(GROUP_M == 4, "the band division below assumes bands of at most 4 tile-rows");
-    const int64_t per_band = opaque(GROUP_M * tiles_n);
-    const int64_t band = t / per_band;
-    const int64_t first_m = band * GROUP_M;
-    const uint32_t gm = (uint32_t)min(tiles_m - first_m, (int64_t)GROUP_M);
-    const uint32_t in = (uint32_t)(t - band * per_band);
-    const uint32_t q = gm == 4   ? in >> 2
-                       : gm == 2 ? in >> 1
-                       : gm == 1 ? in
-                                 : (uint32_t)(((uint64_t)in * 0xAAAAAAABull) >> 33);
-    m = first_m + (int64_t)(in - q * gm);
-    n = (int64_t)q;
-}
-
-// Workgroup barrier for the LDS ring.  __syncthreads() would also wait for
-// every outstanding vector-memory load (its release fence is conservative),
-// draining the register prefetch each stage.  The ring is only written and
-// read with LDS instructions, so each wave waits for its own LDS writes and
-// reads and then meets the others; the "memory" clobber keeps the compiler
-// from moving LDS accesses across the barrier.
-__device__ __forceinline__ void lds_ring_barrier()
-{
-    __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));  // lgkmcnt(0)
-    asm volatile("s_barrier" ::: "memory");
-}
-
-// Coordinates of one 256x256 output tile, and the 128-K stages of it a unit
-// of work covers: ns stages from stage kb (both multiples of 4: whole 512-K
-// groups).
-// (32-bit fields: row and column counts are below 2^29, experts at most
-// 1024; a workgroup holds three tiles at a time in scalar registers.)
-struct Tile {
-    int m0, n0, m_end;
-    int g;  // expert (grouped modes), else 0
-    int kb, ns;
-    int sp;  // split-tail slot (tile * split_s + range), or -1 for a whole tile
-};
-
-constexpr int GROUP_TABLE = 1024;  // experts whose tile table fits in LDS
 
 template <bool GROUPED, int CT, bool SPLIT, int TM, int TN>
 __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_kernel(Gemm4Params p)
@@ -492,7 +420,7 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
         return c;
     };
 
-    // ---- operand loads.  Two consecutive stages of a tile (128 K: one
+    // ---- operand loads.  Two consecutive stages of a tile (256 K: one
     // 128-byte cache line of each row) of A and of B are loaded together
     // into registers, 16 bytes per lane and instruction, and written to the
     // LDS ring two stages later.  Instruction i of this wave covers rows
@@ -516,7 +444,7 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
     const uint32_t w_row = (uint32_t)(prow * BK + ((lane & 3) ^ chunk_perm(prow)) * 16);
     const uint32_t wa_off = (uint32_t)(lane >> 5) * A_STAGE + w_row, wb_off = (uint32_t)(lane >> 5) * B_STAGE + w_row;
     // Loads of stages st, st + 1 (st even) of tile T, load q into R[q] (A
-    // rows for q < 8, then B rows).  A pair past the end or of padding (live
+    // rows for q < QA, then B rows).  A pair past the end or of padding (live
     // false) gets an empty range and loads zeros, which keeps the main loop
     // branch-free.  (32-bit sizes: row counts are below 2^29; a 64-bit
     // compare would need a vector register for a uniform value.)
@@ -545,9 +473,9 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
 
     // ---- scale words.  Per 256-K (two stages) the lane (h, r) supplies, for A
     // sub-tile i, the word of row m0 + wm*WM + 32i + r: entry 32h + (row &
-    // 31) of the row's 32-row scale tile, whose 512-K group s sits at s * 256
+    // 31) of the row's 32-row scale tile, whose 256-K group s sits at s * 256
     // within the tile's KT * 256 bytes (likewise for B).  Each is one 4-byte
-    // load into a register, two stages ahead.  Rows past the operand fall
+    // load into a register, three stages ahead.  Rows past the operand fall
     // outside the resource's range, and groups past K get an empty one: they
     // read zero (2^-127), which times the zero codes there is zero.
     const uint32_t stile = (uint32_t)KT * 256;  // bytes per 32-row scale tile (below 2^32)
@@ -577,9 +505,9 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
     };
     static_assert(TN % 2 == 0, "BF16 stores pair adjacent sub-tiles");
 
-    // ---- per-lane LDS read offsets of the matrix-core fragments.  The lane
-    // needs chunk h (bytes 0-15 of the operand) and chunk 2 + h (bytes
-    // 16-31) of its row's 64 bytes.  Rows of the sub-tiles are 32 apart,
+    // ---- per-lane LDS read offsets of the matrix-core fragments.  Of its
+    // row's 64 bytes (four blocks) the lane needs chunk h, its block of the
+    // stage's first step, and chunk 2 + h, that of the second.  Rows of the sub-tiles are 32 apart,
     // which leaves chunk_perm unchanged, and chunk 2 + h sits in the slot of
     // chunk h XOR 2, so the second read is at the first offset XOR 32.  The
     // sub-tile and the ring buffer are immediate offsets of the LDS read.
@@ -743,24 +671,33 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
         }
     };
 
-    // Stage u of the sequence (64 K) uses ring buffer u % 4 = t, its
-    // position in its 512-K group, and byte t of the group's scale words.
-    // On entry its fragments are in registers (set t & 1) and stage u+1 is
-    // in the ring for every wave.  While the stage's 16 matrix-core
-    // instructions run, the wave
+    // Stage u of the sequence (128 K, two steps) uses ring buffer u % 4 = t,
+    // its position in its 512-K group.  On entry its fragments are in registers
+    // (set t & 1) and stage u+1 is in the ring for every wave.  While the
+    // stage's 2 TM TN matrix-core instructions run, the wave
     //   - at even t, writes the pair of stages u+2, u+3 that it loaded at
     //     stage u-2 into ring buffers (t+2) % 4 and (t+3) % 4 (their
     //     fragments were read at stages u-3 and u-2, before the last
     //     barrier), and loads the pair u+4, u+5 into the same registers, one
     //     128-byte line of each row: the load path sees a steady stream of
     //     whole-line requests, each with two stages' time to land;
-    //   - at t = 3, loads the next group's scale words (consumed at the next stage);
+    //   - at odd t, loads scale words of the next group;
     //   - reads stage u+1's fragments into the other register set.
     // A barrier then makes this wave's LDS writes and reads complete for
     // every wave.  The compiler places the waits for the loads, which only
     // feed registers.  Past the end the loads are empty (their range is) and
     // the fragment reads unused, so the body has no branches.  After a
     // unit's last stage its accumulators are stored and cleared.
+    //
+    // Measured on one MI355X: 12288x4096x24576 in 521 us, 4.74 PFLOP/s.  Without
+    // the scale words, the LDS writes and the loads the matrix cores and their
+    // LDS reads alone take 432 us (a stage 0.75 us, against 0.47 with 16 units
+    // at work: the clock falls under the load); loads cost 11 %, LDS writes 6 %,
+    // scale words 4 %.  What did not pay: loads four stages ahead (-1 to -4 %),
+    // B's fragments a stage ahead (0), one barrier every two stages (at most
+    // 2 %), a unit's first group as its own copy so that waits for loads let
+    // the previous tile's stores drain (registers spill), a start staggered over
+    // the units (0), other cache policies of C's stores (0 to -20 %).
     for (int64_t k = 0; k < my_units; k++) {
         // nxt: the unit after this one (loaded during this unit's last group)
         const ScaleLanes nxt_sl = scale_lanes(nxt);
@@ -788,8 +725,8 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
                     load_scales(ld, ld_sl, ((ld.kb + st4) >> 1) + 1, live && ((ld.kb + st4) >> 1) + 1 < KT, sa, sb);
                 // Per B sub-tile i: read B sub-tile i + 1 (or the next
                 // stage's first) and the next stage's A sub-tile i, then at
-                // even t a quarter of the pair writes and loads, while the
-                // four matrix-core instructions of row i run.  LDS writes and
+                // even t its share of the pair writes and loads, while the
+                // 2 TM matrix-core instructions of row i run.  LDS writes and
                 // reads stay in program order (the compiler cannot tell the
                 // ring buffers apart), so reads come first in each row.
                 v8i xb = fb_first;
@@ -989,35 +926,11 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
     __builtin_amdgcn_s_waitcnt(0 | (7 << 4) | (15 << 8));  // the prefetch past the end: let it land
 }
 
-static int vec_ok(const void *c, int64_t ld_c, int c_dtype)
-{
-    const uintptr_t align = c_dtype == 0 ? 8 : 16;
-    return ((uintptr_t)c % align == 0) && (ld_c % 4 == 0);
-}
-
-// Compute units of the current device (one persistent workgroup each: the
-// kernel's LDS admits one workgroup per CU).
-static int cu_count()
-{
-    static int cache[64];
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64)
-        return 256;
-    if (cache[dev] == 0) {
-        int n = 0;
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
-            n <= 0)
-            n = 256;
-        cache[dev] = n;
-    }
-    return cache[dev];
-}
-
-// Sums of the split tail: thread t of tile r's 16384 takes float4 t of the
-// tile's slots (the partial-tile layout above: wave, sub-tile (i, j),
-// register group q, lane), adds the split_s slots in range order and writes
-// the four BF16 of C they hold, row wm*WM + 32j + (lane & 31), columns
-// wn*128 + 32i + 8q + 4(lane >> 5) .. +3.
+// Sums of the split tiles: thread t of a tile's takes float4 t of its slots
+// (the partial-tile layout above: wave, sub-tile (i, j), register group q,
+// lane), adds the split_s slots in range order and writes the four BF16 of C
+// they hold: row wm*WM + 32j + (lane & 31), columns wn*WN + 32i + 8q +
+// 4(lane >> 5) .. +3.
 template <int TM, int TN>
 __global__ __launch_bounds__(256) void split4_reduce_kernel(Gemm4Params p)
 {

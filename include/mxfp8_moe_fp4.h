@@ -67,19 +67,22 @@ typedef enum mx_score {
  *              scale * s / (sum of the chosen s)
  * Selection score: s + bias formed in 64 bits and compared to 42 bits of its
  * mantissa; without a bias and with group_top 1 the logit itself (the same
- * order, exactly).  An expert whose logit is -inf is never chosen; where
+ * order, exactly).  An expert whose logit is -inf is never chosen and counts as
+ * -inf in its group's score (so with group_top 2 a group with one expert left
+ * ranks last); groups of equal score rank by number; where
  * fewer than topk can be, the remaining ids are -1 (which mx_moe_dispatch
  * does not route) and their weights 0, as for a masked token.  Renormalized
  * weights are formed from score ratios, so they sum to scale however small
  * the chosen scores are.
- * A NaN logit ranks above every number; the weights it takes part in are NaN,
- * the ids stay in range.
+ * A NaN logit ranks above every number, +inf next; the weights they take part
+ * in are NaN (except +inf's sigmoid, which is 1), the ids stay in range.
  * Requirements: tokens >= 0, num_experts in 1..1024, 1 <= topk <=
  * min(MX_ROUTE_MAX_TOPK, topk_groups * num_experts / num_groups),
  * num_experts % num_groups == 0, 1 <= topk_groups <= num_groups, group_top 1
  * or 2 and at most num_experts / num_groups, ld_logits >= num_experts, scale
- * finite (else MX_ERR_INVALID_ARG, or MX_ERR_UNSUPPORTED above 1024 experts
- * or topk 32); pointers aligned to their elements (else MX_ERR_ALIGN);
+ * finite (else MX_ERR_INVALID_ARG, or MX_ERR_UNSUPPORTED above 1024 experts,
+ * topk 32 or 64 groups, from 2^26 tokens or for a leading dimension from 2^28);
+ * pointers aligned to their elements (else MX_ERR_ALIGN);
  * outputs overlap nothing (else MX_ERR_OVERLAP).
  */
 mx_status mx_moe_route(const void *logits, int logits_dtype, int64_t tokens, int64_t num_experts, int64_t ld_logits,
@@ -204,12 +207,14 @@ mx_status mx_swiglu_quantize_fp4(const void *gu, int64_t rows, int64_t F, int64_
  *   b_q  E2M1 [N][ld_b], b_s_swz likewise
  *   c    [M][ld_c] of c_dtype
  * Requirements as mx_gemm's with K % 256 == 0 (else MX_ERR_UNSUPPORTED; K %
- * 32 else MX_ERR_SHAPE) and ld_a, ld_b >= K/2 bytes.  A few rows (M <= 64:
- * single tokens of a sampler) stream B once through all compute units; larger
- * products take mx_gemm's 256x256 tiles and, as there, a workspace of
- * mx_gemm_fp4_workspace_bytes bytes for the split of a partial last round.
- * Which way a product takes, and its sums' order, depend on M, N, K, c's type
- * and alignment and the device's compute-unit count only.
+ * 32 else MX_ERR_SHAPE) and ld_a, ld_b >= K/2 bytes.  The library estimates
+ * the time of each way and takes the least: up to 64 rows (single tokens of a
+ * sampler) a kernel that streams B once through all compute units, else tiles
+ * of 128x128, 256x128 or 256x256, whose partial last round may be split along K
+ * (BF16 C only), with FP32 sums in a workspace of mx_gemm_fp4_workspace_bytes
+ * bytes (0: none needed; at most 64 MiB).  The way, and with it the sums'
+ * order, depends on M, N, K, c's type and alignment and the device's
+ * compute-unit count only.
  */
 int64_t mx_gemm_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int c_dtype);
 mx_status mx_gemm_fp4(int64_t M, int64_t N, int64_t K, const void *a_q, int64_t ld_a, const void *a_s_swz,
@@ -221,7 +226,9 @@ mx_status mx_gemm_fp4(int64_t M, int64_t N, int64_t K, const void *a_q, int64_t 
  * operands (b_q E2M1 [num_groups][N][K/2 bytes] contiguous).  Rows of C
  * outside every group are not written.  Requirements as mx_grouped_gemm's
  * with K % 256 == 0.  Few rows per expert (a sampler's step) stream each
- * routed expert's weights once; the rule goes by M_total and num_groups.
+ * routed expert's weights once; more take tiles of 128x128 or 256x256.  The
+ * rule goes by M_total, num_groups, N and the device's compute-unit count, so
+ * the offsets are read on the device alone.
  */
 mx_status mx_grouped_gemm_fp4(int64_t num_groups, int64_t M_total, int64_t N, int64_t K, const int64_t *group_offsets,
                               const void *a_q, int64_t ld_a, const void *a_s_swz, const void *b_q,

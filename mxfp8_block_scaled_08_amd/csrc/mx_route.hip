@@ -2,8 +2,9 @@
 // combine (gfx950).
 //
 // Routing.  LANES lanes take a token (16 up to 128 experts, 32 up to 256, else
-// the wave), so a wave holds 4, 2 or 1 tokens, and four waves make a workgroup; lane l holds the selection keys
-// of experts l*EPL .. +EPL-1 in registers, 4 to 16 of them.  A key is a double:
+// the wave), so a wave holds 4, 2 or 1 tokens, and four waves make a workgroup;
+// lane l holds the selection keys of experts l*EPL .. +EPL-1 in registers, 4 to
+// 16 of them.  A key is a double:
 // the selection score with its low 10 mantissa bits replaced by the expert's
 // number, in such a way that of two equal scores the lower expert's key is the
 // larger, so one v_max_f64 finds both the best score and the lowest expert that
@@ -13,6 +14,13 @@
 // two experts' sums are compared, not approximated: in FP32 about one row in ten
 // thousand would swap two experts.  FP64 costs the same issue slots as FP32 on
 // CDNA4's vector unit.
+//
+// Bound by the chain of topk reductions, five dependent exchanges each, not by
+// the logits' bytes: 20480 FP32 tokens x 128 experts, top 8, take 8.2 us (10.5
+// MB, 2.1 us of HBM, behind an empty launch of 2.2), 32 BF16 tokens 4.2 us.  With
+// score and number compared apart and element loads it was 12.5 us, with one
+// wave a workgroup 8.6.  4099 tokens x 256 experts in 8 groups with a bias take
+// 12.1 us, and took 19.1 with 16 lanes a token and 16 experts a lane.
 #include "mx_device.h"
 #include "mx_launch.h"
 
@@ -377,7 +385,11 @@ struct RouteBwdParams {
 //            ds_k s_k is zero, so nothing flows to the others)
 //   sigmoid  dx_j = scale (g_j - D) r_j (1 - s_j)
 // which need no division by a small S.  Each lane then gathers the chosen
-// ones' values for its own experts, in order j = 0, 1, ..
+// ones' values for its own experts, in order j = 0, 1, ..  Every column is
+// written once, so nothing is cleared first and no atomics are needed.  20480
+// FP32 tokens x 128 experts, top 8, renormalized: 6.3 us, of which an empty
+// launch is 2.2; it reads the lines of the logits that hold a chosen one (nearly
+// all, 10.5 MB) and writes 10.5 MB, 4.4 us of HBM.
 template <int LANES, int EPL, int DT, bool SOFTMAX>
 __global__ __launch_bounds__(RT_THREADS) void route_bwd_kernel(RouteBwdParams p)
 {
@@ -573,7 +585,10 @@ hipError_t launch_moe_route_bwd(const void *logits, int dtype, int64_t tokens, i
 // columns of d_out and walks the token's slots: the slot's row of y is read
 // once for the dot product, weight * d_out is written to the slot's row of
 // dy.  The dot products are summed over the lanes, then over the waves in
-// order, once per 8 slots.
+// order, once per 8 slots.  Bound by HBM: 20480 tokens, top 8, hidden 2048 move
+// 1.43 GB in 258 us, 5.5 TB/s (a plain copy 5.0); both results of one pass, as
+// two passes would read d_out twice.  Rows up to 512 or 1024 wide take one or
+// two waves, so that no lane is without columns.
 constexpr int CB_SLOTS = 8;
 
 template <int WAVES>

@@ -67,8 +67,8 @@ def _entry(fn):
 
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        first = args[0] if args else kw[name]
-        if not first.is_cuda:
+        first = args[0] if args else kw.get(name)
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise ValueError(f"{name} must be a device tensor")
         dev = first.device
         if stream is None and dev.index == torch._C._cuda_getDevice():

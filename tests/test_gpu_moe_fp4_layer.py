@@ -119,6 +119,50 @@ def test_large_buffers(gpu_lib):
     assert torch.equal(x[-5:], mx.mx_dequantize_fp4(q[M // 32 * 32:], s[M // 32 * N:])[-5:])
 
 
+def test_large_expert_rows_and_stacks(gpu_lib):
+    """y, dy, a stack of weights and the grouped product's B beyond 2^32 bytes:
+    both ends equal the same rows in a small call."""
+    mx = gpu_lib
+    g = torch.Generator(device=dev)
+    g.manual_seed(8)
+    T, k, H = 131_400, 8, 2048
+    n = T * k
+    y = torch.randint(-32768, 32767, (n, H), generator=g, device=dev, dtype=torch.int16).clamp_(0x3000, 0x4000).view(torch.bfloat16)
+    assert y.numel() * 2 > 1 << 32
+    d = torch.randn(T, H, generator=g, device=dev).bfloat16()
+    w = torch.rand(T, k, generator=g, device=dev)
+    slot = torch.arange(n - 1, -1, -1, device=dev, dtype=torch.int32)   # the first token has the last rows
+    dy, dw = mx.mx_moe_combine_bwd(d, y, slot, w)
+    for lo in (0, T - 4):
+        rows = slot[lo * k:(lo + 4) * k].long()
+        some = torch.arange(4 * k, device=dev, dtype=torch.int32)
+        dy2, dw2 = mx.mx_moe_combine_bwd(d[lo:lo + 4], y[rows], some, w[lo:lo + 4].contiguous())
+        assert torch.equal(dy[rows], dy2) and torch.equal(dw[lo:lo + 4], dw2)
+    del dy, dw
+    G, N, K = 1026, 1024, 2048
+    x = y.view(-1)[:G * N * K].view(G, N, K)
+    q, s = mx.mx_quantize_colwise_fp4(x)
+    per = mx.mx_scale_swizzled_bytes(K, N // 32)
+    for e in (0, G - 1):
+        q2, s2 = mx.mx_quantize_colwise_fp4(x[e])
+        assert torch.equal(q[e], q2) and torch.equal(s[e * per:(e + 1) * per], s2)
+    del q, s, x, y
+    G, N, K, M = 260, 8192, 4096, 700
+    b, sb = _random_operand(g, G * N, K)
+    assert b.numel() > 1 << 32
+    a, sa = _random_operand(g, M, K)
+    for rows in ([1, 3], [300, 400]):          # few rows; tiles
+        off = torch.zeros(G + 1, dtype=torch.int64, device=dev)
+        off[1:] = rows[0]
+        off[G] = sum(rows)
+        m = sum(rows)
+        C = mx.mx_grouped_gemm_fp4(off, a[:m], sa, b.view(G, N, K // 2), sb)
+        A = _decode(a, sa)[:m]
+        for e, lo, hi in ((0, 0, rows[0]), (G - 1, rows[0], m)):
+            sl = N * K // 32
+            _close(C[lo:hi], A[lo:hi], _decode(b[e * N:(e + 1) * N], sb[e * sl:(e + 1) * sl]), f"expert {e} of {rows}")
+
+
 def test_grouped_debug_check(gpu_lib, monkeypatch):
     mx = gpu_lib
     g = torch.Generator(device=dev)

@@ -84,10 +84,8 @@ def _entry(fn):
     return call
 
 
-def _at(t: Optional[torch.Tensor], name: str, dev, dtype, shape) -> Optional[int]:
-    """Pointer of t (None stays None), a contiguous tensor of dtype and shape on dev."""
-    if t is None:
-        return None
+def _at(t: torch.Tensor, name: str, dev, dtype, shape) -> int:
+    """Pointer of t, a contiguous tensor of dtype and shape on dev."""
     if t.dtype is dtype and t.device == dev and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
     if t.device != dev:
@@ -112,11 +110,39 @@ def _rows(t: torch.Tensor, name: str, dev, rows: int, cols: int, dtype) -> Tuple
     return t.data_ptr(), t.stride(0) if rows > 1 else cols
 
 
+def _out_at(t: Optional[torch.Tensor], name: str, dev, dtype, *shape) -> Tuple[torch.Tensor, int]:
+    """(t, pointer) of an output of dtype and shape on dev, a new tensor if t is None.
+
+    (Sizes as separate arguments, and no check of what was just made: 0.6 us
+    an output less of a call's 8.)"""
+    if t is None:
+        t = torch.empty(*shape, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    return t, _at(t, name, dev, dtype, shape)
+
+
+def _out_rows(t: Optional[torch.Tensor], name: str, dev, rows: int, cols: int, dtype) -> Tuple[torch.Tensor, int, int]:
+    """(t, pointer, leading dimension) of a [rows][cols] output on dev, a new tensor if t is None."""
+    if t is None:
+        t = torch.empty(rows, cols, dtype=dtype, device=dev)
+        return t, t.data_ptr(), cols
+    return (t, *_rows(t, name, dev, rows, cols, dtype))
+
+
 def _one_of(t: torch.Tensor, name: str, dtypes):
     """t's dtype, which must be among dtypes."""
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     return t.dtype
+
+
+def _out_dtype(t: Optional[torch.Tensor], name: str, dtype: torch.dtype) -> torch.dtype:
+    """The output's type: t's, or dtype where a new tensor is made; BF16 or FP32."""
+    if t is not None:
+        return _one_of(t, name, _OUT)
+    if dtype not in _OUT:
+        raise ValueError(f"out_dtype must be {' or '.join(map(str, _OUT))}, got {dtype}")
+    return dtype
 
 
 _U8 = torch.uint8
@@ -144,16 +170,15 @@ def mx_moe_route(logits: torch.Tensor, topk: int, *, bias: Optional[torch.Tensor
     unrouted (ids -1, weights 0), as experts with a logit of -inf are."""
     tokens, experts = logits.shape
     dev = logits.device
-    if topk_ids is None:
-        topk_ids = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
-    if weights is None:
-        weights = torch.empty((tokens, topk), dtype=torch.float32, device=dev)
-    x, ld = _rows(logits, "logits", dev, tokens, experts, _one_of(logits, "logits", _LOGITS))
-    _call("mx_moe_route", dev, x, _LOGITS[logits.dtype], tokens, experts, ld,
-          _at(bias, "bias", dev, torch.float32, (experts,)), _score(score), num_groups, topk_groups, group_top,
-          topk, int(renormalize), scale, _at(mask, "mask", dev, torch.bool if mask is not None and mask.dtype is torch.bool else _U8, (tokens,)),
-          _at(topk_ids, "topk_ids", dev, torch.int32, (tokens, topk)),
-          _at(weights, "weights", dev, torch.float32, (tokens, topk)))
+    dtype = _one_of(logits, "logits", _LOGITS)
+    x, ld = _rows(logits, "logits", dev, tokens, experts, dtype)
+    pb = None if bias is None else _at(bias, "bias", dev, torch.float32, (experts,))
+    pm = None if mask is None else _at(mask, "mask", dev, torch.bool if mask.dtype is torch.bool else _U8, (tokens,))
+    score = _score(score)
+    topk_ids, pi = _out_at(topk_ids, "topk_ids", dev, torch.int32, tokens, topk)
+    weights, pw = _out_at(weights, "weights", dev, torch.float32, tokens, topk)
+    _call("mx_moe_route", dev, x, _LOGITS[dtype], tokens, experts, ld, pb, score, num_groups, topk_groups, group_top,
+          topk, int(renormalize), scale, pm, pi, pw)
     return topk_ids, weights
 
 
@@ -166,13 +191,14 @@ def mx_moe_route_bwd(d_weights: torch.Tensor, logits: torch.Tensor, topk_ids: to
     tokens, experts = logits.shape
     topk = topk_ids.shape[1]
     dev = d_weights.device
-    if d_logits is None:
-        d_logits = torch.empty((tokens, experts), dtype=logits.dtype, device=dev)
-    x, ld = _rows(logits, "logits", dev, tokens, experts, _one_of(logits, "logits", _LOGITS))
-    d, ld_d = _rows(d_logits, "d_logits", dev, tokens, experts, logits.dtype)
-    _call("mx_moe_route_bwd", dev, x, _LOGITS[logits.dtype], tokens, experts, ld, _score(score), topk, int(renormalize),
-          scale, _at(topk_ids, "topk_ids", dev, torch.int32, (tokens, topk)),
-          _at(d_weights, "d_weights", dev, torch.float32, (tokens, topk)), d, ld_d)
+    dtype = _one_of(logits, "logits", _LOGITS)
+    x, ld = _rows(logits, "logits", dev, tokens, experts, dtype)
+    pi = _at(topk_ids, "topk_ids", dev, torch.int32, (tokens, topk))
+    pw = _at(d_weights, "d_weights", dev, torch.float32, (tokens, topk))
+    score = _score(score)
+    d_logits, d, ld_d = _out_rows(d_logits, "d_logits", dev, tokens, experts, dtype)
+    _call("mx_moe_route_bwd", dev, x, _LOGITS[dtype], tokens, experts, ld, score, topk, int(renormalize), scale, pi, pw,
+          d, ld_d)
     return d_logits
 
 
@@ -190,21 +216,22 @@ def mx_moe_combine_bwd(d_out: torch.Tensor, y: Optional[torch.Tensor], slot: tor
     n = tokens * topk
     dev = d_out.device
     bf = torch.bfloat16
-    if want_dy and dy is None:
-        dy = torch.zeros((n, hidden), dtype=bf, device=dev)
-    if want_d_weights and d_weights is None:
-        d_weights = torch.empty((tokens, topk), dtype=torch.float32, device=dev)
     if want_d_weights and y is None:
         raise ValueError("d_weights needs y")
     o, ld_o = _rows(d_out, "d_out", dev, tokens, hidden, bf)
     py, ld_y = _rows(y, "y", dev, n, hidden, bf) if want_d_weights else (None, 0)
-    pd, ld_dy = _rows(dy, "dy", dev, n, hidden, bf) if want_dy else (None, 0)
-    if tuple(slot.shape) not in ((n,), (tokens, topk)):
+    if slot.shape != (n,) and slot.shape != (tokens, topk):
         raise ValueError(f"slot must hold {n} entries, got {list(slot.shape)}")
-    _call("mx_moe_combine_bwd", dev, o, tokens, hidden, ld_o, py, ld_y,
-          _at(slot, "slot", dev, torch.int32, tuple(slot.shape)),
-          _at(weights, "weights", dev, torch.float32, (tokens, topk)), topk, pd, ld_dy,
-          _at(d_weights, "d_weights", dev, torch.float32, (tokens, topk)) if want_d_weights else None)
+    ps = _at(slot, "slot", dev, torch.int32, slot.shape)
+    pw = _at(weights, "weights", dev, torch.float32, (tokens, topk))
+    pd, ld_dy, pg = None, 0, None
+    if want_dy:
+        if dy is None:
+            dy = torch.zeros((n, hidden), dtype=bf, device=dev)
+        pd, ld_dy = _rows(dy, "dy", dev, n, hidden, bf)
+    if want_d_weights:
+        d_weights, pg = _out_at(d_weights, "d_weights", dev, torch.float32, tokens, topk)
+    _call("mx_moe_combine_bwd", dev, o, tokens, hidden, ld_o, py, ld_y, ps, pw, topk, pd, ld_dy, pg)
     return dy if want_dy else None, d_weights if want_d_weights else None
 
 
@@ -225,8 +252,11 @@ def _scale_bytes(rows: int, cols: int, tiles: int) -> int:
 
 def _scales(s: Optional[torch.Tensor], rows: int, cols: int, tiles: int, name: str, dev):
     """(tensor, pointer) of rearranged scales to write (a new buffer if None)."""
-    if s is None:
+    if s is None and tiles >= cols // 256:
         s = torch.empty(max((rows + 31) // 32 * tiles * 256, 1), dtype=_U8, device=dev)
+        return s, s.data_ptr()
+    if s is None:
+        raise ValueError(f"s_tiles={tiles} is less than the {cols // 256} tiles of a row")
     return s, _scale_ptr(s, name, dev, _scale_bytes(rows, cols, tiles))
 
 
@@ -237,13 +267,11 @@ def mx_quantize_rowwise_fp4(x: torch.Tensor, q: Optional[torch.Tensor] = None, s
     s_swz: its scales in the products' layout)."""
     rows, cols = x.shape
     dev = x.device
-    if q is None:
-        q = torch.empty((rows, cols // 2), dtype=_U8, device=dev)
+    px, ld_x = _rows(x, "x", dev, rows, cols, torch.bfloat16)
     if s_tiles is None:
         s_tiles = cols // 256
+    q, pq, ld_q = _out_rows(q, "q", dev, rows, cols // 2, _U8)
     s_swz, ps = _scales(s_swz, rows, cols, s_tiles, "s_swz", dev)
-    px, ld_x = _rows(x, "x", dev, rows, cols, torch.bfloat16)
-    pq, ld_q = _rows(q, "q", dev, rows, cols // 2, _U8)
     _call("mx_quantize_rowwise_fp4", dev, px, rows, cols, ld_x, pq, ld_q, ps, s_tiles)
     return q, s_swz
 
@@ -286,13 +314,11 @@ def mx_dequantize_fp4(q: torch.Tensor, s_swz: torch.Tensor, y: Optional[torch.Te
     rows, half = q.shape
     cols = 2 * half
     dev = q.device
-    if y is None:
-        y = torch.empty((rows, cols), dtype=out_dtype, device=dev)
     if s_tiles is None:
         s_tiles = cols // 256
     pq, ld_q = _rows(q, "q", dev, rows, half, _U8)
-    py, ld_y = _rows(y, "y", dev, rows, cols, _one_of(y, "y", _OUT))
     ps = _scale_ptr(s_swz, "s_swz", dev, _scale_bytes(rows, cols, s_tiles))
+    y, py, ld_y = _out_rows(y, "y", dev, rows, cols, _out_dtype(y, "y", out_dtype))
     _call("mx_dequantize_fp4", dev, pq, rows, cols, ld_q, ps, s_tiles, py, ld_y, _OUT[y.dtype])
     return y
 
@@ -388,17 +414,18 @@ def mx_gemm_fp4(a_q: torch.Tensor, a_s_swz: torch.Tensor, b_q: torch.Tensor, b_s
     M, half = a_q.shape
     N, K = b_q.shape[0], 2 * half
     dev = a_q.device
-    if c is None:
-        c = torch.empty((M, N), dtype=out_dtype, device=dev)
     pa, ld_a = _rows(a_q, "a_q", dev, M, half, _U8)
     pb, ld_b = _rows(b_q, "b_q", dev, N, half, _U8)
-    pc, ld_c = _rows(c, "c", dev, M, N, _one_of(c, "c", _OUT))
+    pas = _scale_ptr(a_s_swz, "a_s_swz", dev, _scale_bytes(M, K, K // 256))
+    pbs = _scale_ptr(b_s_swz, "b_s_swz", dev, _scale_bytes(N, K, K // 256))
+    dtype = _out_dtype(c, "c", out_dtype)
+    c, pc, ld_c = _out_rows(c, "c", dev, M, N, dtype)
     if workspace is None:
-        need = _gemm_workspace(dev.index, M, N, K, c.dtype)
+        need = _gemm_workspace(dev.index, M, N, K, dtype)
         if need:
             workspace = torch.empty(need, dtype=_U8, device=dev)
-    _call("mx_gemm_fp4", dev, M, N, K, pa, ld_a, _scale_ptr(a_s_swz, "a_s_swz", dev, _scale_bytes(M, K, K // 256)), pb, ld_b,
-          _scale_ptr(b_s_swz, "b_s_swz", dev, _scale_bytes(N, K, K // 256)), pc, ld_c, _OUT[c.dtype], *_scratch(workspace, dev))
+    pw, nw = _scratch(workspace, dev)
+    _call("mx_gemm_fp4", dev, M, N, K, pa, ld_a, pas, pb, ld_b, pbs, pc, ld_c, _OUT[dtype], pw, nw)
     return c
 
 
@@ -412,11 +439,12 @@ def mx_grouped_gemm_fp4(group_offsets: torch.Tensor, a_q: torch.Tensor, a_s_swz:
     G, N, _ = b_q.shape
     K = 2 * half
     dev = group_offsets.device
-    if c is None:
-        c = torch.empty((M, N), dtype=out_dtype, device=dev)
+    po = _at(group_offsets, "group_offsets", dev, torch.int64, (G + 1,))
     pa, ld_a = _rows(a_q, "a_q", dev, M, half, _U8)
-    pc, ld_c = _rows(c, "c", dev, M, N, _one_of(c, "c", _OUT))
-    _call("mx_grouped_gemm_fp4", dev, G, M, N, K, _at(group_offsets, "group_offsets", dev, torch.int64, (G + 1,)),
-          pa, ld_a, _scale_ptr(a_s_swz, "a_s_swz", dev, _scale_bytes(M, K, K // 256)), _at(b_q, "b_q", dev, _U8, (G, N, half)),
-          _scale_ptr(b_s_swz, "b_s_swz", dev, G * ((N + 31) // 32) * K), pc, ld_c, _OUT[c.dtype])
+    pas = _scale_ptr(a_s_swz, "a_s_swz", dev, _scale_bytes(M, K, K // 256))
+    pb = _at(b_q, "b_q", dev, _U8, (G, N, half))
+    pbs = _scale_ptr(b_s_swz, "b_s_swz", dev, G * ((N + 31) // 32) * K)
+    dtype = _out_dtype(c, "c", out_dtype)
+    c, pc, ld_c = _out_rows(c, "c", dev, M, N, dtype)
+    _call("mx_grouped_gemm_fp4", dev, G, M, N, K, po, pa, ld_a, pas, pb, pbs, pc, ld_c, _OUT[dtype])
     return c

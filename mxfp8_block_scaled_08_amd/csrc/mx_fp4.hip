@@ -8,7 +8,7 @@
 // here move far more bytes than they compute on: 2 bytes in and 17/32 out an
 // element, so they are bound by HBM.  One MI355X, where a plain copy moves 5.0
 // TB/s: rows of 163840x2048 in 149 us (5.7 TB/s), 128 experts' columns of
-// 1536x2048 in 176 us (5.8), back to BF16 173 us (5.9), rows to FP32 210 us (7.2),
+// 1536x2048 in 168 us (6.1), back to BF16 173 us (5.9), rows to FP32 210 us (7.2),
 // SwiGLU of 163840x768 121 us (4.7), dispatch of 20480 tokens, top 8, of 2048 85
 // us (the MXFP8 one 113).
 #include "mx_device.h"
@@ -97,7 +97,10 @@ hipError_t launch_quantize_rowwise_fp4(const void *x, int64_t rows, int64_t cols
 // 128-byte line of each row).  Thread (b, p) reads rows 32b .. +31 of columns
 // 2p, 2p + 1: two blocks.  The codes cross LDS so that each output row is
 // stored as whole 128-byte lines (256 rows = 128 bytes), and the scales as the
-// two 256-byte tiles they fill.
+// two 256-byte tiles they fill.  x is read once, past the caches (read through
+// them 191 us instead of 168); the codes are what the next call reads, so they
+// go through them: with non-temporal stores the quantizer itself took 176 us and
+// with a reader behind it 416 instead of 366.
 __global__ __launch_bounds__(256) void quantize_colwise_fp4_kernel(const uint16_t *__restrict__ x, int64_t ld_x,
                                                                    int64_t rows, int64_t cols,
                                                                    uint8_t *__restrict__ qt, int64_t ld_qt,
@@ -145,8 +148,8 @@ __global__ __launch_bounds__(256) void quantize_colwise_fp4_kernel(const uint16_
         for (int k = 0; k < 2; k++) {
             const int col = k * 32 + (tid >> 3), c = tid & 7;
             if (col < nc)
-                st_stream(qt + (i * cols + c0 + col) * ld_qt + rt * 128 + c * 16,
-                          *reinterpret_cast<const uint4 *>(codes[col][(c + (col >> 1)) & 7]));
+                *reinterpret_cast<uint4 *>(qt + (i * cols + c0 + col) * ld_qt + rt * 128 + c * 16) =
+                    *reinterpret_cast<const uint4 *>(codes[col][(c + (col >> 1)) & 7]);
         }
         if (tid < 128 && (tid >> 6) * 32 < nc) {
             const int64_t crow = (i * cols + c0) / 32 + (tid >> 6);

@@ -806,7 +806,7 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
         // ---- split-tail unit (BF16 C, whole-width tiles only): its FP32
         // partial tile goes to its workspace slot, lane-major per sub-tile
         // and register group (64 lanes x 16 bytes per store, whole lines,
-        // non-temporal: nothing here reads it back)
+        // non-temporal; the default policy is within 2 % either way)
         const bool split_unit = SPLIT && cur.sp >= 0;
         if (split_unit) {
             const __amdgpu_buffer_rsrc_t rw = byte_range(p.ws, (uint32_t)(p.split_tiles * p.split_s) *

@@ -257,8 +257,12 @@ template <bool GROUPED, int CT, bool SPLIT, int TM, int TN>
 __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_kernel(Gemm4Params p)
 {
     constexpr int NW = 4;                        // waves, 2x2 over the tile
+    // An expert's last tile with at most half its rows: the matrix cores work on
+    // that half alone.  128 experts, Zipf loads of 163840 rows, N 1536, K 2048:
+    // 352 us against 361; even loads gain less.
+    constexpr bool HALVES = GROUPED && TM == 4;
     constexpr int BM = 64 * TM, BN = 64 * TN;    // the workgroup's tile
-    constexpr int WM = 32 * TM, WN = 32 * TN;    // a wave's rows and columns of it
+    constexpr int WN = 32 * TN;                  // a wave's columns of it; its rows are 64i + 32wm .. +31, i < TM
     constexpr int A_STAGE = BM * BK, B_STAGE = BN * BK;  // LDS bytes of one stage
     __shared__ __attribute__((aligned(1024))) uint8_t sA[NBUF][A_STAGE];
     __shared__ __attribute__((aligned(1024))) uint8_t sB[NBUF][B_STAGE];
@@ -432,9 +436,10 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
     // the permutation, so one offset register serves all eight
     // instructions); a half-wave's 32 lanes then cover 8 rows x 4 slots,
     // every 16-lane service group distinct 16-byte bank slots.  Rows past
-    // the operand (or past the expert, which are never stored) need no clamp:
-    // the tile's buffer range ends at the operand's last row and reads beyond
-    // it return zero.
+    // the operand or past the expert, which are never stored, need no clamp:
+    // the tile's buffer range ends at the last row and reads beyond it return
+    // zero without a memory access (reading on into the next expert's rows, as
+    // at first, cost the grouped products 3 %).
     constexpr int QA = BM / 32, QB = BN / 32, PAIR_LOADS = QA + QB;  // per wave: of A, of B
     const int prow = 8 * wave + ((lane & 31) >> 2);
     const int pchunk = (lane & 3) + 4 * (lane >> 5);
@@ -449,7 +454,7 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
     // branch-free.  (32-bit sizes: row counts are below 2^29; a 64-bit
     // compare would need a vector register for a uniform value.)
     auto pair_load_one = [&](const Tile &T, int st, bool live, v4i *R, int q) {
-        const uint32_t ab = (uint32_t)min((int)(p.M - T.m0), BM) * (uint32_t)p.ld_a;
+        const uint32_t ab = (uint32_t)min(T.m_end - T.m0, BM) * (uint32_t)p.ld_a;
         const uint32_t bb = (uint32_t)min((int)(N - T.n0), BN) * (uint32_t)p.ld_b;
         const uint32_t koff = (uint32_t)(T.kb + st) * BK;
         if (q < QA)
@@ -472,7 +477,7 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
     };
 
     // ---- scale words.  Per 256-K (two stages) the lane (h, r) supplies, for A
-    // sub-tile i, the word of row m0 + wm*WM + 32i + r: entry 32h + (row &
+    // sub-tile i, the word of row m0 + 64i + 32wm + r: entry 32h + (row &
     // 31) of the row's 32-row scale tile, whose 256-K group s sits at s * 256
     // within the tile's KT * 256 bytes (likewise for B).  Each is one 4-byte
     // load into a register, three stages ahead.  Rows past the operand fall
@@ -480,11 +485,11 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
     // read zero (2^-127), which times the zero codes there is zero.
     const uint32_t stile = (uint32_t)KT * 256;  // bytes per 32-row scale tile (below 2^32)
     struct ScaleLanes {
-        uint32_t a, b;  // the lane's offsets for sub-tile 0 (sub-tile i adds i * stile)
+        uint32_t a, b;  // the lane's offsets for sub-tile 0 (sub-tile i adds 2i * stile, i * stile)
     };
     auto scale_lanes = [&](const Tile &T) -> ScaleLanes {
         const int x = (int)(T.m0 & 31) + r32;
-        const int ta = (int)(T.m0 >> 5) + wm * TM + (x >> 5), tb = (int)(T.n0 >> 5) + wn * TN;
+        const int ta = (int)(T.m0 >> 5) + wm + (x >> 5), tb = (int)(T.n0 >> 5) + wn * TN;
         return ScaleLanes{(uint32_t)ta * stile + (uint32_t)((h * 32 + (x & 31)) * 4),
                           (uint32_t)tb * stile + (uint32_t)((h * 32 + r32) * 4)};
     };
@@ -498,7 +503,7 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
         const uint32_t kw = __builtin_amdgcn_readfirstlane((uint32_t)group * 256);
 #pragma unroll
         for (int i = 0; i < TM; i++)
-            xa[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rsa, S.a + (uint32_t)i * stile, kw, 0);
+            xa[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rsa, S.a + (uint32_t)(2 * i) * stile, kw, 0);
 #pragma unroll
         for (int i = 0; i < TN; i++)
             xb[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rsb, S.b + (uint32_t)i * stile, kw, 0);
@@ -507,16 +512,16 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
 
     // ---- per-lane LDS read offsets of the matrix-core fragments.  Of its
     // row's 64 bytes (four blocks) the lane needs chunk h, its block of the
-    // stage's first step, and chunk 2 + h, that of the second.  Rows of the sub-tiles are 32 apart,
+    // stage's first step, and chunk 2 + h, that of the second.  Rows of the sub-tiles are 64 (A) or 32 apart,
     // which leaves chunk_perm unchanged, and chunk 2 + h sits in the slot of
     // chunk h XOR 2, so the second read is at the first offset XOR 32.  The
     // sub-tile and the ring buffer are immediate offsets of the LDS read.
-    const uint32_t a_lo = (uint32_t)((wm * WM + r32) * BK + ((h ^ chunk_perm(r32)) * 16));
+    const uint32_t a_lo = (uint32_t)((wm * 32 + r32) * BK + ((h ^ chunk_perm(r32)) * 16));
     const uint32_t b_lo = (uint32_t)((wn * WN + r32) * BK + ((h ^ chunk_perm(r32)) * 16));
     const uint32_t a_hi = a_lo ^ 32u, b_hi = b_lo ^ 32u;
-    // A sub-tile i (rows wm*WM + 32i ..) and B sub-tile i of ring buffer buf
+    // A sub-tile i (rows 64i + 32wm ..) and B sub-tile i of ring buffer buf
     auto read_a = [&](int buf, int i) -> v8i {
-        const uint8_t *A_ = &sA[buf][0] + i * 32 * BK;
+        const uint8_t *A_ = &sA[buf][0] + i * 64 * BK;
         const v4i lo = *reinterpret_cast<const v4i *>(A_ + a_lo);
         const v4i hi = *reinterpret_cast<const v4i *>(A_ + a_hi);
         return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -537,13 +542,13 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
             for (int v = 0; v < 16; v++)
                 acc[i][j][v] = 0.0f;
 
-    // Per-lane offset of C within a tile for band j = 0: row wm*WM + r32,
+    // Per-lane offset of C within a tile for band j = 0: row 32wm + r32,
     // columns from wn*WN + 4h.  Band j adds j * c_band, wave-uniform (the
     // sub-tile and register group add immediates), so one register serves
     // every band.  The row offsets stay in the vector offset, which the
     // buffer range check covers (the scalar offset is added after it).
     constexpr int CE = CT == 0 ? 2 : 4;  // bytes per C element
-    const uint32_t c_band = (uint32_t)(32 * p.ld_c * CE);
+    const uint32_t c_band = (uint32_t)(64 * p.ld_c * CE);
     // BF16 C is stored after three lane exchanges (see the epilogue): lane l
     // writes 8 columns, chunk k = ((l >> 5) & 1) | (((l >> 4) & 1) << 1) of
     // sub-tile pair half (l >> 3) & 1, of row l & 7 of an 8-row quarter of the
@@ -551,11 +556,11 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
     // offsets too).
     uint32_t c_off;
     if (CT == 0) {
-        const int row = wm * WM + (lane & 7);
+        const int row = wm * 32 + (lane & 7);
         const int col = wn * WN + ((lane >> 3) & 1) * 32 + (((lane >> 5) & 1) | (((lane >> 4) & 1) << 1)) * 8;
         c_off = (uint32_t)((row * p.ld_c + col) * CE);
     } else {
-        c_off = (uint32_t)(((wm * WM + r32) * p.ld_c + wn * WN + 4 * h) * CE);
+        c_off = (uint32_t)(((wm * 32 + r32) * p.ld_c + wn * WN + 4 * h) * CE);
     }
 
     // ---- the workgroup's stages: its units' stages numbered continuously,
@@ -702,7 +707,8 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
         // nxt: the unit after this one (loaded during this unit's last group)
         const ScaleLanes nxt_sl = scale_lanes(nxt);
         const int ng = cur.ns >> 2;  // 512-K groups of this unit
-        auto group = [&](int gi) {
+        auto group = [&](int gi, auto H_) {
+            constexpr int TH = decltype(H_)::value;  // A sub-tiles with valid rows (at most)
             // the next group: of this unit, or the next unit's first (every
             // unit has at least one); it exists when it is in this unit or a
             // next unit exists
@@ -726,16 +732,19 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
                 // Per B sub-tile i: read B sub-tile i + 1 (or the next
                 // stage's first) and the next stage's A sub-tile i, then at
                 // even t its share of the pair writes and loads, while the
-                // 2 TM matrix-core instructions of row i run.  LDS writes and
+                // 2 TH matrix-core instructions of row i run.  LDS writes and
                 // reads stay in program order (the compiler cannot tell the
-                // ring buffers apart), so reads come first in each row.
+                // ring buffers apart), so reads come first in each row.  (Of
+                // half a tile too the last stage reads every A sub-tile: the
+                // next stage may be the next tile's.)
                 v8i xb = fb_first;
 #pragma unroll
                 for (int i = 0; i < TN; i++) {
                     const v8i xn = i + 1 < TN ? read_b(t, i + 1) : read_b(nbuf, 0);
 #pragma unroll
                     for (int a = i * TM / TN; a < (i + 1) * TM / TN; a++)
-                        NA[a] = read_a(nbuf, a);
+                        if (a < TH || t == 3)
+                            NA[a] = read_a(nbuf, a);
                     if (pairs) {
 #pragma unroll
                         for (int q = i * PAIR_LOADS / TN; q < (i + 1) * PAIR_LOADS / TN; q++) {
@@ -747,7 +756,7 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
                     auto step = [&](auto S_) {
                         constexpr int s = decltype(S_)::value, byte = 2 * (t & 1) + s;
 #pragma unroll
-                        for (int j = 0; j < TM; j++)
+                        for (int j = 0; j < TH; j++)
                             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
                                 half_of(xb, s), half_of(FA[j], s), acc[i][j], FMT_E2M1, FMT_E2M1, byte, (int)wb[i],
                                 byte, (int)wa[j]);
@@ -759,11 +768,11 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
                 fb_first = xb;
 #pragma unroll
                 for (int i = 0; i < TN; i++) {
-                    // per row: 2 TM matrix-core instructions between the LDS
+                    // per row: 2 TH matrix-core instructions between the LDS
                     // reads and, at even t, the pair's writes and loads
-                    constexpr int NQ = PAIR_LOADS / TN, REST = 2 * TM * 3 / 4 / (NQ - 1);
+                    constexpr int NQ = PAIR_LOADS / TN, REST = 2 * TH * 3 / 4 / (NQ - 1);
                     __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x008, 2 * TM / 4, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, 2 * TH / 4, 0);
                     __builtin_amdgcn_sched_group_barrier(0x100, 2 * TM / TN, 0);
                     if (t & 1)
                         __builtin_amdgcn_sched_group_barrier(0x020, (TM + TN) / TN, 0);  // scale words
@@ -794,8 +803,12 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
             stage(std::integral_constant<int, 2>{});
             stage(std::integral_constant<int, 3>{});
         };
-        for (int gi = 0; gi < ng; gi++)
-            group(gi);
+        if (HALVES && cur.m_end - cur.m0 <= BM / 2)
+            for (int gi = 0; gi < ng; gi++)
+                group(gi, std::integral_constant<int, TM / 2>{});
+        else
+            for (int gi = 0; gi < ng; gi++)
+                group(gi, std::integral_constant<int, TM>{});
         // the unit after the next one
         bool nxt2_ok = false;
         Tile nxt2 = nxt;
@@ -879,7 +892,7 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
             for (int i = 0; i < TN; i++) {
 #pragma unroll
                 for (int j = 0; j < TM; j++) {
-                    const int64_t m = cur.m0 + wm * WM + j * 32 + r32;
+                    const int64_t m = cur.m0 + wm * 32 + j * 64 + r32;
                     if (m < cur.m_end) {
 #pragma unroll
                         for (int q = 0; q < 4; q++) {
@@ -929,7 +942,7 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
 // Sums of the split tiles: thread t of a tile's takes float4 t of its slots
 // (the partial-tile layout above: wave, sub-tile (i, j), register group q,
 // lane), adds the split_s slots in range order and writes the four BF16 of C
-// they hold: row wm*WM + 32j + (lane & 31), columns wn*WN + 32i + 8q +
+// they hold: row 64j + 32wm + (lane & 31), columns wn*WN + 32i + 8q +
 // 4(lane >> 5) .. +3.
 template <int TM, int TN>
 __global__ __launch_bounds__(256) void split4_reduce_kernel(Gemm4Params p)
@@ -945,7 +958,7 @@ __global__ __launch_bounds__(256) void split4_reduce_kernel(Gemm4Params p)
     const int wave = t / PER_WAVE, idx = (t % PER_WAVE) >> 6, lane = t & 63;
     const int q = idx & 3, j = (idx >> 2) % TM, i = idx / (4 * TM);
     static_assert(PER_WAVE / 64 == TN * TM * 4, "one float4 per lane per (sub-tile, group)");
-    const int row = (wave & 1) * (32 * TM) + j * 32 + (lane & 31);
+    const int row = (wave & 1) * 32 + j * 64 + (lane & 31);
     const int col = (wave >> 1) * (32 * TN) + i * 32 + 8 * q + 4 * (lane >> 5);
     // tile dp_tiles + r: the kernel's tile order (GROUP_M tile-rows at a time)
     const int64_t pid = p.dp_tiles + r;

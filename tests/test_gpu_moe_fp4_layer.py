@@ -77,6 +77,8 @@ def test_products_cut_every_way(gpu_lib, M, N, K, split):
     ([0, 0, 1, 0], 200, 256), ([16] * 4, 48, 768),
     ([300, 0, 17, 129, 1, 128, 127, 90], 1000, 512),  # 128 x 128 tiles
     ([700, 300, 0, 513], 520, 1024),                  # 256 x 256
+    ([384, 385, 383, 641, 256, 513, 1025, 320], 776, 768),   # and tails of every kind: whole, half or less
+    ([128, 900, 1, 1152, 127, 0, 129, 500], 256, 256), ([2000, 64, 65, 63], 512, 1280),
     ([0] * 1023 + [5], 64, 256)])
 def test_grouped_products_cut_every_way(gpu_lib, rows, N, K):
     mx = gpu_lib

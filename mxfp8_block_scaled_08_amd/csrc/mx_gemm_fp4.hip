@@ -1198,8 +1198,9 @@ hipError_t launch_grouped_gemm_fp4(int64_t G, int64_t M_total, int64_t N, int64_
     p.vec_store = vec_ok(c, ld_c, c_dtype);
     p.vec16 = gemm_vec16(c, ld_c, c_dtype);
     // 128 x 128 tiles up to 256 rows an expert, larger ones above: 64 rows an
-    // expert (128 experts, N 1536, K 2048) 43 us against 60 by 256 x 256 tiles,
-    // 256 rows 92 against 100, 512 rows 178 against 160.
+    // expert (128 experts, N 1536, K 2048) 47 us against 52 by 256 x 256 tiles,
+    // 256 rows 96 against 96, 512 rows 180 against 158; at N 2048, K 768 31
+    // against 39, 74 against 75, 128 against 122.
     return M_total <= 256 * G ? launch_group_tiles_t<2, 2>(p, c_dtype, stream)
                               : launch_group_tiles_t<4, 4>(p, c_dtype, stream);
 }

@@ -10,7 +10,9 @@ The operations are those of the MXFP8 learner/sampler hot path in
 "End-to-End MXFP8 Reinforcement Learning on Blackwell" (Figure 1: quantize
 the weights with the learner's quantizer, MXFP8 GEMMs; Table 6: GEMM,
 quantization and scale-rearrangement kernels; Table 2: dense Qwen3-8B and
-the 128-expert Qwen3-30B-A3B MoE).
+the 128-expert Qwen3-30B-A3B MoE).  ``moe_fp4.py`` holds the second part's
+functions (``include/mxfp8_moe_fp4.h``: routing to experts and its gradient,
+the combine's gradient, MXFP4), which are exported here with the others.
 """
 from __future__ import annotations
 

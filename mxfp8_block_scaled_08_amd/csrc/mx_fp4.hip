@@ -7,10 +7,10 @@
 // divides by 2^(e-127), rounds to nearest even and saturates at 6.  All passes
 // here move far more bytes than they compute on: 2 bytes in and 17/32 out an
 // element, so they are bound by HBM.  One MI355X, where a plain copy moves 5.0
-// TB/s: rows of 163840x2048 in 149 us (5.7 TB/s), 128 experts' columns of
-// 1536x2048 in 168 us (6.1), back to BF16 173 us (5.9), rows to FP32 210 us (7.2),
-// SwiGLU of 163840x768 121 us (4.7), dispatch of 20480 tokens, top 8, of 2048 85
-// us (the MXFP8 one 113).
+// TB/s: rows of 163840x2048 in 145 us (5.9 TB/s), back to BF16 137 us (6.2), to
+// FP32 224 us (6.8); 128 experts' columns of 1536x2048 164 us (6.2); SwiGLU of
+// 163840x768 113 us (5.1); dispatch of 20480 tokens, top 8, of 2048 85 us (the
+// MXFP8 one 112).
 #include "mx_device.h"
 #include "mx_launch.h"
 
@@ -64,16 +64,46 @@ __device__ __forceinline__ int64_t swz_at(int64_t row, int64_t b, int64_t kt)
     return ((row >> 5) * kt + (b >> 3)) * 256 + (32 * (b & 1) + (row & 31)) * 4 + ((b & 7) >> 1);
 }
 
-// Unit u = 8 consecutive elements of row u / upr; four lanes make a block.
+// A launch's units (16 bytes of a row each), `per` of them a row.  m = ceil(2^64 /
+// per): u * m / 2^64 exceeds u / per by less than u / 2^64 < 1 / per, so its whole
+// part is the quotient.  (64-bit divisions, whose fast path is a 32-bit one, cost
+// the row-wise passes 4 to 8 %.)
+struct UnitRows {
+    uint64_t m;
+    uint32_t units, per;
+    __device__ __forceinline__ uint32_t row(uint32_t u) const
+    {
+        const uint64_t lo = (uint64_t)(uint32_t)m * u;
+        return (uint32_t)(((m >> 32) * u + (lo >> 32)) >> 32);
+    }
+};
+
+// The rows in runs of whole 32-row tiles and at most 2^31 units, each a launch:
+// f(first row, units, grid).
+template <typename F> static hipError_t by_rows(int64_t rows, int64_t per, F f)
+{
+    const int64_t run = (((int64_t)1 << 31) / per) & ~(int64_t)31;
+    for (int64_t r0 = 0; r0 < rows; r0 += run) {
+        const int64_t units = std::min(run, rows - r0) * per;
+        const UnitRows u{~(uint64_t)0 / (uint64_t)per + 1, (uint32_t)units, (uint32_t)per};
+        f(r0, u, dim3((unsigned)std::min<int64_t>((units + 255) / 256, 65536)));
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess)
+            return err;
+    }
+    return hipSuccess;
+}
+
+// Unit u = 8 consecutive elements of a row; four lanes make a block.
 __global__ __launch_bounds__(256) void quantize_rowwise_fp4_kernel(const uint16_t *__restrict__ x, int64_t ld_x,
                                                                    uint8_t *__restrict__ q, int64_t ld_q,
                                                                    uint8_t *__restrict__ s_swz, int64_t s_tiles,
-                                                                   int64_t units, uint32_t upr)
+                                                                   UnitRows n)
 {
-    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
-        // (units is a multiple of 32, so a quad is live or not as one)
-        const int64_t row = u / upr;
-        const int64_t cu = u - row * upr;
+    for (uint32_t u = blockIdx.x * 256 + threadIdx.x; u < n.units; u += gridDim.x * 256) {
+        // (a row's units are a multiple of 32, so a quad is live or not as one)
+        const int64_t row = n.row(u);
+        const uint32_t cu = u - (uint32_t)row * n.per;
         const uint4 w = ld_stream(x + row * ld_x + cu * 8);
         const uint32_t c = scale_code4(quad_amax(w));
         *reinterpret_cast<uint32_t *>(q + row * ld_q + cu * 4) = fp4_codes(w, c);
@@ -85,12 +115,11 @@ __global__ __launch_bounds__(256) void quantize_rowwise_fp4_kernel(const uint16_
 hipError_t launch_quantize_rowwise_fp4(const void *x, int64_t rows, int64_t cols, int64_t ld_x, void *q, int64_t ld_q,
                                        void *s_swz, int64_t s_tiles, hipStream_t stream)
 {
-    const uint32_t upr = (uint32_t)(cols / 8);
-    const int64_t units = rows * upr;
-    const int64_t blocks = std::min<int64_t>((units + 255) / 256, 65536);
-    hipLaunchKernelGGL(quantize_rowwise_fp4_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, (const uint16_t *)x,
-                       ld_x, (uint8_t *)q, ld_q, (uint8_t *)s_swz, s_tiles, units, upr);
-    return hipGetLastError();
+    return by_rows(rows, cols / 8, [&](int64_t r0, UnitRows n, dim3 grid) {
+        hipLaunchKernelGGL(quantize_rowwise_fp4_kernel, grid, dim3(256), 0, stream, (const uint16_t *)x + r0 * ld_x,
+                           ld_x, (uint8_t *)q + r0 * ld_q, ld_q, (uint8_t *)s_swz + r0 / 32 * s_tiles * 256, s_tiles,
+                           n);
+    });
 }
 
 // Column-wise: a workgroup takes 256 rows x 64 columns of one tensor (one
@@ -189,21 +218,20 @@ __device__ __forceinline__ float e8m0_f32(uint32_t c)
 }
 
 // Unit u = the 16 output bytes of 8 (BF16) or 4 (FP32) consecutive elements of
-// row u / upr, so that a wave's stores are whole lines (with 8 FP32 a lane, two
+// a row, so that a wave's stores are whole lines (with 8 FP32 a lane, two
 // stores 32 bytes apart, 163840 x 2048 took 554 us).
 template <int DT>
 __global__ __launch_bounds__(256) void dequantize_fp4_kernel(const uint8_t *__restrict__ q, int64_t ld_q,
                                                              const uint8_t *__restrict__ s_swz, int64_t s_tiles,
-                                                             void *__restrict__ y, int64_t ld_y, int64_t units,
-                                                             uint32_t upr)
+                                                             void *__restrict__ y, int64_t ld_y, UnitRows n)
 {
     constexpr int N = DT == 0 ? 8 : 4;  // elements a unit
-    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
-        const int64_t row = u / upr;
-        const int64_t cu = u - row * upr;
+    for (uint32_t u = blockIdx.x * 256 + threadIdx.x; u < n.units; u += gridDim.x * 256) {
+        const int64_t row = n.row(u);
+        const uint32_t cu = u - (uint32_t)row * n.per;
         const uint8_t *src = q + row * ld_q + cu * (N / 2);
         const uint32_t w = DT == 0 ? *reinterpret_cast<const uint32_t *>(src) : *reinterpret_cast<const uint16_t *>(src);
-        const float s = e8m0_f32(s_swz[swz_at(row, cu * N / 32, s_tiles)]);
+        const float s = e8m0_f32(s_swz[swz_at(row, cu / (32 / N), s_tiles)]);
         float v[N];
 #pragma unroll
         for (int k = 0; k < N; k++)
@@ -223,16 +251,15 @@ __global__ __launch_bounds__(256) void dequantize_fp4_kernel(const uint8_t *__re
 hipError_t launch_dequantize_fp4(const void *q, int64_t rows, int64_t cols, int64_t ld_q, const void *s_swz,
                                  int64_t s_tiles, void *y, int64_t ld_y, int y_dtype, hipStream_t stream)
 {
-    const uint32_t upr = (uint32_t)(cols / (y_dtype == 0 ? 8 : 4));
-    const int64_t units = rows * upr;
-    const unsigned blocks = (unsigned)std::min<int64_t>((units + 255) / 256, 65536);
-    if (y_dtype == 0)
-        hipLaunchKernelGGL(dequantize_fp4_kernel<0>, dim3(blocks), dim3(256), 0, stream, (const uint8_t *)q, ld_q,
-                           (const uint8_t *)s_swz, s_tiles, y, ld_y, units, upr);
-    else
-        hipLaunchKernelGGL(dequantize_fp4_kernel<1>, dim3(blocks), dim3(256), 0, stream, (const uint8_t *)q, ld_q,
-                           (const uint8_t *)s_swz, s_tiles, y, ld_y, units, upr);
-    return hipGetLastError();
+    const int64_t es = y_dtype == 0 ? 2 : 4;
+    return by_rows(rows, cols * es / 16, [&](int64_t r0, UnitRows n, dim3 grid) {
+        const uint8_t *q0 = (const uint8_t *)q + r0 * ld_q, *s0 = (const uint8_t *)s_swz + r0 / 32 * s_tiles * 256;
+        void *y0 = (uint8_t *)y + r0 * ld_y * es;
+        if (y_dtype == 0)
+            hipLaunchKernelGGL(dequantize_fp4_kernel<0>, grid, dim3(256), 0, stream, q0, ld_q, s0, s_tiles, y0, ld_y, n);
+        else
+            hipLaunchKernelGGL(dequantize_fp4_kernel<1>, grid, dim3(256), 0, stream, q0, ld_q, s0, s_tiles, y0, ld_y, n);
+    });
 }
 
 // Dispatch: token rows quantized once, codes and scale bytes stored to every
@@ -241,12 +268,12 @@ hipError_t launch_dequantize_fp4(const void *q, int64_t rows, int64_t cols, int6
 __global__ __launch_bounds__(256) void moe_scatter_quantize_fp4_kernel(const uint16_t *__restrict__ x, int64_t ld_x,
                                                                        const int32_t *__restrict__ slot, int topk,
                                                                        uint8_t *__restrict__ q, int64_t ld_q,
-                                                                       uint8_t *__restrict__ s_swz, int64_t units,
-                                                                       uint32_t upr, int64_t kt)
+                                                                       uint8_t *__restrict__ s_swz, int64_t kt,
+                                                                       UnitRows n)
 {
-    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
-        const int64_t t = u / upr;
-        const int64_t cu = u - t * upr;
+    for (uint32_t u = blockIdx.x * 256 + threadIdx.x; u < n.units; u += gridDim.x * 256) {
+        const int64_t t = n.row(u);
+        const uint32_t cu = u - (uint32_t)t * n.per;
         const uint4 w = ld_stream(x + t * ld_x + cu * 8);
         const uint32_t c = scale_code4(quad_amax(w));
         const uint32_t o = fp4_codes(w, c);
@@ -267,13 +294,11 @@ hipError_t launch_moe_dispatch_fp4(const void *x, int64_t tokens, int64_t hidden
                                    hipStream_t stream)
 {
     launch_dispatch_order(topk_ids, tokens, topk, experts, offsets, src_token, slot, ws, stream);
-    const uint32_t upr = (uint32_t)(hidden / 8);
-    const int64_t units = tokens * upr;
-    const int64_t blocks = std::min<int64_t>((units + 255) / 256, 65536);
-    hipLaunchKernelGGL(moe_scatter_quantize_fp4_kernel, dim3((unsigned)blocks), dim3(256), 0, stream,
-                       (const uint16_t *)x, ld_x, (const int32_t *)slot, (int)topk, (uint8_t *)q, ld_q,
-                       (uint8_t *)s_swz, units, upr, hidden / 256);
-    return hipGetLastError();
+    return by_rows(tokens, hidden / 8, [&](int64_t t0, UnitRows n, dim3 grid) {
+        hipLaunchKernelGGL(moe_scatter_quantize_fp4_kernel, grid, dim3(256), 0, stream, (const uint16_t *)x + t0 * ld_x,
+                           ld_x, (const int32_t *)slot + t0 * topk, (int)topk, (uint8_t *)q, ld_q, (uint8_t *)s_swz,
+                           hidden / 256, n);
+    });
 }
 
 // SwiGLU with MXFP4 output: h as the MXFP8 form computes it (swiglu_bf16x2),
@@ -281,12 +306,12 @@ hipError_t launch_moe_dispatch_fp4(const void *x, int64_t tokens, int64_t hidden
 __global__ __launch_bounds__(256) void swiglu_quantize_fp4_kernel(const uint16_t *__restrict__ gu, int64_t ld_gu,
                                                                   int64_t F, uint16_t *__restrict__ h, int64_t ld_h,
                                                                   uint8_t *__restrict__ q, int64_t ld_q,
-                                                                  uint8_t *__restrict__ s_swz, int64_t units,
-                                                                  uint32_t upr, int64_t kt)
+                                                                  uint8_t *__restrict__ s_swz, int64_t kt,
+                                                                  UnitRows n)
 {
-    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
-        const int64_t row = u / upr;
-        const int64_t cu = u - row * upr;
+    for (uint32_t u = blockIdx.x * 256 + threadIdx.x; u < n.units; u += gridDim.x * 256) {
+        const int64_t row = n.row(u);
+        const uint32_t cu = u - (uint32_t)row * n.per;
         const uint4 gw = ld_stream(gu + row * ld_gu + cu * 8), uw = ld_stream(gu + row * ld_gu + F + cu * 8);
         const uint4 w = make_uint4(swiglu_bf16x2(gw.x, uw.x), swiglu_bf16x2(gw.y, uw.y), swiglu_bf16x2(gw.z, uw.z),
                                    swiglu_bf16x2(gw.w, uw.w));
@@ -302,12 +327,11 @@ __global__ __launch_bounds__(256) void swiglu_quantize_fp4_kernel(const uint16_t
 hipError_t launch_swiglu_quantize_fp4(const void *gu, int64_t rows, int64_t F, int64_t ld_gu, void *h, int64_t ld_h,
                                       void *q, int64_t ld_q, void *s_swz, hipStream_t stream)
 {
-    const uint32_t upr = (uint32_t)(F / 8);
-    const int64_t units = rows * upr;
-    const int64_t blocks = std::min<int64_t>((units + 255) / 256, 65536);
-    hipLaunchKernelGGL(swiglu_quantize_fp4_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, (const uint16_t *)gu,
-                       ld_gu, F, (uint16_t *)h, ld_h, (uint8_t *)q, ld_q, (uint8_t *)s_swz, units, upr, F / 256);
-    return hipGetLastError();
+    return by_rows(rows, F / 8, [&](int64_t r0, UnitRows n, dim3 grid) {
+        hipLaunchKernelGGL(swiglu_quantize_fp4_kernel, grid, dim3(256), 0, stream, (const uint16_t *)gu + r0 * ld_gu,
+                           ld_gu, F, h ? (uint16_t *)h + r0 * ld_h : nullptr, ld_h, (uint8_t *)q + r0 * ld_q, ld_q,
+                           (uint8_t *)s_swz + r0 / 32 * (F / 256) * 256, F / 256, n);
+    });
 }
 
 }  // namespace mx

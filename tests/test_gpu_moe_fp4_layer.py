@@ -121,6 +121,53 @@ def test_large_buffers(gpu_lib):
     assert torch.equal(x[-5:], mx.mx_dequantize_fp4(q[M // 32 * 32:], s[M // 32 * N:])[-5:])
 
 
+def test_more_rows_than_a_launch_takes(gpu_lib):
+    """More than 2^31 units of 16 bytes: several launches a call.  The last rows
+    and those around the cuts equal the same rows in small calls."""
+    mx = gpu_lib
+    if torch.cuda.mem_get_info()[0] < 150 << 30:
+        pytest.skip("needs 150 GB of free device memory")
+    R, C = (1 << 22) + 40, 4096
+    g = torch.Generator(device=dev)
+    g.manual_seed(6)
+    base = torch.randn(R // 8, 64, generator=g, device=dev).bfloat16()
+    gu = torch.empty(R, 2 * C, dtype=torch.bfloat16, device=dev)
+    gu.view(R // 8, -1, 64).copy_(base[:, None])             # rows 8i .. 8i + 7 repeat 64 values
+    gu[-3:].neg_()
+    tile = lambda s, r, cols: s.view(-1, cols)[r // 32:(r + 32) // 32]  # noqa: E731  (a 32-row tile has cols scale bytes)
+    at = [0, (1 << 22) - 32, 1 << 22]                        # the cut is at row 2^22 (2^21 for FP32 values)
+    q, s, _ = mx.mx_swiglu_quantize_fp4(gu)
+    for r in at:
+        q2, s2, _ = mx.mx_swiglu_quantize_fp4(gu[r:r + 32])
+        assert torch.equal(q[r:r + 32], q2) and torch.equal(tile(s, r, C), s2.view(1, -1))
+    q2, _, _ = mx.mx_swiglu_quantize_fp4(gu[-8:])
+    assert torch.equal(q[-8:], q2)
+    x = gu[:, C:]
+    q, s = mx.mx_quantize_rowwise_fp4(x, q=q, s_swz=s)
+    for r in at:
+        q2, s2 = mx.mx_quantize_rowwise_fp4(x[r:r + 32])
+        assert torch.equal(q[r:r + 32], q2) and torch.equal(tile(s, r, C), s2.view(1, -1))
+    q2, s2 = mx.mx_quantize_rowwise_fp4(x[-8:])
+    assert torch.equal(q[-8:], q2)
+    y = mx.mx_dequantize_fp4(q, s)
+    for r in at:
+        assert torch.equal(y[r:r + 32], mx.mx_dequantize_fp4(q[r:r + 32], tile(s, r, C).reshape(-1)))
+    assert torch.equal(y[-8:], mx.mx_dequantize_fp4(q2, s2))
+    del y
+    half = R // 2 + 36                                       # FP32 values: half the rows are a cut
+    y = mx.mx_dequantize_fp4(q[:half], s, out_dtype=torch.float32)
+    for r in (0, (1 << 21) - 32, 1 << 21):
+        assert torch.equal(y[r:r + 32], mx.mx_dequantize_fp4(q[r:r + 32], tile(s, r, C).reshape(-1), out_dtype=torch.float32))
+    assert torch.equal(y[-8:].bfloat16(), mx.mx_dequantize_fp4(*mx.mx_quantize_rowwise_fp4(x[half - 8:half])))
+    del y
+    ids = torch.zeros(R, 1, dtype=torch.int32, device=dev)   # one expert: the rows keep their order
+    want_q, want_s = q.clone(), s.clone()
+    q.zero_(), s.zero_()
+    _, _, slot, q, s = mx.mx_moe_dispatch_fp4(x, ids, 1, q=q, s_swz=s)
+    assert torch.equal(slot, torch.arange(R, device=dev, dtype=torch.int32))
+    assert torch.equal(q, want_q) and torch.equal(s.view(-1, C)[:-1], want_s.view(-1, C)[:-1])
+
+
 def test_large_expert_rows_and_stacks(gpu_lib):
     """y, dy, a stack of weights and the grouped product's B beyond 2^32 bytes:
     both ends equal the same rows in a small call."""

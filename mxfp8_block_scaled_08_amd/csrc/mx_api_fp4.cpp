@@ -77,7 +77,8 @@ mx_status mx_quantize_colwise_fp4(const void *x, int64_t count, int64_t rows, in
     if (rows == 0 || cols == 0 || count == 0)
         return ok();
     if (oversized(rows, cols, ld_x) || rows >= ((int64_t)1 << 26) || ld_qt >= ((int64_t)1 << 27) ||
-        count >= ((int64_t)1 << 32) / (rows > cols ? rows : cols))
+        count >= ((int64_t)1 << 32) / (rows > cols ? rows : cols) ||
+        rows / 256 * ((cols + 63) / 64) >= ((int64_t)1 << 31) / count)  // (tile numbers are 32-bit)
         return fail(MX_ERR_UNSUPPORTED, "%s: operand too large for this build", fn);
     if (!x || !qt || !st_swz)
         return fail(MX_ERR_INVALID_ARG, "%s: null pointer", fn);

@@ -133,16 +133,17 @@ hipError_t launch_quantize_rowwise_fp4(const void *x, int64_t rows, int64_t cols
 __global__ __launch_bounds__(256) void quantize_colwise_fp4_kernel(const uint16_t *__restrict__ x, int64_t ld_x,
                                                                    int64_t rows, int64_t cols,
                                                                    uint8_t *__restrict__ qt, int64_t ld_qt,
-                                                                   uint8_t *__restrict__ st_swz, int64_t rtiles,
-                                                                   int64_t ctiles, int64_t total)
+                                                                   uint8_t *__restrict__ st_swz, uint32_t rtiles,
+                                                                   uint32_t ctiles, uint32_t total)
 {
     // a column's eight 16-byte blocks, each shifted by the column so that
     // neither the writes (columns 2p apart) nor the reads collide on banks
     __shared__ __attribute__((aligned(16))) uint8_t codes[64][8][16];
     __shared__ __attribute__((aligned(16))) uint8_t scales[512];
     const int tid = threadIdx.x, b = tid >> 5, p = tid & 31;
-    for (int64_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
-        const int64_t rt = tile % rtiles, ct = (tile / rtiles) % ctiles, i = tile / (rtiles * ctiles);
+    for (uint32_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
+        const uint32_t across = tile / rtiles, of = across / ctiles;
+        const int64_t rt = tile - across * rtiles, ct = across - of * ctiles, i = of;
         const int64_t c0 = ct * 64;
         const int nc = (int)min(cols - c0, (int64_t)64);
         uint32_t w[32];
@@ -194,8 +195,8 @@ hipError_t launch_quantize_colwise_fp4(const void *x, int64_t count, int64_t row
 {
     const int64_t rtiles = rows / 256, ctiles = (cols + 63) / 64, total = count * rtiles * ctiles;
     hipLaunchKernelGGL(quantize_colwise_fp4_kernel, dim3((unsigned)std::min<int64_t>(total, 1 << 20)), dim3(256), 0,
-                       stream, (const uint16_t *)x, ld_x, rows, cols, (uint8_t *)qt, ld_qt, (uint8_t *)st_swz, rtiles,
-                       ctiles, total);
+                       stream, (const uint16_t *)x, ld_x, rows, cols, (uint8_t *)qt, ld_qt, (uint8_t *)st_swz,
+                       (uint32_t)rtiles, (uint32_t)ctiles, (uint32_t)total);
     return hipGetLastError();
 }
 

@@ -163,6 +163,7 @@ def test_quantize_refusals():
     r(OVER, qt=A + 32)
     r(OVER, scales=B + 16 * 64)
     r(UNSUP, count=1 << 40)
+    r(UNSUP, rows=1 << 25, cols=1 << 25, ld_x=1 << 25, ld_qt=1 << 24)      # 2^36 tiles
     assert call("mx_quantize_colwise_fp4", col, count=0) == mx.MX_OK
     deq = dict(q=A, rows=4, cols=256, ld_q=128, s=B, tiles=1, y=C, ld_y=256, dt=BF)
     r = lambda st, word="", **kw: refused("mx_dequantize_fp4", deq, st, word, **kw)  # noqa: E731

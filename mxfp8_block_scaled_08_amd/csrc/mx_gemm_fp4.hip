@@ -44,7 +44,7 @@ struct Gemm4Params {
     int64_t G;
     int64_t b_group_stride, bs_group_stride;
     int64_t tiles_m, tiles_n;
-    int ksplit;                   // few rows: waves that share a column tile along K
+    int ks_log, pb_log;  // few rows: log2 of the waves that share a column tile along K, of a workgroup's tiles
     uint32_t as_bytes, bs_bytes;  // rearranged scale bytes of A (all rows) and of one B
     int vec_store;  // C rows allow 4-element vector stores
     int vec16;      // BF16 C: rows allow 16-byte stores (8 elements)
@@ -72,29 +72,31 @@ constexpr int ROWS_CHUNK = 64;  // few rows: rows of one workgroup
 constexpr int FMT_E2M1 = 4;  // the instruction's operand format code
 
 // Few rows.  A wave takes 16 columns of C and a range of 256-K groups, of up to
-// 16 * MT rows at a time; ksplit waves of a workgroup share the columns, each
+// 16 * MT rows at a time; 2^ks_log waves of a workgroup share the columns, each
 // with its own range of K, and their sums meet in LDS, added in K order.  B,
 // which is most of what there is to read, goes straight to registers in the
 // matrix cores' layout, up to MAXG groups (2 KiB each) in flight a wave, and
 // stays there while the rows of A pass, 16 * MT after another; A comes out of
-// L2.  Bound by reading B: one row x 24576x4096 (53 MB) takes 12.4 us, 4.3 TB/s;
-// x 6144x4096 5.0 us, of which an empty launch is 2.4.  With four waves a tile
-// and one group in flight, as at first, x 4096x12288 took 16.7 us instead of 7.4.
+// L2.  Bound by reading B: one row x 24576x4096 (53 MB) takes 12.3 us, 4.4 TB/s;
+// x 6144x4096 4.6 us, of which an empty launch is 2.4.  With four waves a tile
+// and one group in flight, as at first, x 4096x12288 took 16.7 us instead of 7.2;
+// dividing by the split instead of shifting costs 0.2 us before the first load.
 template <bool GROUPED, int CT, int MT, int MAXG>
 __global__ __launch_bounds__(1024) void gemm4_rows_kernel(Gemm4Params p)
 {
     extern __shared__ __attribute__((aligned(16))) float part[];  // [waves][MT][64][4]
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int waves = blockDim.x >> 6, ks = p.ksplit, per_block = waves / ks;
-    const int kp = wave % ks;
+    const int ks = 1 << p.ks_log, per_block = 1 << p.pb_log;
+    const int kp = wave & (ks - 1);
     const int r = lane & 15, g = lane >> 4;
     // the workgroups are numbered over the chunks of up to ROWS_CHUNK rows (of
     // an expert, when grouped: experts without rows have none), a chunk's
     // column tiles after each other
-    const int64_t blocks_n = (p.tiles_n + per_block - 1) / per_block;
-    const int rank = (int)(blockIdx.x / blocks_n);
-    const int64_t tn = (blockIdx.x - rank * blocks_n) * per_block + wave / ks;
+    // (a dense product has one chunk; grid and tile numbers are below 2^32)
+    const uint32_t blocks_n = ((uint32_t)p.tiles_n + per_block - 1) >> p.pb_log;
+    const uint32_t rank = GROUPED ? blockIdx.x / blocks_n : 0;
+    const int64_t first_tn = (int64_t)(blockIdx.x - rank * blocks_n) << p.pb_log, tn = first_tn + (wave >> p.ks_log);
     int64_t lo = (int64_t)rank * ROWS_CHUNK, hi = min(lo + ROWS_CHUNK, p.M);
     const uint8_t *B = p.b, *BS = p.bs;
     if (GROUPED) {
@@ -115,11 +117,11 @@ __global__ __launch_bounds__(1024) void gemm4_rows_kernel(Gemm4Params p)
                     incl += o;
             }
             const int first = before + incl - n;  // number of the expert's first chunk
-            const uint64_t m = __ballot(rank >= first && rank < first + n);
+            const uint64_t m = __ballot((int)rank >= first && (int)rank < first + n);
             if (m) {
                 const int at = __builtin_ctzll(m);
                 grp = e0 + at;
-                lo = __shfl(a + (int64_t)(rank - first) * ROWS_CHUNK, at, 64);
+                lo = __shfl(a + (int64_t)((int)rank - first) * ROWS_CHUNK, at, 64);
                 hi = min(lo + ROWS_CHUNK, __shfl(b, at, 64));
             }
             before += __shfl(incl, 63, 64);
@@ -131,7 +133,7 @@ __global__ __launch_bounds__(1024) void gemm4_rows_kernel(Gemm4Params p)
         BS += grp * p.bs_group_stride;
     }
     const int KT = (int)(p.K / 256);
-    const int g0 = kp * KT / ks, g1 = (kp + 1) * KT / ks;
+    const int g0 = kp * KT >> p.ks_log, g1 = (kp + 1) * KT >> p.ks_log;
     // (a column tile past the last: an empty range, nothing stored)
     const int64_t n0 = min(tn * 16, p.N);
     const int rows_n = (int)min(p.N - n0, (int64_t)16);
@@ -225,7 +227,7 @@ __global__ __launch_bounds__(1024) void gemm4_rows_kernel(Gemm4Params p)
                             c[e] = v[e];
             }
         };
-        if (ks == 1) {
+        if (p.ks_log == 0) {
 #pragma unroll
             for (int i = 0; i < MT; i++)
                 store(n0, i, lane, acc[i]);
@@ -242,7 +244,7 @@ __global__ __launch_bounds__(1024) void gemm4_rows_kernel(Gemm4Params p)
             v4f v = sums[tile * ks * MT * 64 + rest];
             for (int w = 1; w < ks; w++)
                 v += sums[(tile * ks + w) * MT * 64 + rest];
-            store(((blockIdx.x - rank * blocks_n) * per_block + tile) * 16, rest / 64, rest & 63, v);
+            store((first_tn + tile) * 16, rest / 64, rest & 63, v);
         }
     }
 }
@@ -987,14 +989,14 @@ __global__ __launch_bounds__(256) void split4_reduce_kernel(Gemm4Params p)
 
 static int64_t scale_bytes(int64_t rows, int64_t K) { return ((rows + 31) / 32) * (K / 256) * 256; }
 
-// The waves that share a column tile along K, so that about 8 waves a compute
-// unit have loads in flight (`tiles`: column tiles that have rows).
+// Log2 of the waves that share a column tile along K, so that about 8 waves a
+// compute unit have loads in flight (`tiles`: column tiles that have rows).
 static int k_split(int64_t tiles, int64_t KT, int64_t cus)
 {
-    int ks = 1;
-    while (ks < 16 && tiles * ks < 8 * cus && 2 * ks <= KT)
-        ks *= 2;
-    return ks;
+    int log = 0;
+    while (log < 4 && (tiles << log) < 8 * cus && (2 << log) <= KT)
+        log++;
+    return log;
 }
 
 // live: groups that have rows (at most)
@@ -1005,12 +1007,13 @@ static hipError_t launch_rows_t(Gemm4Params p, int64_t live, hipStream_t stream)
     p.bs_bytes = (uint32_t)scale_bytes(p.N, p.K);
     p.vec_store = vec_ok(p.c, p.ld_c, CT);
     p.tiles_n = (p.N + 15) / 16;
-    p.ksplit = k_split(p.tiles_n * live, p.K / 256, cu_count());
-    const int waves = std::max(4, p.ksplit), per_block = waves / p.ksplit;
+    p.ks_log = k_split(p.tiles_n * live, p.K / 256, cu_count());
+    p.pb_log = std::max(0, 2 - p.ks_log);
+    const int waves = 1 << (p.ks_log + p.pb_log), per_block = 1 << p.pb_log;
     // chunks of rows: at most one that is not full for each group that has any
     const int64_t chunks = GROUPED ? live + p.M / ROWS_CHUNK : (p.M + ROWS_CHUNK - 1) / ROWS_CHUNK;
     const int64_t grid = (p.tiles_n + per_block - 1) / per_block * chunks;
-    const size_t lds = p.ksplit > 1 ? (size_t)waves * MT * 1024 : 0;
+    const size_t lds = p.ks_log > 0 ? (size_t)waves * MT * 1024 : 0;
     hipLaunchKernelGGL((gemm4_rows_kernel<GROUPED, CT, MT, MAXG>), dim3((unsigned)grid), dim3(64 * waves), lds, stream,
                        p);
     return hipGetLastError();

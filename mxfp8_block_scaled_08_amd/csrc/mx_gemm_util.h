@@ -1,6 +1,7 @@
 // What the block-scaled product kernels share (mx_gemm.hip, mx_gemm_fp4.hip):
 // vector types, wave-uniform values, the tile walk, the LDS ring's barrier and
-// chunk permutation, BF16 packing, tile coordinates and the compute-unit count.
+// chunk permutation, BF16 packing, tile coordinates and the compute-unit count
+// (which the routing's launcher takes too).
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -1,10 +1,10 @@
 // Routing of tokens to experts, its gradient, and the gradient of the MoE
 // combine (gfx950).
 //
-// Routing.  LANES lanes take a token (16 up to 128 experts, 32 up to 256, else
-// the wave), so a wave holds 4, 2 or 1 tokens, and four waves make a workgroup;
-// lane l holds the selection keys of experts l*EPL .. +EPL-1 in registers, 4 to
-// 16 of them.  A key is a double:
+// Routing.  LANES lanes take a token (16, 32 or 64 of them, by the numbers of
+// experts and tokens), so a wave holds 4, 2 or 1 tokens, and four waves make a
+// workgroup; lane l holds the selection keys of experts l*EPL .. +EPL-1 in
+// registers, 4 to 16 of them.  A key is a double:
 // the selection score with its low 10 mantissa bits replaced by the expert's
 // number, in such a way that of two equal scores the lower expert's key is the
 // larger, so one v_max_f64 finds both the best score and the lowest expert that
@@ -15,13 +15,13 @@
 // thousand would swap two experts.  FP64 costs the same issue slots as FP32 on
 // CDNA4's vector unit.
 //
-// Bound by the chain of topk reductions, five dependent exchanges each, not by
-// the logits' bytes: 20480 FP32 tokens x 128 experts, top 8, take 8.2 us (10.5
-// MB, 2.1 us of HBM, behind an empty launch of 2.2), 32 BF16 tokens 4.2 us.  With
-// score and number compared apart and element loads it was 12.5 us, with one
-// wave a workgroup 8.6.  4099 tokens x 256 experts in 8 groups with a bias take
-// 12.1 us, and took 19.1 with 16 lanes a token and 16 experts a lane.
+// Bound by the chain of topk reductions, four to six dependent exchanges each, not
+// by the logits' bytes: 20480 FP32 tokens x 128 experts, top 8, take 8.0 us (10.5
+// MB, 2.1 us of HBM, behind an empty launch of 2.2), 32 tokens 3.6 us.  With score
+// and number compared apart and element loads it was 12.5 us, with one wave a
+// workgroup 8.6.
 #include "mx_device.h"
+#include "mx_gemm_util.h"
 #include "mx_launch.h"
 
 #include <algorithm>
@@ -514,19 +514,40 @@ static bool vec_rows(const void *p, int64_t ld, int dtype, int64_t experts, int 
     return experts % epl == 0 && ld % 4 == 0 && (uintptr_t)p % (dtype == 0 ? 8 : 16) == 0;
 }
 
-// The lanes a token and the experts a lane holds, by the number of experts.
-template <typename F> static void by_experts(int64_t experts, F f)
+// The lanes a token and the experts a lane holds.  While the tokens make at most
+// eight waves a compute unit, latency counts: the most lanes, so the fewest keys a
+// lane.  Beyond, half the lanes, so that a wave's reductions serve twice the
+// tokens.  FP32, top 8, us, most lanes / half:
+//   32 x 128 3.6 / 4.3, 4096 x 128 4.3 / 4.6, 8192 x 128 5.8 / 5.1, 20480 x 128 10.2 / 8.0
+//   32 x 256 3.7 / 4.4, 2048 x 256 4.5 / 4.7, 4096 x 256 6.2 / 5.3, 20480 x 256 19.8 / 13.4
+//   32 x 512 4.4 / 5.8, 2048 x 512 5.5 / 6.3, 4096 x 512 7.7 / 7.4, 20480 x 512 26.9 / 21.2
+// with 8 groups 4099 x 256 14.1 / 12.3.  The gradient has no reductions a choice
+// and takes the rule up to 256 experts (32 x 128 2.9 / 3.6, 20480 x 128 6.7 / 6.2),
+// the most lanes for 512 (14.4 / 20.2).
+template <bool BWD, typename F> static void by_experts(int64_t tokens, int64_t experts, F f)
 {
+    using I4 = std::integral_constant<int, 4>;
+    using I8 = std::integral_constant<int, 8>;
+    using I16 = std::integral_constant<int, 16>;
+    using I32 = std::integral_constant<int, 32>;
+    using I64 = std::integral_constant<int, 64>;
+    const int64_t most = 8 * (int64_t)cu_count();  // waves
     if (experts <= 64)
-        f(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
+        f(I16{}, I4{});
+    else if (experts <= 128 && tokens * 32 <= most * 64)
+        f(I32{}, I4{});
     else if (experts <= 128)
-        f(std::integral_constant<int, 16>{}, std::integral_constant<int, 8>{});
+        f(I16{}, I8{});
+    else if (experts <= 256 && tokens <= most)
+        f(I64{}, I4{});
     else if (experts <= 256)
-        f(std::integral_constant<int, 32>{}, std::integral_constant<int, 8>{});
-    else if (experts <= 512)
-        f(std::integral_constant<int, 64>{}, std::integral_constant<int, 8>{});
-    else
-        f(std::integral_constant<int, 64>{}, std::integral_constant<int, 16>{});
+        f(I32{}, I8{});
+    else if (experts > 512)
+        f(I64{}, I16{});
+    else if (BWD || tokens <= most)
+        f(I64{}, I8{});
+    else if constexpr (!BWD)
+        f(I32{}, I16{});
 }
 
 template <int LANES, int EPL, int DT, bool SOFTMAX>
@@ -546,7 +567,7 @@ hipError_t launch_moe_route(const void *logits, int dtype, int64_t tokens, int64
                             int64_t topk, bool renorm, float scale, const uint8_t *mask, int32_t *ids, float *weights,
                             hipStream_t stream)
 {
-    by_experts(experts, [&](auto lanes, auto epl) {
+    by_experts<false>(tokens, experts, [&](auto lanes, auto epl) {
         constexpr int L = decltype(lanes)::value, E = decltype(epl)::value;
         const RouteParams p{logits, tokens, ld, (int)experts, vec_rows(logits, ld, dtype, experts, E) ? 1 : 0, bias,
                             (int)groups, (int)(experts / groups), (int)keep_groups, (int)group_top, (int)topk,
@@ -563,7 +584,7 @@ hipError_t launch_moe_route_bwd(const void *logits, int dtype, int64_t tokens, i
                                 bool softmax, int64_t topk, bool renorm, float scale, const int32_t *ids,
                                 const float *dw, void *dx, int64_t ld_d, hipStream_t stream)
 {
-    by_experts(experts, [&](auto lanes, auto epl) {
+    by_experts<true>(tokens, experts, [&](auto lanes, auto epl) {
         constexpr int L = decltype(lanes)::value, E = decltype(epl)::value;
         const bool vec = vec_rows(logits, ld, dtype, experts, E) && vec_rows(dx, ld_d, dtype, experts, E);
         const RouteBwdParams p{logits, tokens, ld, (int)experts, vec ? 1 : 0, (int)topk, renorm ? 1 : 0, scale, ids,

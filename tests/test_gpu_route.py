@@ -68,6 +68,28 @@ def test_route_and_gradient(gpu_lib, T, E, k, renorm, score):
         assert (err <= tol).all(), (err / tol).max()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k", [(4301, 128, 8), (4500, 70, 20), (2301, 256, 8), (2100, 131, 32), (2303, 512, 8),
+                                   (2150, 300, 17)])
+def test_many_tokens(gpu_lib, T, E, k, score):
+    """More tokens than eight waves a compute unit of the wide form: half the lanes a token."""
+    if torch.cuda.get_device_properties(0).multi_processor_count > 256:
+        pytest.skip("sized for 256 compute units")
+    test_route_and_gradient(gpu_lib, T, E, k, score == "softmax", score)
+    rng = np.random.default_rng(T)
+    G = {128: 8, 70: 7, 256: 8, 131: 1, 512: 16, 300: 10}[E]
+    keep = max(1, (G + 1) // 2)
+    bias = rng.standard_normal(E).astype(np.float32) * 0.1
+    mask = (rng.random(T) < 0.9).astype(np.uint8)
+    x = _logits(rng, T, E, torch.float32)
+    _check(gpu_lib, x, min(k, keep * (E // G)), score, bias=bias, num_groups=G, topk_groups=keep, group_top=2 if G > 1 else 1,
+           mask=mask, renormalize=False)
+    # the same rows in a small batch: the same choice
+    ids, _ = gpu_lib.mx_moe_route(x.cuda(), k, score=score)
+    few, _ = gpu_lib.mx_moe_route(x[-99:].cuda(), k, score=score)
+    assert torch.equal(ids[-99:], few)
+
+
 def _sizes(x, ids, g, softmax, renorm):
     """Bound of the terms of each logit's gradient."""
     out = np.zeros(x.shape)

@@ -201,7 +201,7 @@ struct RouteParams {
     int64_t tokens, ld;
     int experts, vec;
     const float *bias;
-    int groups, group_size, keep_groups, group_top;
+    int groups, group_size, keep_groups, group_top, part_log;
     int topk, renorm;
     float scale;
     const uint8_t *mask;
@@ -263,26 +263,38 @@ __global__ __launch_bounds__(RT_THREADS) void route_kernel(RouteParams p)
         key[i] = make_key(v, e);
     }
     if (GROUPS) {
-        // group scores: lane g of the token scans group g's keys (starting at
-        // its own offset, so that the lanes' banks differ), then counts the
-        // groups that rank before its own
+        // group scores: 2^part_log neighbouring lanes scan a group's keys, take
+        // the two largest each and join them in pairs; then lane g counts the
+        // groups that rank before group g.  (One lane a group took 32 x 256 in 8
+        // groups 9.5 us instead of 6.3, 4099 x 256 12.3 instead of 11.3.)
         double *keys = s_keys + sub * p.experts, *score = s_keys + TOKENS * p.experts + sub * p.groups;
 #pragma unroll
         for (int i = 0; i < EPL; i++)
             if (l * EPL + i < p.experts)
                 keys[l * EPL + i] = key[i];
         __syncthreads();
-        for (int g = l; g < p.groups; g += LANES) {
+        const int parts = 1 << p.part_log, part = l & (parts - 1);
+        for (int g0 = 0; g0 < p.groups; g0 += LANES >> p.part_log) {
+            const int g = g0 + (l >> p.part_log);
             double a = -(double)INFINITY, b = a;  // largest, second
-            int at = g % p.group_size;
+            if (g < p.groups) {
+                // (each group from its own place on, so that the lanes' banks differ)
+                const int turn = (g << p.part_log) % p.group_size;
 #pragma unroll 4
-            for (int i = 0; i < p.group_size; i++) {
-                const double v = key_score(keys[g * p.group_size + at]);
-                at = at + 1 == p.group_size ? 0 : at + 1;
-                b = max_key(b, __builtin_fmin(v, a));
-                a = max_key(a, v);
+                for (int i = part; i < p.group_size; i += parts) {
+                    const int at = i + turn < p.group_size ? i + turn : i + turn - p.group_size;
+                    const double v = key_score(keys[g * p.group_size + at]);
+                    b = max_key(b, __builtin_fmin(v, a));
+                    a = max_key(a, v);
+                }
             }
-            score[g] = p.group_top > 1 ? a + b : a;
+            for (int d = 1; d < parts; d *= 2) {
+                const double a2 = __shfl_xor(a, d, 64), b2 = __shfl_xor(b, d, 64);
+                b = max_key(__builtin_fmin(a, a2), max_key(b, b2));
+                a = max_key(a, a2);
+            }
+            if (g < p.groups && part == 0)
+                score[g] = p.group_top > 1 ? a + b : a;
         }
         __syncthreads();
         uint64_t kept = 0;
@@ -521,7 +533,7 @@ static bool vec_rows(const void *p, int64_t ld, int dtype, int64_t experts, int 
 //   32 x 128 3.6 / 4.3, 4096 x 128 4.3 / 4.6, 8192 x 128 5.8 / 5.1, 20480 x 128 10.2 / 8.0
 //   32 x 256 3.7 / 4.4, 2048 x 256 4.5 / 4.7, 4096 x 256 6.2 / 5.3, 20480 x 256 19.8 / 13.4
 //   32 x 512 4.4 / 5.8, 2048 x 512 5.5 / 6.3, 4096 x 512 7.7 / 7.4, 20480 x 512 26.9 / 21.2
-// with 8 groups 4099 x 256 14.1 / 12.3.  The gradient has no reductions a choice
+// The gradient has no reductions a choice
 // and takes the rule up to 256 experts (32 x 128 2.9 / 3.6, 20480 x 128 6.7 / 6.2),
 // the most lanes for 512 (14.4 / 20.2).
 template <bool BWD, typename F> static void by_experts(int64_t tokens, int64_t experts, F f)
@@ -551,10 +563,12 @@ template <bool BWD, typename F> static void by_experts(int64_t tokens, int64_t e
 }
 
 template <int LANES, int EPL, int DT, bool SOFTMAX>
-static void launch_route_t(const RouteParams &p, hipStream_t stream)
+static void launch_route_t(RouteParams p, hipStream_t stream)
 {
     constexpr int TOKENS = RT_THREADS / LANES;
     const dim3 grid((unsigned)((p.tokens + TOKENS - 1) / TOKENS)), block(RT_THREADS);
+    while ((p.groups << (p.part_log + 1)) <= LANES)
+        p.part_log++;
     if (p.groups > 1)
         hipLaunchKernelGGL((route_kernel<LANES, EPL, DT, SOFTMAX, true>), grid, block,
                            (size_t)TOKENS * (p.experts + p.groups) * 8, stream, p);
@@ -570,7 +584,7 @@ hipError_t launch_moe_route(const void *logits, int dtype, int64_t tokens, int64
     by_experts<false>(tokens, experts, [&](auto lanes, auto epl) {
         constexpr int L = decltype(lanes)::value, E = decltype(epl)::value;
         const RouteParams p{logits, tokens, ld, (int)experts, vec_rows(logits, ld, dtype, experts, E) ? 1 : 0, bias,
-                            (int)groups, (int)(experts / groups), (int)keep_groups, (int)group_top, (int)topk,
+                            (int)groups, (int)(experts / groups), (int)keep_groups, (int)group_top, 0, (int)topk,
                             renorm ? 1 : 0, scale, mask, ids, weights};
         if (dtype == 0)
             softmax ? launch_route_t<L, E, 0, true>(p, stream) : launch_route_t<L, E, 0, false>(p, stream);

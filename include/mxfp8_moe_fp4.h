@@ -210,11 +210,10 @@ mx_status mx_swiglu_quantize_fp4(const void *gu, int64_t rows, int64_t F, int64_
  * 32 else MX_ERR_SHAPE) and ld_a, ld_b >= K/2 bytes.  The library estimates
  * the time of each way and takes the least: up to 64 rows (single tokens of a
  * sampler) a kernel that streams B once through all compute units, else tiles
- * of 128x128, 256x128 or 256x256, whose partial last round may be split along K
- * (BF16 C only), with FP32 sums in a workspace of mx_gemm_fp4_workspace_bytes
- * bytes (0: none needed; at most 64 MiB).  The way, and with it the sums'
- * order, depends on M, N, K, c's type and alignment and the device's
- * compute-unit count only.
+ * of 128x128, 256x128 or 256x256, whose partial last round may be split along
+ * K, with FP32 sums in a workspace of mx_gemm_fp4_workspace_bytes bytes (0: none
+ * needed; at most 64 MiB).  The way, and with it the sums' order, depends on M,
+ * N, K and the device's compute-unit count only.
  */
 int64_t mx_gemm_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int c_dtype);
 mx_status mx_gemm_fp4(int64_t M, int64_t N, int64_t K, const void *a_q, int64_t ld_a, const void *a_s_swz,
@@ -227,7 +226,7 @@ mx_status mx_gemm_fp4(int64_t M, int64_t N, int64_t K, const void *a_q, int64_t 
  * outside every group are not written.  Requirements as mx_grouped_gemm's
  * with K % 256 == 0.  Few rows per expert (a sampler's step) stream each
  * routed expert's weights once; more take tiles of 128x128 or 256x256.  The
- * rule goes by M_total, num_groups, N and the device's compute-unit count, so
+ * rule goes by M_total, num_groups, N, K and the device's compute-unit count, so
  * the offsets are read on the device alone.
  */
 mx_status mx_grouped_gemm_fp4(int64_t num_groups, int64_t M_total, int64_t N, int64_t K, const int64_t *group_offsets,

@@ -231,7 +231,7 @@ int64_t mx_gemm_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int c_dtype
 {
     if (M <= 0 || N <= 0 || K <= 0 || K % 256 != 0 || (c_dtype != MX_BF16 && c_dtype != MX_F32))
         return 0;
-    return mx::gemm_fp4_workspace_bytes(M, N, K, c_dtype, true);
+    return mx::gemm_fp4_workspace_bytes(M, N, K);
 }
 
 mx_status mx_gemm_fp4(int64_t M, int64_t N, int64_t K, const void *a_q, int64_t ld_a, const void *a_s_swz,
@@ -249,7 +249,7 @@ mx_status mx_gemm_fp4(int64_t M, int64_t N, int64_t K, const void *a_q, int64_t 
                              swz_bytes(N, K / 32), extent(M, N, ld_c, c_dtype == MX_BF16 ? 2 : 4)};
     if ((st = any_overlap(fn, bufs, lens, 5, 4)) != MX_OK)
         return st;
-    const int64_t need = mx::gemm_fp4_workspace_bytes(M, N, K, c_dtype, mx::gemm_vec16(c, ld_c, c_dtype));
+    const int64_t need = mx::gemm_fp4_workspace_bytes(M, N, K);
     if ((st = check_workspace(fn, workspace, workspace_bytes, need, 16, bufs, lens, 5)) != MX_OK)
         return st;
     return hip_status(mx::launch_gemm_fp4(M, N, K, a_q, ld_a, a_s_swz, b_q, ld_b, b_s_swz, c, ld_c, c_dtype,

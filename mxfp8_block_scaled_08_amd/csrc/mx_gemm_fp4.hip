@@ -818,7 +818,7 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
             nxt2_ok = k + 2 < my_units;
             nxt2 = nxt2_ok ? unit(k + 2) : nxt;
         }
-        // ---- split-tail unit (BF16 C, whole-width tiles only): its FP32
+        // ---- split-tail unit: its FP32
         // partial tile goes to its workspace slot, lane-major per sub-tile
         // and register group (64 lanes x 16 bytes per store, whole lines,
         // non-temporal; the default policy is within 2 % either way)
@@ -943,10 +943,10 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
 
 // Sums of the split tiles: thread t of a tile's takes float4 t of its slots
 // (the partial-tile layout above: wave, sub-tile (i, j), register group q,
-// lane), adds the split_s slots in range order and writes the four BF16 of C
+// lane), adds the split_s slots in range order and writes the four elements of C
 // they hold: row 64j + 32wm + (lane & 31), columns wn*WN + 32i + 8q +
 // 4(lane >> 5) .. +3.
-template <int TM, int TN>
+template <int CT, int TM, int TN>
 __global__ __launch_bounds__(256) void split4_reduce_kernel(Gemm4Params p)
 {
     constexpr int BM = 64 * TM, BN = 64 * TN;
@@ -971,19 +971,48 @@ __global__ __launch_bounds__(256) void split4_reduce_kernel(Gemm4Params p)
     const int64_t in = pid - grp * per_group;
     const int64_t m = (first_m + in % gm) * BM + row;
     const int64_t n = (in / gm) * BN + col;
-    if (m >= p.M)
+    if (m >= p.M || n >= p.N)
         return;
     const float4 *src = reinterpret_cast<const float4 *>(p.ws) + (int64_t)r * p.split_s * (BM * BN / 4) + t;
     float4 a = src[0];
-    for (int sidx = 1; sidx < p.split_s; sidx++) {
-        const float4 b = src[(int64_t)sidx * (BM * BN / 4)];
+    const auto add = [&](float4 b) {
         a.x += b.x;
         a.y += b.y;
         a.z += b.z;
         a.w += b.w;
+    };
+    // many ranges: four loads in flight, as one after another they take their
+    // latency each (64x256x16384 in 32 ranges: 18.6 us, so 12.2)
+    int sidx = 1;
+    for (; sidx + 4 <= p.split_s; sidx += 4) {
+        float4 b[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            b[i] = src[(int64_t)(sidx + i) * (BM * BN / 4)];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            add(b[i]);
     }
-    *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(p.c) + m * p.ld_c + n) =
-        make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+    for (; sidx < p.split_s; sidx++)
+        add(src[(int64_t)sidx * (BM * BN / 4)]);
+    const bool whole = p.vec_store && n + 3 < p.N;
+    const float v[4] = {a.x, a.y, a.z, a.w};
+    if (CT == 0) {
+        uint16_t *c = reinterpret_cast<uint16_t *>(p.c) + m * p.ld_c + n;
+        const uint2 w = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+        if (whole)
+            *reinterpret_cast<uint2 *>(c) = w;
+        else
+            for (int e = 0; e < 4 && n + e < p.N; e++)
+                c[e] = (uint16_t)((e < 2 ? w.x : w.y) >> (16 * (e & 1)));
+    } else {
+        float *c = reinterpret_cast<float *>(p.c) + m * p.ld_c + n;
+        if (whole)
+            *reinterpret_cast<float4 *>(c) = a;
+        else
+            for (int e = 0; e < 4 && n + e < p.N; e++)
+                c[e] = v[e];
+    }
 }
 
 
@@ -1026,8 +1055,9 @@ static hipError_t launch_rows_t(Gemm4Params p, int64_t live, hipStream_t stream)
 // The estimates, in us, fitted on one MI355X at M 1..4608, N 512..24576, K
 // 512..24576 (two kernels in a row: 2 us each at least):
 //   few rows (M <= 64): 2 + 0.195 a MB of B + 0.1 a MB of A as it is read, once
-//     for every 16 columns.  1x6144x4096 5.0, 64x6144x4096 12.0, 32x4096x12288
-//     12.6.
+//     for every 16 columns, times 0.85 of the units over the workgroups where
+//     those are fewer.  1x6144x4096 4.6, 64x6144x4096 11.8, 32x4096x12288 12.6,
+//     64x1000x16384 23.3 (12.4 by tiles), 1x256x16384 7.8 (12.0 by tiles).
 //   tiles: a round of w tiles takes a fixed part and a time for each 128-K
 //     stage that grows with the compute units in use, as the tiles share L2 and
 //     power: 128x128 0.27 .. 0.34, or 0.64 when units hold two; 256x128 0.38 ..
@@ -1035,8 +1065,10 @@ static hipError_t launch_rows_t(Gemm4Params p, int64_t live, hipStream_t stream)
 //     x4096: 12.9, against 18.8 and 27.6), large ones read less: with every unit
 //     busy 256x256 moves 1.33 as fast as 128x128 (12288x4096x24576: 527 against
 //     687).
-//   split: 3 for the second kernel, 0.3 a MB of partial sums.  65x4096x12288 in
-//     six ranges 17.2, whole 26.5; 333x6144x4096 in two 24.4, whole 12.9.
+//   split: 3 for the second kernel, 0.05 a range, 0.3 a MB of partial sums.
+//     128x4096x12288 15.4, 2044x94x14592 14.3 (33 whole), 100x515x8192 10.6 (21
+//     whole), 333x6144x4096 in two 24.4, whole 12.9.  (With 0.2 a MB 128x6144x4096
+//     splits too far: 16 against 11.7.)
 struct TilePlan {
     bool rows = false;
     int tm = 4, tn = 4;
@@ -1044,7 +1076,7 @@ struct TilePlan {
     int64_t bytes() const { return S >= 2 ? rem * S * 64 * tm * 64 * tn * 4 : 0; }
 };
 
-static TilePlan tile_plan(int64_t M, int64_t N, int64_t K, int c_dtype, bool vec16, int64_t cus)
+static TilePlan tile_plan(int64_t M, int64_t N, int64_t K, int64_t cus)
 {
     struct Shape {
         int tm, tn, per_cu;
@@ -1068,28 +1100,28 @@ static TilePlan tile_plan(int64_t M, int64_t N, int64_t K, int c_dtype, bool vec
             }
         };
         take(1, rounds + (rem ? stages * rate(rem) : 0));
-        // (BF16 whole-line stores of full-width tiles only; at most 64 MiB of sums)
-        if (rem && c_dtype == 0 && vec16 && N % bn == 0)
+        // (at most 64 MiB of sums)
+        if (rem)
             for (int64_t S = 2; S <= std::min<int64_t>(groups, slots / rem) && rem * S * bm * bn * 4 <= (64 << 20); S++)
-                take(S, rounds + (double)((groups + S - 1) / S * 4) * rate(rem * S) + 3 +
+                take(S, rounds + (double)((groups + S - 1) / S * 4) * rate(rem * S) + 3 + 0.05 * (double)S +
                             0.3 * (double)(rem * S * bm * bn * 4) * 1e-6);
     }
     if (M <= ROWS_CHUNK) {
         const double mb = (double)K * 17 / 32 * 1e-6;
-        best.rows = 2 + 0.195 * N * mb + 0.1 * ((N + 15) / 16) * M * mb < least;
+        const int64_t tiles = (N + 15) / 16;
+        const int ks_log = k_split(tiles, K / 256, cus);
+        const double idle = std::max(1.0, 0.85 * (double)cus / (double)std::max<int64_t>(1, tiles >> std::max(0, 2 - ks_log)));
+        best.rows = 2 + (0.195 * N * mb + 0.1 * tiles * M * mb) * idle < least;
         if (best.rows)
             best.S = 1;
     }
     return best;
 }
 
-int64_t gemm_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int c_dtype, bool vec16)
-{
-    return tile_plan(M, N, K, c_dtype, vec16, cu_count()).bytes();
-}
+int64_t gemm_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K) { return tile_plan(M, N, K, cu_count()).bytes(); }
 
-template <int TM, int TN>
-static hipError_t launch_tiles_t(Gemm4Params p, const TilePlan &plan, int c_dtype, void *ws, hipStream_t stream)
+template <int CT, int TM, int TN>
+static hipError_t launch_tiles_t(Gemm4Params p, const TilePlan &plan, void *ws, hipStream_t stream)
 {
     constexpr int BM = 64 * TM, BN = 64 * TN;
     p.tiles_m = (p.M + BM - 1) / BM;
@@ -1097,24 +1129,23 @@ static hipError_t launch_tiles_t(Gemm4Params p, const TilePlan &plan, int c_dtyp
     const int64_t tiles = p.tiles_m * p.tiles_n;
     const int64_t slots = (int64_t)cu_count() * (TM * TN <= 4 ? 2 : 1);  // workgroups that run at once
     p.dp_tiles = tiles;
-    unsigned grid = (unsigned)std::min<int64_t>(tiles, slots);
-    if (plan.S > 1) {
-        p.dp_tiles = tiles - plan.rem;
-        p.split_tiles = (int)plan.rem;
-        p.split_s = (int)plan.S;
-        p.ws = (float *)ws;
-        grid = (unsigned)std::max<int64_t>(std::min<int64_t>(p.dp_tiles, slots), plan.rem * plan.S);
-        hipLaunchKernelGGL((gemm4_tile_kernel<false, 0, true, TM, TN>), dim3(grid), dim3(GM_THREADS), 0, stream, p);
-        const hipError_t err = hipGetLastError();
-        if (err != hipSuccess)
-            return err;
-        hipLaunchKernelGGL((split4_reduce_kernel<TM, TN>), dim3((unsigned)(p.split_tiles * (BM * BN / 4 / 256))),
-                           dim3(256), 0, stream, p);
-    } else if (c_dtype == 0) {
-        hipLaunchKernelGGL((gemm4_tile_kernel<false, 0, false, TM, TN>), dim3(grid), dim3(GM_THREADS), 0, stream, p);
-    } else {
-        hipLaunchKernelGGL((gemm4_tile_kernel<false, 1, false, TM, TN>), dim3(grid), dim3(GM_THREADS), 0, stream, p);
+    if (plan.S == 1) {
+        hipLaunchKernelGGL((gemm4_tile_kernel<false, CT, false, TM, TN>),
+                           dim3((unsigned)std::min<int64_t>(tiles, slots)), dim3(GM_THREADS), 0, stream, p);
+        return hipGetLastError();
     }
+    p.dp_tiles = tiles - plan.rem;
+    p.split_tiles = (int)plan.rem;
+    p.split_s = (int)plan.S;
+    p.ws = (float *)ws;
+    const int64_t grid = std::max<int64_t>(std::min<int64_t>(p.dp_tiles, slots), plan.rem * plan.S);
+    hipLaunchKernelGGL((gemm4_tile_kernel<false, CT, true, TM, TN>), dim3((unsigned)grid), dim3(GM_THREADS), 0, stream,
+                       p);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess)
+        return err;
+    hipLaunchKernelGGL((split4_reduce_kernel<CT, TM, TN>), dim3((unsigned)(p.split_tiles * (BM * BN / 4 / 256))),
+                       dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -1134,7 +1165,7 @@ hipError_t launch_gemm_fp4(int64_t M, int64_t N, int64_t K, const void *a_q, int
     p.bs = (const uint8_t *)b_s;
     p.c = c;
     p.ld_c = ld_c;
-    const TilePlan plan = tile_plan(M, N, K, c_dtype, gemm_vec16(c, ld_c, c_dtype), cu_count());
+    const TilePlan plan = tile_plan(M, N, K, cu_count());
     if (plan.rows) {
         if (c_dtype == 0)
             return M <= 16   ? launch_rows_t<false, 0, 1, 4>(p, 1, stream)
@@ -1149,10 +1180,10 @@ hipError_t launch_gemm_fp4(int64_t M, int64_t N, int64_t K, const void *a_q, int
     p.vec_store = vec_ok(c, ld_c, c_dtype);
     p.vec16 = gemm_vec16(c, ld_c, c_dtype);
     if (plan.tm == 4 && plan.tn == 4)
-        return launch_tiles_t<4, 4>(p, plan, c_dtype, ws, stream);
+        return c_dtype == 0 ? launch_tiles_t<0, 4, 4>(p, plan, ws, stream) : launch_tiles_t<1, 4, 4>(p, plan, ws, stream);
     if (plan.tm == 4)
-        return launch_tiles_t<4, 2>(p, plan, c_dtype, ws, stream);
-    return launch_tiles_t<2, 2>(p, plan, c_dtype, ws, stream);
+        return c_dtype == 0 ? launch_tiles_t<0, 4, 2>(p, plan, ws, stream) : launch_tiles_t<1, 4, 2>(p, plan, ws, stream);
+    return c_dtype == 0 ? launch_tiles_t<0, 2, 2>(p, plan, ws, stream) : launch_tiles_t<1, 2, 2>(p, plan, ws, stream);
 }
 
 // The tile count depends on the device-side offsets: as many workgroups as run
@@ -1166,6 +1197,28 @@ template <int TM, int TN> static hipError_t launch_group_tiles_t(Gemm4Params p, 
     else
         hipLaunchKernelGGL((gemm4_tile_kernel<true, 1, false, TM, TN>), grid, dim3(GM_THREADS), 0, stream, p);
     return hipGetLastError();
+}
+
+// Whether a grouped product takes 256 x 256 tiles, by estimates as tile_plan's with
+// a time for each tile's stores; of the `live` experts' last tiles about 0.4 (by
+// 256 rows, whose smaller half is multiplied alone) and 0.5 (by 128) are extra.
+// 128 x 128 against 256 x 256, us:
+//   128 experts, N 1536, K 2048, rows an expert 64: 47 / 52, 128: 66 / 64, 512: 180 / 158
+//   128 experts, N 2048, K 768,  rows 128: 45 / 47, 320: 87 / 94, 512: 128 / 122
+//   8 experts, rows 512, N 512, K 1792: 10 / 19, N 4096, K 4096: 58 / 61; rows 1024: 104 / 96
+//   32 experts, rows 1280, N 2048, K 256: 50 / 52
+static bool large_group_tiles(int64_t M, int64_t N, int64_t K, int64_t live, int64_t cus)
+{
+    const double stages = (double)K / 128;
+    // rounds of one 256 x 256 tile a unit, of two 128 x 128 ones
+    const double large = ((double)M / 256 + 0.4 * (double)live) * (double)((N + 255) / 256) / (double)cus;
+    const double small = ((double)M / 128 + 0.5 * (double)live) * (double)((N + 127) / 128) / (double)(2 * cus);
+    const double t_large =
+        3 + (large <= 1 ? stages * (0.58 + 0.38 * large) + 3 * large : (large + 0.35) * (stages * 0.96 + 3));
+    const double t_small = 2 + (small <= 0.5 ? stages * (0.27 + 0.14 * small) + small
+                                : small <= 1 ? stages * 0.64 + 1
+                                             : (small + 0.35) * (stages * 0.64 + 1));
+    return t_large < t_small;
 }
 
 hipError_t launch_grouped_gemm_fp4(int64_t G, int64_t M_total, int64_t N, int64_t K, const int64_t *offsets,
@@ -1200,12 +1253,8 @@ hipError_t launch_grouped_gemm_fp4(int64_t G, int64_t M_total, int64_t N, int64_
     p.bs_bytes = (uint32_t)p.bs_group_stride;
     p.vec_store = vec_ok(c, ld_c, c_dtype);
     p.vec16 = gemm_vec16(c, ld_c, c_dtype);
-    // 128 x 128 tiles up to 256 rows an expert, larger ones above: 64 rows an
-    // expert (128 experts, N 1536, K 2048) 47 us against 52 by 256 x 256 tiles,
-    // 256 rows 96 against 96, 512 rows 180 against 158; at N 2048, K 768 31
-    // against 39, 74 against 75, 128 against 122.
-    return M_total <= 256 * G ? launch_group_tiles_t<2, 2>(p, c_dtype, stream)
-                              : launch_group_tiles_t<4, 4>(p, c_dtype, stream);
+    return large_group_tiles(M_total, N, K, live, cu_count()) ? launch_group_tiles_t<4, 4>(p, c_dtype, stream)
+                                                              : launch_group_tiles_t<2, 2>(p, c_dtype, stream);
 }
 
 }  // namespace mx

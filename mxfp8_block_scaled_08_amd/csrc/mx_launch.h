@@ -199,7 +199,7 @@ void launch_dispatch_order(const int32_t *topk_ids, int64_t tokens, int64_t topk
 // MXFP4 products (mx_gemm_fp4.hip): ld_a, ld_b in bytes, K % 256 == 0.  ws: at
 // least gemm_fp4_workspace_bytes(...) bytes, 16-byte aligned (may be null when
 // that is 0).
-int64_t gemm_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int c_dtype, bool vec16);
+int64_t gemm_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_fp4(int64_t M, int64_t N, int64_t K, const void *a_q, int64_t ld_a, const void *a_s,
                            const void *b_q, int64_t ld_b, const void *b_s, void *c, int64_t ld_c, int c_dtype,
                            void *ws, hipStream_t stream);

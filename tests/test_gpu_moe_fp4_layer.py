@@ -57,7 +57,8 @@ def _random_operand(g, rows, K):
     (200, 4096, 12288, True), (90, 1024, 8192, True),                             # and split along K
     (2048, 4096, 2048, False), (2000, 4104, 2304, False),                         # 256 x 128
     (2048, 8192, 2048, False), (4096, 4096, 8192, False),                         # 256 x 256
-    (4608, 4096, 12288, True)])
+    (4608, 4096, 12288, True),
+    (2044, 94, 14592, True), (90, 1001, 8192, True), (131, 130, 5120, True)])     # split, columns left over
 def test_products_cut_every_way(gpu_lib, M, N, K, split):
     mx = gpu_lib
     g = torch.Generator(device=dev)
@@ -70,6 +71,25 @@ def test_products_cut_every_way(gpu_lib, M, N, K, split):
         C = mx.mx_gemm_fp4(a, sa, b, sb, out_dtype=dt)
         _close(C, A, B, f"{M}x{N}x{K} {dt}")
         assert torch.equal(C, mx.mx_gemm_fp4(a, sa, b, sb, out_dtype=dt))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [(200, 4096, 12288), (77, 1001, 8192)])
+def test_split_products_into_unaligned_rows(gpu_lib, M, N, K, dt):
+    """C of any alignment and leading dimension; what is around it stays."""
+    mx = gpu_lib
+    g = torch.Generator(device=dev)
+    g.manual_seed(M)
+    a, sa = _random_operand(g, M, K)
+    b, sb = _random_operand(g, N, K)
+    assert mx.mx_gemm_fp4_workspace_bytes(M, N, K, dt) > 0
+    want = mx.mx_gemm_fp4(a, sa, b, sb, out_dtype=dt)
+    for left, right in ((0, 1), (1, 2), (3, 4), (8, 8)):
+        buf = torch.full((M + 1, left + N + right), 7.0, dtype=dt, device=dev)
+        mx.mx_gemm_fp4(a, sa, b, sb, c=buf[:M, left:left + N])
+        assert torch.equal(buf[:M, left:left + N], want)
+        buf[:M, left:left + N] = 7.0
+        assert (buf == 7.0).all()
 
 
 @pytest.mark.parametrize("rows,N,K", [

@@ -228,34 +228,37 @@ __global__ __launch_bounds__(RT_THREADS) void route_kernel(RouteParams p)
     const bool scored = p.bias != nullptr || p.group_top > 1;
     float mx = 0.0f, fsum = 1.0f;
     double inv = 1.0;
+    double key[EPL];  // (until the selection: the row's exponentials)
     if (SOFTMAX && (scored || !p.renorm)) {
         mx = x[0];
 #pragma unroll
         for (int i = 1; i < EPL; i++)
             mx = max_nan(mx, x[i]);
         mx = shift_of(max_of<LANES>(mx));
-        if (!p.renorm) {
+        if (scored) {
+            double s = 0.0;
+#pragma unroll
+            for (int i = 0; i < EPL; i++) {
+                key[i] = exp((double)x[i] - (double)mx);
+                s += key[i];
+            }
+            s = sum_of<LANES>(s);
+            inv = 1.0 / s;
+            fsum = (float)s;
+        } else {
             fsum = 0.0f;
 #pragma unroll
             for (int i = 0; i < EPL; i++)
                 fsum += expf(x[i] - mx);
             fsum = sum_of<LANES>(fsum);
         }
-        if (scored) {
-            double s = 0.0;
-#pragma unroll
-            for (int i = 0; i < EPL; i++)
-                s += exp((double)x[i] - (double)mx);
-            inv = 1.0 / sum_of<LANES>(s);
-        }
     }
-    double key[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; i++) {
         const int e = l * EPL + i;
         double v = (double)x[i];
         if (scored && x[i] != -INFINITY) {
-            v = SOFTMAX ? exp((double)x[i] - (double)mx) * inv : 1.0 / (1.0 + exp(-(double)x[i]));
+            v = SOFTMAX ? key[i] * inv : 1.0 / (1.0 + exp(-(double)x[i]));
             if (p.bias != nullptr)
                 v += (double)p.bias[e];
             v = v != v ? (double)x[i] : v;  // a NaN or +inf in the row: its experts rank by their logits, NaN first

@@ -889,7 +889,8 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
                     }
                 }
             }
-        } else {
+        } else if (p.vec_store) {
+            // columns left over: each lane stores its own four of its own row
 #pragma unroll
             for (int i = 0; i < TN; i++) {
 #pragma unroll
@@ -904,23 +905,21 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
                             if (CT == 0) {
                                 uint16_t *crow = reinterpret_cast<uint16_t *>(p.c) + m * p.ld_c;
                                 const uint32_t w0 = pack_bf16x2(v0, v1), w1 = pack_bf16x2(v2, v3);
-                                if (p.vec_store && n + 3 < N) {
+                                if (n + 3 < N) {
                                     *reinterpret_cast<uint2 *>(crow + n) = make_uint2(w0, w1);
                                 } else {
                                     if (n + 0 < N) crow[n + 0] = (uint16_t)w0;
                                     if (n + 1 < N) crow[n + 1] = (uint16_t)(w0 >> 16);
                                     if (n + 2 < N) crow[n + 2] = (uint16_t)w1;
-                                    if (n + 3 < N) crow[n + 3] = (uint16_t)(w1 >> 16);
                                 }
                             } else {
                                 float *crow = reinterpret_cast<float *>(p.c) + m * p.ld_c;
-                                if (p.vec_store && n + 3 < N) {
+                                if (n + 3 < N) {
                                     *reinterpret_cast<float4 *>(crow + n) = make_float4(v0, v1, v2, v3);
                                 } else {
                                     if (n + 0 < N) crow[n + 0] = v0;
                                     if (n + 1 < N) crow[n + 1] = v1;
                                     if (n + 2 < N) crow[n + 2] = v2;
-                                    if (n + 3 < N) crow[n + 3] = v3;
                                 }
                             }
                         }
@@ -930,6 +929,55 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
                         acc[i][j][v] = 0.0f;
                 }
             }
+        } else {
+            // rows of C that allow no vector stores: band by band through LDS, so
+            // that a store's lanes run along a row (stored as above, 64 lines an
+            // instruction, 6088x3097x7936 took 144 us, now 121).  Stages 2 and 3
+            // of the ring are free until the next unit's first stage writes them:
+            // every wave has read them before the last barrier, and the one below
+            // holds those writes back.  16-byte chunk c of row r sits in slot c ^ r.
+            constexpr int CHUNKS = WN / 4, REGION = 32 * WN * 4;
+            static_assert(REGION <= A_STAGE && REGION <= B_STAGE, "a wave's band fits a stage");
+            uint8_t *const band = wave < 2 ? &sA[2 + wave][0] : &sB[wave][0];
+            // (offsets are formed here, per tile, not kept across the main loop)
+            int ln = lane;
+            asm volatile("" : "+v"(ln));
+            const int row = ln & 31;
+#pragma unroll
+            for (int j = 0; j < TM; j++) {
+#pragma unroll
+                for (int i = 0; i < TN; i++)
+#pragma unroll
+                    for (int q = 0; q < 4; q++) {
+                        const int c = (i * 8 + 2 * q + (ln >> 5)) ^ (row & (CHUNKS - 1));
+                        *reinterpret_cast<v4f *>(band + row * (WN * 4) + c * 16) =
+                            v4f{acc[i][j][4 * q + 0], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                    }
+#pragma unroll
+                for (int i = 0; i < TN; i++)
+#pragma unroll
+                    for (int v = 0; v < 16; v++)
+                        acc[i][j][v] = 0.0f;
+                const int m0 = cur.m0 + wm * 32 + j * 64, rows = min(cur.m_end - m0, 32);
+#pragma unroll 4
+                for (int r = 0; r < rows; r++) {
+#pragma unroll
+                    for (int k = 0; k < WN / 64; k++) {
+                        const int e = k * 64 + ln;
+                        const int n = cur.n0 + wn * WN + e;
+                        const float v = *reinterpret_cast<const float *>(
+                            band + r * (WN * 4) + ((e >> 2) ^ (r & (CHUNKS - 1))) * 16 + (e & 3) * 4);
+                        if (n < N) {
+                            const int64_t at = (int64_t)(m0 + r) * p.ld_c + n;
+                            if (CT == 0)
+                                reinterpret_cast<__bf16 *>(p.c)[at] = (__bf16)v;
+                            else
+                                reinterpret_cast<float *>(p.c)[at] = v;
+                        }
+                    }
+                }
+            }
+            lds_ring_barrier();
         }
         if (!nxt_ok)
             break;

@@ -92,6 +92,28 @@ def test_split_products_into_unaligned_rows(gpu_lib, M, N, K, dt):
         assert (buf == 7.0).all()
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [(333, 1000, 1024), (2000, 4103, 2304), (4097, 4095, 4096), (700, 50, 768), (1500, 513, 256)])
+def test_products_into_unaligned_rows(gpu_lib, M, N, K, dt):
+    """The same of every tile size, several tiles a workgroup, unsplit or with a split rest."""
+    mx = gpu_lib
+    g = torch.Generator(device=dev)
+    g.manual_seed(M)
+    a, sa = _random_operand(g, M, K)
+    b, sb = _random_operand(g, N, K)
+    A, B = _decode(a, sa), _decode(b, sb)
+    want = None
+    for left, right in ((1, 2), (0, 0), (3, 5), (2, 1)):
+        buf = torch.full((M + 1, left + N + right), 7.0, dtype=dt, device=dev)
+        mx.mx_gemm_fp4(a, sa, b, sb, c=buf[:M, left:left + N])
+        if want is None:
+            want = buf[:M, left:left + N].clone()
+            _close(want, A, B, f"{M}x{N}x{K}")
+        assert torch.equal(buf[:M, left:left + N], want)
+        buf[:M, left:left + N] = 7.0
+        assert (buf == 7.0).all()
+
+
 @pytest.mark.parametrize("rows,N,K", [
     ([150] + [1] * 50 + [0] * 13, 96, 512),           # few rows: an expert of three chunks
     ([0, 0, 1, 0], 200, 256), ([16] * 4, 48, 768),
@@ -99,6 +121,7 @@ def test_split_products_into_unaligned_rows(gpu_lib, M, N, K, dt):
     ([700, 300, 0, 513], 520, 1024),                  # 256 x 256
     ([384, 385, 383, 641, 256, 513, 1025, 320], 776, 768),   # and tails of every kind: whole, half or less
     ([128, 900, 1, 1152, 127, 0, 129, 500], 256, 256), ([2000, 64, 65, 63], 512, 1280),
+    ([900, 3, 2500, 1100, 129, 4000, 31, 0], 4097, 2048), ([40, 300, 1, 77], 1001, 1024),   # and rows of odd length
     ([0] * 1023 + [5], 64, 256)])
 def test_grouped_products_cut_every_way(gpu_lib, rows, N, K):
     mx = gpu_lib

@@ -122,7 +122,8 @@ mx_status mx_moe_route_bwd(const void *logits, int logits_dtype, int64_t tokens,
  *   dy         BF16 [tokens*topk][ld_dy] out, or null (not wanted): rows that
  *              no slot names keep their bytes (they belong to no expert)
  *   d_weights  DEVICE float [tokens][topk] out, or null (not wanted; y may
- *              then be null too).  The sum's order depends on hidden only.
+ *              then be null too).  The sum's order depends on hidden, tokens
+ *              and the device's compute-unit count only.
  * dy is the expert down projection's output gradient: mx_quantize_dual_grouped
  * and the grouped products take it as it is.  Slots are distinct
  * (mx_moe_dispatch's are); where two name one row, that row holds one of the

@@ -47,19 +47,19 @@ template <int DT> __device__ __forceinline__ float logit_at(const void *p, int64
 
 // A lane's EPL consecutive logits from expert e0 of the row at element `row`;
 // -inf past the experts and where the token is not live.  vec: rows are aligned
-// to 16 bytes (8 for 4 BF16) and experts a multiple of EPL, so a lane's run is
-// whole and loads as vectors.
+// to 16 bytes (8 for 4 BF16) and experts a multiple of 4, so that a run loads as
+// vectors of four.
 template <int EPL, int DT>
 __device__ __forceinline__ void load_logits(const void *p, int64_t row, int e0, int experts, bool live, bool vec,
                                             float *x)
 {
     if (vec) {
-        const bool in = live && e0 < experts;
         if (DT == 0) {
 #pragma unroll
             for (int i = 0; i < EPL; i += 4) {
-                const uint2 w = in ? *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p) + row + e0 + i)
-                                   : make_uint2(0xFF80FF80u, 0xFF80FF80u);
+                uint2 w = make_uint2(0xFF80FF80u, 0xFF80FF80u);
+                if (live && e0 + i < experts)
+                    w = *reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p) + row + e0 + i);
                 x[i] = bf16_f32(w.x & 0xFFFFu);
                 x[i + 1] = bf16_f32(w.x >> 16);
                 x[i + 2] = bf16_f32(w.y & 0xFFFFu);
@@ -69,7 +69,7 @@ __device__ __forceinline__ void load_logits(const void *p, int64_t row, int e0, 
 #pragma unroll
             for (int i = 0; i < EPL; i += 4) {
                 f4_t w = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                if (in)
+                if (live && e0 + i < experts)
                     w = *reinterpret_cast<const f4_t *>(reinterpret_cast<const float *>(p) + row + e0 + i);
 #pragma unroll
                 for (int k = 0; k < 4; k++)
@@ -496,10 +496,10 @@ __global__ __launch_bounds__(RT_THREADS) void route_bwd_kernel(RouteBwdParams p)
         acc[i] = full ? pr[i] / total * (acc[i] - dot) : acc[i];
     const int64_t out = t * p.ld_d + l * EPL;
     if (p.vec) {
-        if (l * EPL >= p.experts)
-            return;
 #pragma unroll
         for (int i = 0; i < EPL; i += 4) {
+            if (l * EPL + i >= p.experts)
+                return;
             if (DT == 0) {
                 typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
                 const f4_t a = {acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
@@ -522,11 +522,11 @@ __global__ __launch_bounds__(RT_THREADS) void route_bwd_kernel(RouteBwdParams p)
     }
 }
 
-// Rows that a lane's run of EPL logits can be read from (written to) as
-// vectors of four: 8-byte aligned for BF16, 16-byte for FP32.
-static bool vec_rows(const void *p, int64_t ld, int dtype, int64_t experts, int epl)
+// Rows that a lane's run of logits can be read from (written to) as vectors of
+// four: 8-byte aligned for BF16, 16-byte for FP32.
+static bool vec_rows(const void *p, int64_t ld, int dtype, int64_t experts)
 {
-    return experts % epl == 0 && ld % 4 == 0 && (uintptr_t)p % (dtype == 0 ? 8 : 16) == 0;
+    return experts % 4 == 0 && ld % 4 == 0 && (uintptr_t)p % (dtype == 0 ? 8 : 16) == 0;
 }
 
 // The lanes a token and the experts a lane holds.  While the tokens make at most
@@ -586,7 +586,7 @@ hipError_t launch_moe_route(const void *logits, int dtype, int64_t tokens, int64
 {
     by_experts<false>(tokens, experts, [&](auto lanes, auto epl) {
         constexpr int L = decltype(lanes)::value, E = decltype(epl)::value;
-        const RouteParams p{logits, tokens, ld, (int)experts, vec_rows(logits, ld, dtype, experts, E) ? 1 : 0, bias,
+        const RouteParams p{logits, tokens, ld, (int)experts, vec_rows(logits, ld, dtype, experts) ? 1 : 0, bias,
                             (int)groups, (int)(experts / groups), (int)keep_groups, (int)group_top, 0, (int)topk,
                             renorm ? 1 : 0, scale, mask, ids, weights};
         if (dtype == 0)
@@ -603,7 +603,7 @@ hipError_t launch_moe_route_bwd(const void *logits, int dtype, int64_t tokens, i
 {
     by_experts<true>(tokens, experts, [&](auto lanes, auto epl) {
         constexpr int L = decltype(lanes)::value, E = decltype(epl)::value;
-        const bool vec = vec_rows(logits, ld, dtype, experts, E) && vec_rows(dx, ld_d, dtype, experts, E);
+        const bool vec = vec_rows(logits, ld, dtype, experts) && vec_rows(dx, ld_d, dtype, experts);
         const RouteBwdParams p{logits, tokens, ld, (int)experts, vec ? 1 : 0, (int)topk, renorm ? 1 : 0, scale, ids,
                                dw, dx, ld_d};
         const dim3 grid((unsigned)((tokens * L + RT_THREADS - 1) / RT_THREADS)), block(RT_THREADS);
@@ -626,7 +626,9 @@ hipError_t launch_moe_route_bwd(const void *logits, int dtype, int64_t tokens, i
 // order, once per 8 slots.  Bound by HBM: 20480 tokens, top 8, hidden 2048 move
 // 1.43 GB in 258 us, 5.5 TB/s (a plain copy 5.0); both results of one pass, as
 // two passes would read d_out twice.  Rows up to 512 or 1024 wide take one or
-// two waves, so that no lane is without columns.
+// two waves, so that no lane is without columns; wide rows of up to two tokens a
+// compute unit take eight (64 x 8 x 4096: 7.2 us with four, 6.1 with eight, 512 x 8
+// x 4096 14.7 / 12.8, 1024 x 8 x 4096 25.6 / 28.1).
 constexpr int CB_SLOTS = 8;
 
 template <int WAVES>
@@ -714,6 +716,8 @@ hipError_t launch_moe_combine_bwd(const void *d_out, int64_t tokens, int64_t hid
         MX_CB(1);
     else if (units <= 128)
         MX_CB(2);
+    else if (units > 256 && tokens <= 2 * (int64_t)cu_count())
+        MX_CB(8);
     else
         MX_CB(4);
 #undef MX_CB

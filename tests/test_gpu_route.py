@@ -47,7 +47,8 @@ def _check(mx, x, topk, score, **kw):
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 5, 5), (7, 64, 1), (33, 65, 8), (130, 128, 8), (61, 160, 6),
-                                   (29, 256, 17), (18, 513, 32), (9, 1024, 8)])
+                                   (29, 256, 17), (18, 513, 32), (9, 1024, 8), (40, 500, 8), (21, 1000, 4), (50, 100, 3),
+                                   (13, 260, 9)])
 def test_route_and_gradient(gpu_lib, T, E, k, renorm, score):
     rng = np.random.default_rng(T * E + k)
     for dtype in (torch.float32, torch.bfloat16):
@@ -268,7 +269,7 @@ def test_route_empty_and_deterministic(gpu_lib):
 
 
 @pytest.mark.parametrize("T,H,k", [(1, 8, 1), (1, 2048, 8), (5, 64, 3), (33, 520, 8), (17, 1024, 9), (40, 2048, 8),
-                                   (11, 4104, 20), (300, 256, 2)])
+                                   (11, 4104, 20), (300, 256, 2), (3, 7168, 8), (514, 2056, 3)])
 def test_combine_bwd(gpu_lib, T, H, k):
     mx = gpu_lib
     rng = np.random.default_rng(T + H + k)

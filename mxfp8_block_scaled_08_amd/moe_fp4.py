@@ -15,8 +15,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import (_OUT, MX_BF16, MX_F32, _check, _ld, _u8, load, mx_moe_dispatch_workspace_bytes,
-               mx_scale_swizzled_bytes)
+from . import _OUT, MX_BF16, MX_F32, _check, _u8, load, mx_moe_dispatch_workspace_bytes
 
 MX_SCORE_SOFTMAX, MX_SCORE_SIGMOID = 0, 1
 
@@ -291,23 +290,21 @@ def mx_quantize_colwise_fp4(x: torch.Tensor, qt: Optional[torch.Tensor] = None, 
     dev = x.device
     if stream is not None or dev.index is None or dev.index != _current():
         return _elsewhere(mx_quantize_colwise_fp4, locals())
+    bf = torch.bfloat16
     if x.dim() == 3:
         count, rows, cols = x.shape
         if not x.is_contiguous():
             raise ValueError("a stack must be contiguous [count][rows][cols]")
-        flat, shape = x.view(count * rows, cols), (count, cols, rows // 2)
+        px, ld_x = _first_rows(x, "x", count * rows, cols, bf)
+        qt, pq = _out_at(qt, "qt", dev, _U8, count, cols, rows // 2)
+        ld_qt = rows // 2
     else:
         (rows, cols), count = x.shape, 1
-        flat, shape = x, (cols, rows // 2)
-    if qt is None:
-        qt = torch.empty(shape, dtype=_U8, device=dev)
-    if tuple(qt.shape) != shape or (x.dim() == 3 and not qt.is_contiguous()):
-        raise ValueError(f"qt must be {list(shape)}, and contiguous for a stack, got {list(qt.shape)}")
-    need = count * mx_scale_swizzled_bytes(cols, rows // 32)
+        px, ld_x = _first_rows(x, "x", rows, cols, bf)
+        qt, pq, ld_qt = _out_rows(qt, "qt", dev, cols, rows // 2, _U8)
+    need = count * _scale_bytes(cols, rows, rows // 256)
     if st_swz is None:
         st_swz = torch.empty(max(need, 1), dtype=_U8, device=dev)
-    px, ld_x = _rows(flat, "x", dev, count * rows, cols, torch.bfloat16)
-    pq, ld_qt = _rows(qt.view(count * cols, rows // 2) if x.dim() == 3 else qt, "qt", dev, count * cols, rows // 2, _U8)
     _call("mx_quantize_colwise_fp4", dev, px, count, rows, cols, ld_x, pq, ld_qt,
           _scale_ptr(st_swz, "st_swz", dev, need))
     return qt, st_swz
@@ -347,24 +344,17 @@ def mx_moe_dispatch_fp4(x: torch.Tensor, topk_ids: torch.Tensor, num_experts: in
     topk = topk_ids.shape[1]
     n = tokens * topk
     i32 = torch.int32
-    if offsets is None:
-        offsets = torch.empty(num_experts + 1, dtype=torch.int64, device=dev)
-    if src is None:
-        src = torch.empty(n, dtype=i32, device=dev)
-    if slot is None:
-        slot = torch.empty(n, dtype=i32, device=dev)
-    if q is None:
-        q = torch.empty((n, hidden // 2), dtype=_U8, device=dev)
+    px, ld_x = _first_rows(x, "x", tokens, hidden, torch.bfloat16)
+    pi = _at(topk_ids, "topk_ids", dev, i32, (tokens, topk))
+    offsets, po = _out_at(offsets, "offsets", dev, torch.int64, num_experts + 1)
+    src, pr = _out_at(src, "src", dev, i32, n)
+    slot, pl = _out_at(slot, "slot", dev, i32, n)
+    q, pq, ld_q = _out_rows(q, "q", dev, n, hidden // 2, _U8)
     s_swz, ps = _scales(s_swz, n, hidden, hidden // 256, "s_swz", dev)
-    need = mx_moe_dispatch_workspace_bytes(tokens, topk, num_experts)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=_U8, device=dev)
-    px, ld_x = _rows(x, "x", dev, tokens, hidden, torch.bfloat16)
-    pq, ld_q = _rows(q, "q", dev, n, hidden // 2, _U8)
-    _call("mx_moe_dispatch_fp4", dev, px, tokens, hidden, ld_x, _at(topk_ids, "topk_ids", dev, i32, (tokens, topk)),
-          topk, num_experts, _at(offsets, "offsets", dev, torch.int64, (num_experts + 1,)),
-          _at(src, "src", dev, i32, (n,)), _at(slot, "slot", dev, i32, (n,)), pq, ld_q, ps,
-          *_scratch(workspace, dev))
+        workspace = torch.empty(max(mx_moe_dispatch_workspace_bytes(tokens, topk, num_experts), 1), dtype=_U8, device=dev)
+    pw, nw = _scratch(workspace, dev)
+    _call("mx_moe_dispatch_fp4", dev, px, tokens, hidden, ld_x, pi, topk, num_experts, po, pr, pl, pq, ld_q, ps, pw, nw)
     return offsets, src, slot, q, s_swz
 
 
@@ -385,14 +375,12 @@ def mx_swiglu_quantize_fp4(gu: torch.Tensor, q: Optional[torch.Tensor] = None, s
         return _elsewhere(mx_swiglu_quantize_fp4, locals())
     rows, F2 = gu.shape
     F = F2 // 2
-    if q is None:
-        q = torch.empty((rows, F // 2), dtype=_U8, device=dev)
+    pg, ld_gu = _first_rows(gu, "gu", rows, F2, torch.bfloat16)
+    ph, ld_h = None, 0
+    if h is not None or want_h:
+        h, ph, ld_h = _out_rows(h, "h", dev, rows, F, torch.bfloat16)
+    q, pq, ld_q = _out_rows(q, "q", dev, rows, F // 2, _U8)
     s_swz, ps = _scales(s_swz, rows, F, F // 256, "s_swz", dev)
-    if h is None and want_h:
-        h = torch.empty((rows, F), dtype=torch.bfloat16, device=dev)
-    pg, ld_gu = _rows(gu, "gu", dev, rows, F2, torch.bfloat16)
-    ph, ld_h = _rows(h, "h", dev, rows, F, torch.bfloat16) if h is not None else (None, 0)
-    pq, ld_q = _rows(q, "q", dev, rows, F // 2, _U8)
     _call("mx_swiglu_quantize_fp4", dev, pg, rows, F, ld_gu, ph, ld_h, pq, ld_q, ps)
     return q, s_swz, h
 

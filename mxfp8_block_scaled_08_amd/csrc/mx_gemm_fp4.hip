@@ -77,7 +77,9 @@ constexpr int FMT_E2M1 = 4;  // the instruction's operand format code
 // which is most of what there is to read, goes straight to registers in the
 // matrix cores' layout, up to MAXG groups (2 KiB each) in flight a wave, and
 // stays there while the rows of A pass, 16 * MT after another; A comes out of
-// L2.  Bound by reading B: one row x 24576x4096 (53 MB) takes 12.3 us, 4.4 TB/s;
+// L2.  (Two sets of two groups of both operands, one multiplied while the other
+// loads, are slower: 1x24576x4096 15.4 us instead of 13.7.)
+// Bound by reading B: one row x 24576x4096 (53 MB) takes 12.3 us, 4.4 TB/s;
 // x 6144x4096 4.6 us, of which an empty launch is 2.4.  With four waves a tile
 // and one group in flight, as at first, x 4096x12288 took 16.7 us instead of 7.2;
 // dividing by the split instead of shifting costs 0.2 us before the first load.
@@ -1067,7 +1069,9 @@ __global__ __launch_bounds__(256) void split4_reduce_kernel(Gemm4Params p)
 static int64_t scale_bytes(int64_t rows, int64_t K) { return ((rows + 31) / 32) * (K / 256) * 256; }
 
 // Log2 of the waves that share a column tile along K, so that about 8 waves a
-// compute unit have loads in flight (`tiles`: column tiles that have rows).
+// compute unit have loads in flight (`tiles`: column tiles that have rows).  With
+// 16 a unit 1x6144x4096 takes 6.9 us instead of 5.9, 1x24576x4096 13.6 instead of
+// 14.0, out of HBM both; most shapes are the same.
 static int k_split(int64_t tiles, int64_t KT, int64_t cus)
 {
     int log = 0;

@@ -101,8 +101,9 @@ mx_status mx_moe_route(const void *logits, int logits_dtype, int64_t tokens, int
  *              twice in a row counts twice
  *   d_weights  DEVICE float [tokens][topk]
  *   d_logits   [tokens][ld_d] of logits_dtype out: all num_experts columns of
- *              every row are written (zeros where nothing flows), computed in
- *              FP32 and rounded once
+ *              every row are written (zeros where nothing flows: all of a row
+ *              without a valid id, a masked token's, whose logits are not read),
+ *              computed in FP32 and rounded once
  * Requirements as mx_moe_route's, with topk in 1..MX_ROUTE_MAX_TOPK and
  * ld_d >= num_experts.
  */

@@ -434,7 +434,11 @@ __global__ __launch_bounds__(RT_THREADS) void route_bwd_kernel(RouteBwdParams p)
     float pr[EPL];
     float total = 1.0f;
     if (full) {
-        load_logits<EPL, DT>(p.logits, row, l * EPL, p.experts, live, p.vec != 0, pr);
+        // A row without a chosen expert (a masked token's, whose logits may hold
+        // anything) is not read and counts as -inf throughout: zeros flow.
+        const uint64_t chosen = __ballot(id[0] >= 0 || id[NSEL - 1] >= 0) >> (lane & ~(LANES - 1));
+        const bool any = (chosen & (~0ull >> (64 - LANES))) != 0;
+        load_logits<EPL, DT>(p.logits, row, l * EPL, p.experts, any, p.vec != 0, pr);
 #pragma unroll
         for (int i = 0; i < EPL; i++)
             mx = max_nan(mx, pr[i]);

@@ -264,6 +264,33 @@ def test_route_empty_and_deterministic(gpu_lib):
         assert torch.equal(c[0], e[0]) and torch.equal(c[1], e[1])
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k", [(37, 40, 3), (50, 128, 8), (41, 256, 17), (19, 1000, 8), (4301, 128, 8), (2303, 512, 4)])
+def test_gradient_of_masked_rows(gpu_lib, T, E, k, score):
+    """A masked token's logits may hold anything: its gradient is zero, that of
+    the other rows the one they have alone.  So for rows of -inf alone."""
+    mx = gpu_lib
+    rng = np.random.default_rng(T + E)
+    mask = torch.from_numpy((rng.random(T) < 0.6).astype(np.uint8)).cuda()
+    mask[:6] = 0
+    mask[6] = 1
+    for dtype in (torch.float32, torch.bfloat16):
+        clean = _logits(rng, T, E, dtype).cuda()
+        clean[6] = -float("inf")
+        x = clean.clone()
+        x[mask == 0] = float("nan")
+        x[1], x[2], x[3, 5], x[4] = float("inf"), -float("inf"), float("inf"), 0.0
+        g = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).cuda()
+        live = mask == 1
+        for renorm in (True, False):
+            how = dict(score=score, renormalize=renorm, scale=1.5)
+            ids, w = mx.mx_moe_route(x, k, mask=mask, **how)
+            assert (ids[~live] == -1).all() and (w[~live] == 0).all() and (ids[6] == -1).all()
+            dx = mx.mx_moe_route_bwd(g, x, ids, **how)
+            assert (dx[~live] == 0).all() and (dx[6] == 0).all() and torch.isfinite(dx).all()
+            assert torch.equal(dx[live], mx.mx_moe_route_bwd(g, clean, ids, **how)[live])
+
+
 # ---------------------------------------------------------------------------
 # the combine's gradient
 

@@ -224,9 +224,11 @@ mx_status mx_gemm_fp4(int64_t M, int64_t N, int64_t K, const void *a_q, int64_t 
 
 /*
  * Grouped MXFP4 product: mx_grouped_gemm's row groups and offsets with MXFP4
- * operands (b_q E2M1 [num_groups][N][K/2 bytes] contiguous).  Rows of C
- * outside every group are not written.  Requirements as mx_grouped_gemm's
- * with K % 256 == 0.  Few rows per expert (a sampler's step) stream each
+ * operands (b_q E2M1 [num_groups][N][K/2 bytes] contiguous).  group_offsets
+ * [num_groups] may lie below M_total, as mx_moe_dispatch_fp4 leaves it where
+ * assignments are not routed (M_total = tokens*topk): rows of A and its scales
+ * outside every group are not used, rows of C not written.  Other requirements
+ * as mx_grouped_gemm's with K % 256 == 0.  Few rows per expert (a sampler's step) stream each
  * routed expert's weights once; more take tiles of 128x128 or 256x256.  The
  * rule goes by M_total, num_groups, N, K and the device's compute-unit count, so
  * the offsets are read on the device alone.

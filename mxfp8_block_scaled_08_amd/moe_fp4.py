@@ -433,7 +433,8 @@ def mx_grouped_gemm_fp4(group_offsets: torch.Tensor, a_q: torch.Tensor, a_s_swz:
                         b_s_swz: torch.Tensor, c: Optional[torch.Tensor] = None,
                         out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """Per-expert C: rows [off[g], off[g+1]) of A times B_g^T, B as
-    [G][N][K/2 bytes], MXFP4.  Rows outside every group are not written."""
+    [G][N][K/2 bytes], MXFP4.  off[G] may be less than A's rows (unrouted
+    assignments); rows outside every group are not written."""
     dev = group_offsets.device
     if stream is not None or dev.index is None or dev.index != _current():
         return _elsewhere(mx_grouped_gemm_fp4, locals())

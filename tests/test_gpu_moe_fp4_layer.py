@@ -506,3 +506,36 @@ def test_binding_refusals(gpu_lib):
         a, sa = _random_operand(g, 200, 12288)
         b, sb = _random_operand(g, 4096, 12288)
         mx.mx_gemm_fp4(a, sa, b, sb, workspace=torch.empty(1024, dtype=torch.uint8, device=dev))
+
+
+# ---------------------------------------------------------------------------
+# padded batches, uneven loads, strides, arguments that exclude each other
+
+
+@pytest.mark.parametrize("T", [4, 300])
+def test_padded_batch_under_the_debug_check(gpu_lib, monkeypatch, T):
+    """Unrouted tokens leave rows behind the last expert's: the products take
+    offsets that end below M_total, with MX_DEBUG too, and keep those rows of C."""
+    mx = gpu_lib
+    E, k, H, F = 8, 2, 256, 256
+    x = mxsynth.normal_bf16((T, H), 1.0, seed=1).to(dev)
+    logits = torch.randn(T, E, generator=torch.Generator().manual_seed(2)).to(dev)
+    mask = torch.ones(T, dtype=torch.bool, device=dev)
+    mask[T // 2:] = False
+    logits[~mask], x[~mask] = float("nan"), float("nan")
+    W = _weights(mx, E, H, F, 5)
+    want, f = _forward(mx, x, logits, W, E, k, mask=mask)
+    n = int(f["off"][-1])
+    assert n == T // 2 * k
+    monkeypatch.setenv("MX_DEBUG", "1")
+    o = dict(gu=torch.full((T * k, 2 * F), 7.0, dtype=torch.bfloat16, device=dev),
+             y=torch.full((T * k, H), 7.0, dtype=torch.bfloat16, device=dev))
+    out, f = _forward(mx, x, logits, W, E, k, o=o, mask=mask)
+    assert torch.equal(out, want) and (out[~mask] == 0).all() and torch.isfinite(out).all()
+    assert (f["gu"][n:] == 7).all() and (f["y"][n:] == 7).all()
+    b = _backward(mx, torch.ones_like(out), logits, f, W)
+    assert (b["dx"][~mask] == 0).all() and torch.isfinite(b["dx"]).all() and torch.isfinite(b["dh"][:n]).all()
+    # what the check is for is still refused
+    for bad, at in (([1, 1, 2], 0), ([0, 2, 1], 2), ([0, 1, n + T * k], 2)):
+        with pytest.raises(mx.MxError, match=rf"group_offsets\[{at}\]"):
+            mx.mx_grouped_gemm_fp4(torch.tensor(bad, device=dev), f["q"], f["s"], W["gu"][0][:2].contiguous(), W["gu"][1])

@@ -67,10 +67,11 @@ typedef enum mx_score {
  *              scale * s / (sum of the chosen s)
  * Selection score: s + bias formed in 64 bits and compared to 42 bits of its
  * mantissa; without a bias and with group_top 1 the logit itself (the same
- * order, exactly).  An expert whose logit is -inf is never chosen and counts as
- * -inf in its group's score (so with group_top 2 a group with one expert left
- * ranks last); groups of equal score rank by number; where
- * fewer than topk can be, the remaining ids are -1 (which mx_moe_dispatch
+ * order, exactly).  An expert whose logit is -inf is never chosen and takes no
+ * part in its group's score; with group_top 2 a group with one expert left ranks
+ * below every group with more, among such groups by that expert's score, and a
+ * group with none ranks last; groups of equal score rank by number.  Where
+ * fewer than topk can be chosen, the remaining ids are -1 (which mx_moe_dispatch
  * does not route) and their weights 0, as for a masked token.  Renormalized
  * weights are formed from score ratios, so they sum to scale however small
  * the chosen scores are.

@@ -180,6 +180,17 @@ __device__ __forceinline__ double key_score(double k)
     return k > KEY_NONE ? __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, k) & ~1023ull) : -(double)INFINITY;
 }
 
+// Score, where two are summed, of a group with one expert left: below every sum
+// (these numbers are under -2^1018), in the order of that expert's score a, and
+// above -inf, an empty group's.  a's 54 bits (the key's low 10 are clear), as a
+// whole number in a's order, are taken off the largest magnitude's pattern.
+__device__ __forceinline__ double lone_score(double a)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, a);
+    const uint64_t order = ((b >> 63) ? ~b : b | (1ull << 63)) >> 10;
+    return a > KEY_NONE ? __builtin_bit_cast(double, 0xFFEFFFFFFFFFFFFFull - order) : -(double)INFINITY;
+}
+
 // Shift of a row's exponentials by its largest logit; -inf rows (nothing to
 // choose) shift by zero.
 __device__ __forceinline__ float shift_of(float mx) { return mx == -INFINITY ? 0.0f : mx; }
@@ -297,7 +308,7 @@ __global__ __launch_bounds__(RT_THREADS) void route_kernel(RouteParams p)
                 a = max_key(a, a2);
             }
             if (g < p.groups && part == 0)
-                score[g] = p.group_top > 1 ? a + b : a;
+                score[g] = p.group_top < 2 ? a : b == -(double)INFINITY ? lone_score(a) : a + b;
         }
         __syncthreads();
         uint64_t kept = 0;

@@ -291,6 +291,38 @@ def test_gradient_of_masked_rows(gpu_lib, T, E, k, score):
             assert torch.equal(dx[live], mx.mx_moe_route_bwd(g, clean, ids, **how)[live])
 
 
+@pytest.mark.parametrize("T,E,G,bias", [(9, 32, 4, False), (9, 256, 8, True), (5, 60, 20, True), (3, 1024, 64, False),
+                                        (4301, 128, 8, True)])
+def test_groups_of_two_with_experts_missing(gpu_lib, T, E, G, bias):
+    """group_top 2 where -inf leaves a group one expert or none: groups of two
+    and more first, then those of one by its score, empty ones last, so that a
+    token keeps an expert as long as one can be chosen."""
+    mx = gpu_lib
+    size = E // G
+    b = torch.linspace(-0.4, 0.4, E).cuda() if bias else None
+    x = torch.full((T, E), -float("inf"))
+    x[:, E - 1] = -3.0                                  # the last group alone has an expert
+    for score in ("softmax", "sigmoid"):
+        how = dict(score=score, bias=b, num_groups=G, group_top=2)
+        ids, w = mx.mx_moe_route(x.cuda(), 2, topk_groups=1, **how)
+        assert (ids[:, 0] == E - 1).all() and (ids[:, 1] == -1).all()
+        assert (w[:, 0] == 1).all() and (w[:, 1] == 0).all()
+        y = x.clone()
+        y[:, size] = 4.0                                # group 1: one expert of a larger score
+        ids, _ = mx.mx_moe_route(y.cuda(), 2, topk_groups=1, **how)
+        assert (ids[:, 0] == size).all() and (ids[:, 1] == -1).all()
+        ids, _ = mx.mx_moe_route(y.cuda(), 2, topk_groups=2, **how)
+        assert (ids[:, 0] == size).all() and (ids[:, 1] == E - 1).all()
+        y[:, 2 * size:2 * size + 2] = -3.0              # group 2: two of smaller ones
+        ids, _ = mx.mx_moe_route(y.cuda(), 2, topk_groups=1, **how)
+        assert (ids.sort(1).values == torch.tensor([2 * size, 2 * size + 1]).cuda()).all()
+        ids, _ = mx.mx_moe_route(y.cuda(), 4, topk_groups=3, **how)
+        assert (ids[:, 0] == size).all()
+        assert (ids.sort(1).values == torch.tensor([size, 2 * size, 2 * size + 1, E - 1]).cuda()).all()
+        ids, w = mx.mx_moe_route(torch.full_like(x, -float("inf")).cuda(), 2, topk_groups=1, **how)
+        assert (ids == -1).all() and (w == 0).all()
+
+
 # ---------------------------------------------------------------------------
 # the combine's gradient
 

@@ -75,8 +75,12 @@ typedef enum mx_score {
  * does not route) and their weights 0, as for a masked token.  Renormalized
  * weights are formed from score ratios, so they sum to scale however small
  * the chosen scores are.
- * A NaN logit ranks above every number, +inf next; the weights they take part
- * in are NaN (except +inf's sigmoid, which is 1), the ids stay in range.
+ * NaN and +inf: a NaN logit ranks above every number and, where logits are
+ * compared, +inf next.  Where scores are compared (a bias, or group_top 2), a
+ * softmax row that holds a NaN or +inf has no scores and ranks by its logits in
+ * that order, without the bias; a sigmoid's +inf has the score 1.  The weights
+ * they take part in are NaN (except +inf's sigmoid, which is 1), the ids stay in
+ * range.
  * Requirements: tokens >= 0, num_experts in 1..1024, 1 <= topk <=
  * min(MX_ROUTE_MAX_TOPK, topk_groups * num_experts / num_groups),
  * num_experts % num_groups == 0, 1 <= topk_groups <= num_groups, group_top 1

@@ -148,9 +148,9 @@ template <int LANES> __device__ __forceinline__ float max_of(float v)
 }
 
 // Selection keys.  Scores are at most FLT_MAX in magnitude (or a few units);
-// NaN becomes DBL_MAX's pattern and +inf half of it, above every score.  For
-// positive scores the larger low bits win, for negative ones the smaller.  What
-// cannot be chosen is below KEY_NONE.
+// NaN becomes DBL_MAX's pattern and +inf a quarter of it, above every score and
+// two +inf together below a NaN.  For positive scores the larger low bits win,
+// for negative ones the smaller.  What cannot be chosen is below KEY_NONE.
 constexpr double KEY_NONE = -1e300;
 constexpr uint32_t KEY_GONE_HI = 0xFFEFFFFFu;  // upper word of a key that was taken: about -DBL_MAX
 
@@ -163,7 +163,7 @@ __device__ __forceinline__ double make_key(double v, int e)
     if (v != v)
         b = 0x7FEFFFFFFFFFFFFFull;
     if (v == (double)INFINITY)
-        b = 0x7FDFFFFFFFFFFFFFull;
+        b = 0x7FCFFFFFFFFFFFFFull;
     if (v == -(double)INFINITY)
         return __builtin_bit_cast(double, (uint64_t)KEY_GONE_HI << 32);
     return __builtin_bit_cast(double, (b & ~1023ull) | (uint64_t)((b >> 63) ? e : 1023 - e));

@@ -323,6 +323,35 @@ def test_groups_of_two_with_experts_missing(gpu_lib, T, E, G, bias):
         assert (ids == -1).all() and (w == 0).all()
 
 
+@pytest.mark.parametrize("E", [32, 128, 256, 1024])
+def test_order_of_nan_and_inf(gpu_lib, E):
+    """Logits compared: NaN, then +inf, then numbers.  Scores compared: a softmax
+    row with either ranks by its logits in that order, the bias left out; with
+    sigmoid NaN is first and +inf has the score 1."""
+    mx = gpu_lib
+    nan, inf = float("nan"), float("inf")
+    x = torch.linspace(-2, 2, E).repeat(3, 1)
+    x[0, 9], x[0, 3] = nan, inf
+    x[1, 3] = inf
+    x[2, 9] = nan
+    bias = torch.zeros(E)
+    bias[20], bias[9] = 5.0, -5.0
+    top = E - 1
+    for score in ("softmax", "sigmoid"):
+        ids = mx.mx_moe_route(x.cuda(), 3, score=score)[0].cpu()
+        assert ids.tolist() == [[9, 3, top], [3, top, top - 1], [9, top, top - 1]]
+    ids = mx.mx_moe_route(x.cuda(), 3, bias=bias.cuda())[0].cpu()
+    assert ids.tolist() == [[9, 3, top], [3, top, top - 1], [9, top, top - 1]]
+    ids = mx.mx_moe_route(x.cuda(), 3, score="sigmoid", bias=bias.cuda())[0].cpu()
+    assert ids.tolist() == [[9, 20, 3], [20, 3, top], [9, 20, top]]
+    # groups of the same: one that holds a NaN ranks above one of two +inf
+    y = torch.linspace(-2, 2, E).repeat(2, 1)
+    y[0, :2], y[0, E // 4] = inf, nan
+    y[1, :2], y[1, E // 4 + 1] = inf, 1.0
+    ids = mx.mx_moe_route(y.cuda(), 1, num_groups=4, topk_groups=1, group_top=2)[0].cpu()
+    assert ids.tolist() == [[E // 4], [0]]
+
+
 # ---------------------------------------------------------------------------
 # the combine's gradient
 

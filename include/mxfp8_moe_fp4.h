@@ -233,9 +233,10 @@ mx_status mx_gemm_fp4(int64_t M, int64_t N, int64_t K, const void *a_q, int64_t 
  * [num_groups] may lie below M_total, as mx_moe_dispatch_fp4 leaves it where
  * assignments are not routed (M_total = tokens*topk): rows of A and its scales
  * outside every group are not used, rows of C not written.  Other requirements
- * as mx_grouped_gemm's with K % 256 == 0.  Few rows per expert (a sampler's step) stream each
- * routed expert's weights once; more take tiles of 128x128 or 256x256.  The
- * rule goes by M_total, num_groups, N, K and the device's compute-unit count, so
+ * as mx_grouped_gemm's with K % 256 == 0.  Few rows per expert (a sampler's
+ * step) stream a routed expert's weights once for every 64 of its rows; more
+ * take tiles of 128x128 or 256x256.  The rule goes by M_total, num_groups, N, K
+ * and the device's compute-unit count, so
  * the offsets are read on the device alone.
  */
 mx_status mx_grouped_gemm_fp4(int64_t num_groups, int64_t M_total, int64_t N, int64_t K, const int64_t *group_offsets,

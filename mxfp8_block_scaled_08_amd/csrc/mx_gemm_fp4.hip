@@ -71,36 +71,162 @@ __device__ __forceinline__ v8i half_of(v8i x, int s)
 constexpr int ROWS_CHUNK = 64;  // few rows: rows of one workgroup
 constexpr int FMT_E2M1 = 4;  // the instruction's operand format code
 
-// Few rows.  A wave takes 16 columns of C and a range of 256-K groups, of up to
-// 16 * MT rows at a time; 2^ks_log waves of a workgroup share the columns, each
+// Few rows.  A wave takes 16 columns of C and a range of 256-K groups, of a chunk
+// of up to 16 * MT rows; 2^ks_log waves of a workgroup share the columns, each
 // with its own range of K, and their sums meet in LDS, added in K order.  B,
 // which is most of what there is to read, goes straight to registers in the
-// matrix cores' layout, up to MAXG groups (2 KiB each) in flight a wave, and
-// stays there while the rows of A pass, 16 * MT after another; A comes out of
+// matrix cores' layout, MAXG groups (2 KiB each) in flight a wave, once a chunk:
+// all its rows pass while a group of B is there.  (Experts' chunks in passes of 16
+// rows that read B each, as at first: 17, 0, 30, 1, 16, 0, 64 and 0 rows x
+// 3968x12288 96 us, so 69; 128 rows on one of 8 experts 68, so 39.)  A comes out of
 // L2.  (Two sets of two groups of both operands, one multiplied while the other
-// loads, are slower: 1x24576x4096 15.4 us instead of 13.7.)
-// Bound by reading B: one row x 24576x4096 (53 MB) takes 12.3 us, 4.4 TB/s;
-// x 6144x4096 4.6 us, of which an empty launch is 2.4.  With four waves a tile
-// and one group in flight, as at first, x 4096x12288 took 16.7 us instead of 7.2;
+// loads, take 12 % longer for 1x24576x4096.)
+// Bound by reading B: out of HBM one row x 24576x4096 (53 MB) takes 12.6 us, 4.2
+// TB/s, x 6144x4096 5.8 us, of which an empty launch is 1.6.  With four waves a
+// tile and one group in flight, as at first, x 4096x12288 took 2.3 times as long;
 // dividing by the split instead of shifting costs 0.2 us before the first load.
-template <bool GROUPED, int CT, int MT, int MAXG>
-__global__ __launch_bounds__(1024) void gemm4_rows_kernel(Gemm4Params p)
+template <int CT, int MT, int MAXG>
+__device__ __forceinline__ void rows_chunk(const Gemm4Params &p, float *part, const uint8_t *B, const uint8_t *BS,
+                                           int64_t lo, int64_t hi, int64_t first_tn)
 {
-    extern __shared__ __attribute__((aligned(16))) float part[];  // [waves][MT][64][4]
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int ks = 1 << p.ks_log, per_block = 1 << p.pb_log;
     const int kp = wave & (ks - 1);
     const int r = lane & 15, g = lane >> 4;
+    const int64_t tn = first_tn + (wave >> p.ks_log);
+    const int KT = (int)(p.K / 256);
+    const int g0 = kp * KT >> p.ks_log, g1 = (kp + 1) * KT >> p.ks_log;
+    // (a column tile past the last: an empty range, nothing stored)
+    const int64_t n0 = min(tn * 16, p.N);
+    const int rows_n = (int)min(p.N - n0, (int64_t)16);
+    const __amdgpu_buffer_rsrc_t rb = byte_range(B + n0 * p.ld_b, (uint32_t)(rows_n * p.ld_b));
+    const __amdgpu_buffer_rsrc_t rbs = byte_range(BS, p.bs_bytes), ras = byte_range(p.as, p.as_bytes);
+    const uint32_t stile = (uint32_t)KT * 256;
+    const int sh = 8 * (g >> 1);
+    const uint32_t brow = (uint32_t)n0 + r;  // (rows past N: zero codes, any scale)
+    const uint32_t bs_off = (brow >> 5) * stile + (32 * (g & 1) + (brow & 31)) * 4;
+    const uint32_t b_off = (uint32_t)(r * p.ld_b + g * 16);
+    v4i xb[MAXG][2];
+    uint32_t wb[MAXG];
+    auto load_b = [&](int gb) {
+#pragma unroll
+        for (int q = 0; q < MAXG; q++) {
+            const bool in = gb + q < g1;
+            wb[q] = in ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rbs, bs_off, (uint32_t)(gb + q) * 256, 0) : 0u;
+#pragma unroll
+            for (int s = 0; s < 2; s++)
+                xb[q][s] = in ? __builtin_amdgcn_raw_buffer_load_b128(rb, b_off + (uint32_t)s * 64,
+                                                                      (uint32_t)(gb + q) * 128, STREAM)
+                              : v4i{0, 0, 0, 0};
+        }
+    };
+    load_b(g0);
+    const int rows_m = (int)(hi - lo);
+    const __amdgpu_buffer_rsrc_t ra = byte_range(p.a + lo * p.ld_a, (uint32_t)(rows_m * p.ld_a));
+    uint32_t as_off[MT], a_off[MT];
+#pragma unroll
+    for (int i = 0; i < MT; i++) {
+        const uint32_t row = (uint32_t)lo + 16 * i + r;
+        as_off[i] = (row >> 5) * stile + (32 * (g & 1) + (row & 31)) * 4;
+        a_off[i] = (uint32_t)((16 * i + r) * p.ld_a + g * 16);
+    }
+    v4f acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; i++)
+        acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int gb = g0; gb < g1;) {
+#pragma unroll
+        for (int q = 0; q < MAXG; q++) {
+            if (gb + q >= g1)
+                break;
+#pragma unroll
+            for (int i = 0; i < MT; i++) {
+                const uint32_t wa =
+                    (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(ras, as_off[i], (uint32_t)(gb + q) * 256, 0) >> sh;
+                auto step = [&](auto S_) {
+                    constexpr int s = decltype(S_)::value;
+                    const v4i xa = __builtin_amdgcn_raw_buffer_load_b128(ra, a_off[i] + (uint32_t)s * 64,
+                                                                         (uint32_t)(gb + q) * 128, 0);
+                    acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        widen(xb[q][s]), widen(xa), acc[i], FMT_E2M1, FMT_E2M1, 2 * s, (int)(wb[q] >> sh), 2 * s,
+                        (int)wa);
+                };
+                step(std::integral_constant<int, 0>{});
+                step(std::integral_constant<int, 1>{});
+            }
+        }
+        gb += MAXG;
+        if (gb < g1)
+            load_b(gb);
+    }
+    // fragment i: lane (r, g) holds row lo + 16i + r, columns c0 + 4g .. +3
+    auto store = [&](int64_t c0, int i, int ln, v4f v) {
+        const int64_t m = lo + 16 * i + (ln & 15), n = c0 + 4 * (ln >> 4);
+        if (m >= hi || n >= p.N)
+            return;
+        const int64_t at = m * p.ld_c + n;
+        if (CT == 0) {
+            uint16_t *c = reinterpret_cast<uint16_t *>(p.c) + at;
+            typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+            const bf16x4_t w = __builtin_convertvector(v, bf16x4_t);
+            if (p.vec_store && n + 3 < p.N)
+                *reinterpret_cast<uint2 *>(c) = __builtin_bit_cast(uint2, w);
+            else
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    if (n + e < p.N)
+                        c[e] = __builtin_bit_cast(uint16_t, (__bf16)w[e]);
+        } else {
+            float *c = reinterpret_cast<float *>(p.c) + at;
+            if (p.vec_store && n + 3 < p.N)
+                *reinterpret_cast<v4f *>(c) = v;
+            else
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    if (n + e < p.N)
+                        c[e] = v[e];
+        }
+    };
+    if (p.ks_log == 0) {
+#pragma unroll
+        for (int i = 0; i < MT; i++)
+            store(tn * 16, i, lane, acc[i]);
+        return;
+    }
+    v4f *sums = reinterpret_cast<v4f *>(part);
+#pragma unroll
+    for (int i = 0; i < MT; i++)
+        sums[(wave * MT + i) * 64 + lane] = acc[i];
+    __syncthreads();
+    for (int u = tid; u < per_block * MT * 64; u += blockDim.x) {
+        const int tile = u / (MT * 64), rest = u - tile * (MT * 64);
+        v4f v = sums[tile * ks * MT * 64 + rest];
+#pragma unroll 1
+        for (int w = 1; w < ks; w++)
+            v += sums[(tile * ks + w) * MT * 64 + rest];
+        store((first_tn + tile) * 16, rest / 64, rest & 63, v);
+    }
+}
+
+// The kernel: the workgroup's chunk of rows, then rows_chunk of it.  MT 16-row
+// fragments hold a chunk; a grouped product with chunks of more than 16 rows (MT
+// 4) takes for each the fewest that hold it.
+template <bool GROUPED, int CT, int MT>
+__global__ __launch_bounds__(1024) void gemm4_rows_kernel(Gemm4Params p)
+{
+    extern __shared__ __attribute__((aligned(16))) float part[];  // [waves][MT][64][4]
+    const int lane = threadIdx.x & 63;
     // the workgroups are numbered over the chunks of up to ROWS_CHUNK rows (of
     // an expert, when grouped: experts without rows have none), a chunk's
     // column tiles after each other
     // (a dense product has one chunk; grid and tile numbers are below 2^32)
-    const uint32_t blocks_n = ((uint32_t)p.tiles_n + per_block - 1) >> p.pb_log;
+    const uint32_t blocks_n = ((uint32_t)p.tiles_n + (1 << p.pb_log) - 1) >> p.pb_log;
     const uint32_t rank = GROUPED ? blockIdx.x / blocks_n : 0;
-    const int64_t first_tn = (int64_t)(blockIdx.x - rank * blocks_n) << p.pb_log, tn = first_tn + (wave >> p.ks_log);
+    const int64_t first_tn = (int64_t)(blockIdx.x - rank * blocks_n) << p.pb_log;
     int64_t lo = (int64_t)rank * ROWS_CHUNK, hi = min(lo + ROWS_CHUNK, p.M);
     const uint8_t *B = p.b, *BS = p.bs;
+    int rows = 0;  // of an expert's chunk
     if (GROUPED) {
         int before = 0, grp = -1;  // chunks of the experts so far; the chunk's expert
         for (int e0 = 0; e0 < (int)p.G && grp < 0; e0 += 64) {
@@ -133,122 +259,15 @@ __global__ __launch_bounds__(1024) void gemm4_rows_kernel(Gemm4Params p)
         grp = __builtin_amdgcn_readfirstlane(grp);
         B += grp * p.b_group_stride;
         BS += grp * p.bs_group_stride;
+        if (MT > 1)
+            rows = __builtin_amdgcn_readfirstlane((int)(hi - lo));
     }
-    const int KT = (int)(p.K / 256);
-    const int g0 = kp * KT >> p.ks_log, g1 = (kp + 1) * KT >> p.ks_log;
-    // (a column tile past the last: an empty range, nothing stored)
-    const int64_t n0 = min(tn * 16, p.N);
-    const int rows_n = (int)min(p.N - n0, (int64_t)16);
-    const __amdgpu_buffer_rsrc_t rb = byte_range(B + n0 * p.ld_b, (uint32_t)(rows_n * p.ld_b));
-    const __amdgpu_buffer_rsrc_t rbs = byte_range(BS, p.bs_bytes), ras = byte_range(p.as, p.as_bytes);
-    const uint32_t stile = (uint32_t)KT * 256;
-    const int sh = 8 * (g >> 1);
-    const uint32_t brow = (uint32_t)n0 + r;  // (rows past N: zero codes, any scale)
-    const uint32_t bs_off = (brow >> 5) * stile + (32 * (g & 1) + (brow & 31)) * 4;
-    const uint32_t b_off = (uint32_t)(r * p.ld_b + g * 16);
-    v4i xb[MAXG][2];
-    uint32_t wb[MAXG];
-    auto load_b = [&](int gb) {
-#pragma unroll
-        for (int q = 0; q < MAXG; q++) {
-            const bool in = gb + q < g1;
-            wb[q] = in ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rbs, bs_off, (uint32_t)(gb + q) * 256, 0) : 0u;
-#pragma unroll
-            for (int s = 0; s < 2; s++)
-                xb[q][s] = in ? __builtin_amdgcn_raw_buffer_load_b128(rb, b_off + (uint32_t)s * 64,
-                                                                      (uint32_t)(gb + q) * 128, STREAM)
-                              : v4i{0, 0, 0, 0};
-        }
-    };
-    const bool one = g1 - g0 <= MAXG;  // the wave's whole range fits in registers
-    if (one)
-        load_b(g0);
-    for (int64_t m0 = lo; m0 < hi; m0 += 16 * MT) {
-        const int rows_m = (int)min(hi - m0, (int64_t)(16 * MT));
-        const __amdgpu_buffer_rsrc_t ra = byte_range(p.a + m0 * p.ld_a, (uint32_t)(rows_m * p.ld_a));
-        uint32_t as_off[MT], a_off[MT];
-#pragma unroll
-        for (int i = 0; i < MT; i++) {
-            const uint32_t row = (uint32_t)m0 + 16 * i + r;
-            as_off[i] = (row >> 5) * stile + (32 * (g & 1) + (row & 31)) * 4;
-            a_off[i] = (uint32_t)((16 * i + r) * p.ld_a + g * 16);
-        }
-        v4f acc[MT];
-#pragma unroll
-        for (int i = 0; i < MT; i++)
-            acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int gb = g0; gb < g1; gb += MAXG) {
-            if (!one)
-                load_b(gb);
-#pragma unroll
-            for (int q = 0; q < MAXG; q++) {
-                if (gb + q >= g1)
-                    break;
-#pragma unroll
-                for (int i = 0; i < MT; i++) {
-                    const uint32_t wa =
-                        (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(ras, as_off[i], (uint32_t)(gb + q) * 256, 0) >> sh;
-                    auto step = [&](auto S_) {
-                        constexpr int s = decltype(S_)::value;
-                        const v4i xa = __builtin_amdgcn_raw_buffer_load_b128(ra, a_off[i] + (uint32_t)s * 64,
-                                                                             (uint32_t)(gb + q) * 128, 0);
-                        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            widen(xb[q][s]), widen(xa), acc[i], FMT_E2M1, FMT_E2M1, 2 * s, (int)(wb[q] >> sh), 2 * s,
-                            (int)wa);
-                    };
-                    step(std::integral_constant<int, 0>{});
-                    step(std::integral_constant<int, 1>{});
-                }
-            }
-        }
-        // fragment i: lane (r, g) holds row m0 + 16i + r, columns c0 + 4g .. +3
-        auto store = [&](int64_t c0, int i, int ln, v4f v) {
-            const int64_t m = m0 + 16 * i + (ln & 15), n = c0 + 4 * (ln >> 4);
-            if (m >= hi || n >= p.N)
-                return;
-            const int64_t at = m * p.ld_c + n;
-            if (CT == 0) {
-                uint16_t *c = reinterpret_cast<uint16_t *>(p.c) + at;
-                typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
-                const bf16x4_t w = __builtin_convertvector(v, bf16x4_t);
-                if (p.vec_store && n + 3 < p.N)
-                    *reinterpret_cast<uint2 *>(c) = __builtin_bit_cast(uint2, w);
-                else
-#pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        if (n + e < p.N)
-                            c[e] = __builtin_bit_cast(uint16_t, (__bf16)w[e]);
-            } else {
-                float *c = reinterpret_cast<float *>(p.c) + at;
-                if (p.vec_store && n + 3 < p.N)
-                    *reinterpret_cast<v4f *>(c) = v;
-                else
-#pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        if (n + e < p.N)
-                            c[e] = v[e];
-            }
-        };
-        if (p.ks_log == 0) {
-#pragma unroll
-            for (int i = 0; i < MT; i++)
-                store(n0, i, lane, acc[i]);
-            continue;
-        }
-        v4f *sums = reinterpret_cast<v4f *>(part);
-        __syncthreads();  // (the previous pass's sums have been read)
-#pragma unroll
-        for (int i = 0; i < MT; i++)
-            sums[(wave * MT + i) * 64 + lane] = acc[i];
-        __syncthreads();
-        for (int u = tid; u < per_block * MT * 64; u += blockDim.x) {
-            const int tile = u / (MT * 64), rest = u - tile * (MT * 64);
-            v4f v = sums[tile * ks * MT * 64 + rest];
-            for (int w = 1; w < ks; w++)
-                v += sums[(tile * ks + w) * MT * 64 + rest];
-            store((first_tn + tile) * 16, rest / 64, rest & 63, v);
-        }
-    }
+    if (MT == 1 || (GROUPED && rows <= 16))
+        rows_chunk<CT, 1, 4>(p, part, B, BS, lo, hi, first_tn);
+    else if (MT == 2 || (GROUPED && rows <= 32))
+        rows_chunk<CT, 2, 4>(p, part, B, BS, lo, hi, first_tn);
+    else
+        rows_chunk<CT, 4, 2>(p, part, B, BS, lo, hi, first_tn);
 }
 
 // ---------------------------------------------------------------------------
@@ -1081,7 +1100,7 @@ static int k_split(int64_t tiles, int64_t KT, int64_t cus)
 }
 
 // live: groups that have rows (at most)
-template <bool GROUPED, int CT, int MT, int MAXG>
+template <bool GROUPED, int CT, int MT>
 static hipError_t launch_rows_t(Gemm4Params p, int64_t live, hipStream_t stream)
 {
     p.as_bytes = (uint32_t)scale_bytes(p.M, p.K);
@@ -1095,7 +1114,7 @@ static hipError_t launch_rows_t(Gemm4Params p, int64_t live, hipStream_t stream)
     const int64_t chunks = GROUPED ? live + p.M / ROWS_CHUNK : (p.M + ROWS_CHUNK - 1) / ROWS_CHUNK;
     const int64_t grid = (p.tiles_n + per_block - 1) / per_block * chunks;
     const size_t lds = p.ks_log > 0 ? (size_t)waves * MT * 1024 : 0;
-    hipLaunchKernelGGL((gemm4_rows_kernel<GROUPED, CT, MT, MAXG>), dim3((unsigned)grid), dim3(64 * waves), lds, stream,
+    hipLaunchKernelGGL((gemm4_rows_kernel<GROUPED, CT, MT>), dim3((unsigned)grid), dim3(64 * waves), lds, stream,
                        p);
     return hipGetLastError();
 }
@@ -1220,12 +1239,12 @@ hipError_t launch_gemm_fp4(int64_t M, int64_t N, int64_t K, const void *a_q, int
     const TilePlan plan = tile_plan(M, N, K, cu_count());
     if (plan.rows) {
         if (c_dtype == 0)
-            return M <= 16   ? launch_rows_t<false, 0, 1, 4>(p, 1, stream)
-                   : M <= 32 ? launch_rows_t<false, 0, 2, 4>(p, 1, stream)
-                             : launch_rows_t<false, 0, 4, 2>(p, 1, stream);
-        return M <= 16   ? launch_rows_t<false, 1, 1, 4>(p, 1, stream)
-               : M <= 32 ? launch_rows_t<false, 1, 2, 4>(p, 1, stream)
-                         : launch_rows_t<false, 1, 4, 2>(p, 1, stream);
+            return M <= 16   ? launch_rows_t<false, 0, 1>(p, 1, stream)
+                   : M <= 32 ? launch_rows_t<false, 0, 2>(p, 1, stream)
+                             : launch_rows_t<false, 0, 4>(p, 1, stream);
+        return M <= 16   ? launch_rows_t<false, 1, 1>(p, 1, stream)
+               : M <= 32 ? launch_rows_t<false, 1, 2>(p, 1, stream)
+                         : launch_rows_t<false, 1, 4>(p, 1, stream);
     }
     p.as_bytes = (uint32_t)scale_bytes(M, K);
     p.bs_bytes = (uint32_t)scale_bytes(N, K);
@@ -1294,13 +1313,17 @@ hipError_t launch_grouped_gemm_fp4(int64_t G, int64_t M_total, int64_t N, int64_
     p.b_group_stride = N * (K / 2);
     p.bs_group_stride = scale_bytes(N, K);
     // Few rows: while the experts that can have any give less than a 128 x 128
-    // tile a compute unit, and one pass of 16 rows mostly does.  8 experts' rows,
-    // one each, N 1536, K 2048: 7.2 us against 9.5 by tiles; 32 experts: 16.0
-    // against 14.7.
+    // tile a compute unit, with up to 16 rows each on average.  By few rows / by
+    // tiles, us: 8 experts of one row, N 1536, K 2048: 5.9 / 10.5, N 3968, K 4096:
+    // 16.6 / 18.8, N 2048, K 14336: 30 / 49; of 16 rows 6.6 / 8.9, 20.5 / 17.1 and
+    // 36 / 49; 21 experts of 9 rows, N 1536, K 2048: 12.1 / 10.2; 32 of one row (more
+    // tiles than units): 13.4 / 15.6.
     const int64_t live = std::min(G, M_total);
     if (live * ((N + 127) / 128) < cu_count() && M_total <= 16 * live)
-        return c_dtype == 0 ? launch_rows_t<true, 0, 1, 4>(p, live, stream)
-                            : launch_rows_t<true, 1, 1, 4>(p, live, stream);
+        return M_total <= 16 ? (c_dtype == 0 ? launch_rows_t<true, 0, 1>(p, live, stream)
+                                             : launch_rows_t<true, 1, 1>(p, live, stream))
+                             : (c_dtype == 0 ? launch_rows_t<true, 0, 4>(p, live, stream)
+                                             : launch_rows_t<true, 1, 4>(p, live, stream));
     p.as_bytes = (uint32_t)scale_bytes(M_total, K);
     p.bs_bytes = (uint32_t)p.bs_group_stride;
     p.vec_store = vec_ok(c, ld_c, c_dtype);

@@ -539,3 +539,58 @@ def test_padded_batch_under_the_debug_check(gpu_lib, monkeypatch, T):
     for bad, at in (([1, 1, 2], 0), ([0, 2, 1], 1), ([0, 1, n + T * k], 2)):
         with pytest.raises(mx.MxError, match=rf"group_offsets\[{at}\]"):
             mx.mx_grouped_gemm_fp4(torch.tensor(bad, device=dev), f["q"], f["s"], W["gu"][0][:2].contiguous(), W["gu"][1])
+
+
+def _takes_few_rows(G, M, N):
+    """The rule by which a grouped product takes the few-row kernel."""
+    live = min(G, M)
+    return live * ((N + 127) // 128) < torch.cuda.get_device_properties(0).multi_processor_count and M <= 16 * live
+
+
+def test_few_rows_of_experts_beyond_4_gib(gpu_lib):
+    """The few-row kernel with an expert whose weights start beyond 2^32 bytes."""
+    mx = gpu_lib
+    g = torch.Generator(device=dev)
+    g.manual_seed(8)
+    G, N, K = 260, 8192, 4096
+    rows = [1, 2]
+    m = sum(rows)
+    assert _takes_few_rows(G, m, N)
+    b, sb = _random_operand(g, G * N, K)
+    assert (G - 1) * N * K // 2 > 1 << 32
+    a, sa = _random_operand(g, m, K)
+    off = torch.full((G + 1,), rows[0], dtype=torch.int64, device=dev)
+    off[0], off[G] = 0, m
+    C = mx.mx_grouped_gemm_fp4(off, a, sa, b.view(G, N, K // 2), sb)
+    A, per = _decode(a, sa), N * K // 32
+    for e, lo, hi in ((0, 0, rows[0]), (G - 1, rows[0], m)):
+        _close(C[lo:hi], A[lo:hi], _decode(b[e * N:(e + 1) * N], sb[e * per:(e + 1) * per]), f"expert {e}")
+
+
+@pytest.mark.parametrize("rows,N,K", [
+    ([17, 0, 30, 1, 16, 0, 64, 0], 3968, 4096),      # chunks of 17 to 64 rows, long K
+    ([0, 128, 0, 0, 0, 0, 0, 0], 3968, 4096),        # every row on one expert: two chunks
+    ([33, 95, 0, 0, 0, 0, 0, 0], 2048, 14336), ([0, 0, 0, 0, 0, 0, 0, 120], 1000, 12288),
+    ([15, 32, 33, 0, 48, 0, 0, 0], 130, 8192)])
+def test_few_rows_of_uneven_loads(gpu_lib, rows, N, K):
+    """Chunks of several passes of 16 rows, and more of K than stays in registers."""
+    mx = gpu_lib
+    G, M = len(rows), sum(rows)
+    assert _takes_few_rows(G, M, N)
+    g = torch.Generator(device=dev)
+    g.manual_seed(M + K)
+    off = np.concatenate([[0], np.cumsum(rows)])
+    a, sa = _random_operand(g, M, K)
+    n32 = (N + 31) // 32 * 32
+    b = torch.randint(0, 256, (G, N, K // 2), generator=g, device=dev, dtype=torch.uint8)
+    sb = torch.randint(121, 134, (G, n32 * (K // 32)), generator=g, device=dev, dtype=torch.uint8)
+    A = _decode(a, sa)
+    for dt in (torch.bfloat16, torch.float32):
+        buf = torch.full((M + 1, N), 7.0, dtype=dt, device=dev)
+        C = mx.mx_grouped_gemm_fp4(torch.from_numpy(off).to(dev), a, sa, b, sb, c=buf[:M])
+        for e in range(G):
+            if rows[e]:
+                lo, hi = off[e], off[e + 1]
+                _close(C[lo:hi], A[lo:hi], _decode(b[e], sb[e]), f"expert {e}")
+        assert (buf[M] == 7).all()
+        assert torch.equal(C, mx.mx_grouped_gemm_fp4(torch.from_numpy(off).to(dev), a, sa, b, sb, out_dtype=dt))

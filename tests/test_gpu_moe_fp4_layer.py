@@ -594,3 +594,25 @@ def test_few_rows_of_uneven_loads(gpu_lib, rows, N, K):
                 _close(C[lo:hi], A[lo:hi], _decode(b[e], sb[e]), f"expert {e}")
         assert (buf[M] == 7).all()
         assert torch.equal(C, mx.mx_grouped_gemm_fp4(torch.from_numpy(off).to(dev), a, sa, b, sb, out_dtype=dt))
+
+
+@pytest.mark.parametrize("M", [7, 290])
+def test_strided_operands_give_the_same_bytes(gpu_lib, M):
+    """The sums' order goes by M, N and K alone: operands and C of any stride
+    and alignment give what contiguous ones do."""
+    mx = gpu_lib
+    g = torch.Generator(device=dev)
+    g.manual_seed(M)
+    N, K = 272, 1024
+    a, sa = _random_operand(g, M, K)
+    b, sb = _random_operand(g, N, K)
+    wa = torch.full((M, K // 2 + 48), 0x77, dtype=torch.uint8, device=dev)
+    wb = torch.full((N, K // 2 + 16), 0x77, dtype=torch.uint8, device=dev)
+    wa[:, 16:16 + K // 2], wb[:, :K // 2] = a, b
+    for dt in (torch.bfloat16, torch.float32):
+        want = mx.mx_gemm_fp4(a, sa, b, sb, out_dtype=dt)
+        for pad, left in ((0, 0), (8, 8), (5, 3), (1, 0)):
+            buf = torch.full((M, N + left + pad), 9.0, dtype=dt, device=dev)
+            mx.mx_gemm_fp4(wa[:, 16:16 + K // 2], sa, wb[:, :K // 2], sb, c=buf[:, left:left + N])
+            assert torch.equal(buf[:, left:left + N], want)
+            assert (buf[:, :left] == 9).all() and (buf[:, left + N:] == 9).all()

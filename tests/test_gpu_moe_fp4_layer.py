@@ -616,3 +616,15 @@ def test_strided_operands_give_the_same_bytes(gpu_lib, M):
             mx.mx_gemm_fp4(wa[:, 16:16 + K // 2], sa, wb[:, :K // 2], sb, c=buf[:, left:left + N])
             assert torch.equal(buf[:, left:left + N], want)
             assert (buf[:, :left] == 9).all() and (buf[:, left + N:] == 9).all()
+
+
+def test_combine_gradient_refuses_an_output_that_is_not_wanted(gpu_lib):
+    mx = gpu_lib
+    x = torch.randn(4, 256, device=dev).bfloat16()
+    y = torch.randn(8, 256, device=dev).bfloat16()
+    slot = torch.arange(8, dtype=torch.int32, device=dev)
+    w = torch.rand(4, 2, device=dev)
+    with pytest.raises(ValueError, match="dy"):
+        mx.mx_moe_combine_bwd(x, y, slot, w, dy=torch.empty_like(y), want_dy=False)
+    with pytest.raises(ValueError, match="d_weights"):
+        mx.mx_moe_combine_bwd(x, y, slot, w, d_weights=torch.empty_like(w), want_d_weights=False)

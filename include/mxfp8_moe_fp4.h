@@ -134,7 +134,7 @@ mx_status mx_moe_route_bwd(const void *logits, int logits_dtype, int64_t tokens,
  * and the grouped products take it as it is.  Slots are distinct
  * (mx_moe_dispatch's are); where two name one row, that row holds one of the
  * two values.  Slots outside [0, tokens*topk) are skipped.
- * Requirements: tokens, hidden >= 0, topk >= 1, tokens * topk < 2^30 (else
+ * Requirements: tokens, hidden >= 0, topk >= 1, tokens * topk and hidden < 2^30 (else
  * MX_ERR_INVALID_ARG); hidden % 8 == 0 (else MX_ERR_SHAPE); d_out, y and dy
  * 16-byte aligned rows (ld % 8; else MX_ERR_ALIGN); outputs overlap nothing
  * (else MX_ERR_OVERLAP).

@@ -118,7 +118,7 @@ mx_status mx_moe_combine_bwd(const void *d_out, int64_t tokens, int64_t hidden, 
     if (hidden % 8 != 0)
         return fail(MX_ERR_SHAPE, "%s: hidden=%lld is not a multiple of 8", fn, (long long)hidden);
     const int64_t max_rows = (int64_t)1 << 30;
-    if (topk >= max_rows || tokens > max_rows / topk || hidden >= max_rows)
+    if (topk >= max_rows || tokens >= (max_rows + topk - 1) / topk || hidden >= max_rows)
         return fail(MX_ERR_INVALID_ARG, "%s: tokens * topk and hidden must be below 2^30", fn);
     if (ld_dout < hidden || (dy && ld_dy < hidden) || (d_weights && ld_y < hidden))
         return fail(MX_ERR_INVALID_ARG, "%s: leading dimension too small (ld_dout=%lld ld_y=%lld ld_dy=%lld)", fn,

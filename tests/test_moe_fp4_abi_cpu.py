@@ -242,6 +242,15 @@ def test_gemm_refusals():
     assert call("mx_grouped_gemm_fp4", gg, M=0) == mx.MX_OK
 
 
+def test_limits_of_sizes():
+    """Sizes at the stated limits: the largest that is taken reaches the checks behind it."""
+    combine = dict(d_out=A, tokens=4, hidden=64, ld_o=64, y=B, ld_y=64, slot=None, w=D, topk=2, dy=E, ld_dy=64, dw=F)
+    for tokens, topk in ((1 << 29, 2), (1 << 30, 1), (1, 1 << 30), (1 << 27, 8)):
+        refused("mx_moe_combine_bwd", combine, INV, "2^30", tokens=tokens, topk=topk)
+    for tokens, topk in (((1 << 29) - 1, 2), ((1 << 30) - 1, 1), (1, (1 << 30) - 1), (357913941, 3)):
+        refused("mx_moe_combine_bwd", combine, INV, "null", tokens=tokens, topk=topk)
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes():
     x = torch.zeros(4, 16)
     for f, args in ((mx.mx_moe_route, (x, 2)), (mx.mx_quantize_rowwise_fp4, (x,)), (mx.mx_gemm_fp4, (x, x, x, x))):

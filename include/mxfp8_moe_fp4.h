@@ -86,7 +86,7 @@ typedef enum mx_score {
  * num_experts % num_groups == 0, 1 <= topk_groups <= num_groups, group_top 1
  * or 2 and at most num_experts / num_groups, ld_logits >= num_experts, scale
  * finite (else MX_ERR_INVALID_ARG, or MX_ERR_UNSUPPORTED above 1024 experts,
- * topk 32 or 64 groups, from 2^26 tokens or for a leading dimension from 2^28);
+ * topk 32, 64 groups or 2^26 - 4 tokens, or for a leading dimension from 2^28);
  * pointers aligned to their elements (else MX_ERR_ALIGN);
  * outputs overlap nothing (else MX_ERR_OVERLAP).
  */

@@ -31,9 +31,9 @@ static mx_status check_route(const char *fn, int dtype, int64_t tokens, int64_t 
                     (long long)experts);
     if (!std::isfinite(scale))
         return fail(MX_ERR_INVALID_ARG, "%s: scale is not finite", fn);
-    // (a launch has at most 2^32 - 1 threads, up to 64 a token)
-    if (tokens >= ((int64_t)1 << 26) || ld >= ((int64_t)1 << 28))
-        return fail(MX_ERR_UNSUPPORTED, "%s: 2^26 tokens or more, or a leading dimension of 2^28", fn);
+    // (a launch has at most 2^32 - 1 threads, 64 a token in whole workgroups of 256)
+    if (tokens > ((int64_t)1 << 26) - 4 || ld >= ((int64_t)1 << 28))
+        return fail(MX_ERR_UNSUPPORTED, "%s: more than 2^26 - 4 tokens, or a leading dimension of 2^28", fn);
     return MX_OK;
 }
 

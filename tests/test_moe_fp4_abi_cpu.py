@@ -249,6 +249,13 @@ def test_limits_of_sizes():
         refused("mx_moe_combine_bwd", combine, INV, "2^30", tokens=tokens, topk=topk)
     for tokens, topk in (((1 << 29) - 1, 2), ((1 << 30) - 1, 1), (1, (1 << 30) - 1), (357913941, 3)):
         refused("mx_moe_combine_bwd", combine, INV, "null", tokens=tokens, topk=topk)
+    # a launch of 2^32 threads, 64 a token, is one too many
+    bwd = dict(logits=None, dt=BF, tokens=4, experts=1024, ld=1024, score=1, topk=8, renorm=1, scale=1.0, ids=B, dw=C,
+               dx=D, ld_d=1024)
+    for name, base in (("mx_moe_route", dict(ROUTE, logits=None)), ("mx_moe_route_bwd", bwd)):
+        for tokens in ((1 << 26) - 3, (1 << 26) - 1, 1 << 26):
+            refused(name, base, UNSUP, "tokens", tokens=tokens)
+        refused(name, base, INV, "null", tokens=(1 << 26) - 4)
 
 
 def test_binding_refuses_host_tensors_and_wrong_shapes():

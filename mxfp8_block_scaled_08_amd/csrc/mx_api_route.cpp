@@ -87,9 +87,11 @@ mx_status mx_moe_route_bwd(const void *logits, int logits_dtype, int64_t tokens,
     mx_status st = check_route(fn, logits_dtype, tokens, num_experts, ld_logits, score, topk, scale);
     if (st != MX_OK)
         return st;
-    if (ld_d < num_experts || ld_d >= ((int64_t)1 << 28))
-        return fail(MX_ERR_INVALID_ARG, "%s: ld_d=%lld must lie in num_experts=%lld .. 2^28 - 1", fn, (long long)ld_d,
+    if (ld_d < num_experts)
+        return fail(MX_ERR_INVALID_ARG, "%s: ld_d=%lld < num_experts=%lld", fn, (long long)ld_d,
                     (long long)num_experts);
+    if (ld_d >= ((int64_t)1 << 28))
+        return fail(MX_ERR_UNSUPPORTED, "%s: ld_d=%lld must be below 2^28", fn, (long long)ld_d);
     if (tokens == 0)
         return ok();
     if (!logits || !topk_ids || !d_weights || !d_logits)

@@ -256,6 +256,9 @@ def test_limits_of_sizes():
         for tokens in ((1 << 26) - 3, (1 << 26) - 1, 1 << 26):
             refused(name, base, UNSUP, "tokens", tokens=tokens)
         refused(name, base, INV, "null", tokens=(1 << 26) - 4)
+    refused("mx_moe_route", ROUTE, UNSUP, "leading", ld=1 << 28)
+    refused("mx_moe_route_bwd", bwd, UNSUP, "leading", ld=1 << 28)
+    refused("mx_moe_route_bwd", bwd, UNSUP, "ld_d", ld_d=1 << 28)
 
 
 def test_binding_refuses_host_tensors_and_wrong_shapes():

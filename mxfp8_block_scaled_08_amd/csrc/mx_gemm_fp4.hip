@@ -980,6 +980,9 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
                     for (int v = 0; v < 16; v++)
                         acc[i][j][v] = 0.0f;
                 const int m0 = cur.m0 + wm * 32 + j * 64, rows = min(cur.m_end - m0, 32);
+                // (a wave's LDS accesses run in order; the fences keep the compiler
+                // from moving one lane's reads over the other lanes' writes)
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll 4
                 for (int r = 0; r < rows; r++) {
 #pragma unroll
@@ -997,6 +1000,7 @@ __global__ __launch_bounds__(GM_THREADS, TM * TN <= 4 ? 2 : 1) void gemm4_tile_k
                         }
                     }
                 }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             }
             lds_ring_barrier();
         }

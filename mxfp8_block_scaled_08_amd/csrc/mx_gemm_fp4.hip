@@ -1093,8 +1093,8 @@ static int64_t scale_bytes(int64_t rows, int64_t K) { return ((rows + 31) / 32) 
 
 // Log2 of the waves that share a column tile along K, so that about 8 waves a
 // compute unit have loads in flight (`tiles`: column tiles that have rows).  With
-// 16 a unit 1x6144x4096 takes 6.9 us instead of 5.9, 1x24576x4096 13.6 instead of
-// 14.0, out of HBM both; most shapes are the same.
+// 16 a unit, out of HBM: 1x6144x4096 6.15 us instead of 5.8, 64x6144x4096 14.3
+// instead of 13.0, 1x24576x4096 12.15 instead of 12.6; most shapes are the same.
 static int k_split(int64_t tiles, int64_t KT, int64_t cus)
 {
     int log = 0;
@@ -1131,8 +1131,9 @@ static hipError_t launch_rows_t(Gemm4Params p, int64_t live, hipStream_t stream)
 // 512..24576 (two kernels in a row: 2 us each at least):
 //   few rows (M <= 64): 2 + 0.195 a MB of B + 0.1 a MB of A as it is read, once
 //     for every 16 columns, times 0.85 of the units over the workgroups where
-//     those are fewer.  1x6144x4096 4.6, 64x6144x4096 11.8, 32x4096x12288 12.6,
-//     64x1000x16384 23.3 (12.4 by tiles), 1x256x16384 7.8 (12.0 by tiles).
+//     those are fewer.  Out of HBM, by few rows / by tiles: 1x6144x4096 5.8 / 15.0,
+//     64x6144x4096 13.0 / 15.5, 32x4096x12288 13.3 / 15.7, 64x1000x16384 23.1 /
+//     13.9, 1x256x16384 8.4 / 12.4.
 //   tiles: a round of w tiles takes a fixed part and a time for each 128-K
 //     stage that grows with the compute units in use, as the tiles share L2 and
 //     power: 128x128 0.27 .. 0.34, or 0.64 when units hold two; 256x128 0.38 ..

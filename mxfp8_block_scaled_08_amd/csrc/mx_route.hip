@@ -15,11 +15,15 @@
 // thousand would swap two experts.  FP64 costs the same issue slots as FP32 on
 // CDNA4's vector unit.
 //
-// Bound by the chain of topk reductions, four to six dependent exchanges each, not
-// by the logits' bytes: 20480 FP32 tokens x 128 experts, top 8, take 8.0 us (10.5
-// MB, 2.1 us of HBM, behind an empty launch of 2.2), 32 tokens 3.6 us.  With score
-// and number compared apart and element loads it was 12.5 us, with one wave a
-// workgroup 8.6.
+// With many tokens bound by issue slots: 20480 FP32 tokens x 128 experts, top 8,
+// take 7.6 us (10.5 MB, 2.1 us of HBM, behind an empty launch of 1.6), with a
+// vector instruction issued in 79 % of a busy unit's cycles; a round of the top-k
+// spends EPL - 1 maxima, three instructions an exchange and two a key to drop the
+// winner.  4099 BF16 tokens x 256, sigmoid with a bias, 4 of 8 groups: 10.8 us, 59 %
+// (FP64 exponentials and divisions, the rounds, and waits at the groups' two
+// barriers).  32 tokens, 3.4 us, wait on the chain of the rounds' exchanges.  With
+// score and number compared apart and element loads 20480 x 128 took 12.5 us, with
+// one wave a workgroup 8.6.
 #include "mx_device.h"
 #include "mx_gemm_util.h"
 #include "mx_launch.h"
@@ -413,8 +417,8 @@ struct RouteBwdParams {
 // which need no division by a small S.  Each lane then gathers the chosen
 // ones' values for its own experts, in order j = 0, 1, ..  Every column is
 // written once, so nothing is cleared first and no atomics are needed.  20480
-// FP32 tokens x 128 experts, top 8, renormalized: 6.3 us, of which an empty
-// launch is 2.2; it reads the lines of the logits that hold a chosen one (nearly
+// FP32 tokens x 128 experts, top 8, renormalized: 5.9 us, of which an empty
+// launch is 1.6; it reads the lines of the logits that hold a chosen one (nearly
 // all, 10.5 MB) and writes 10.5 MB, 4.4 us of HBM.
 template <int LANES, int EPL, int DT, bool SOFTMAX>
 __global__ __launch_bounds__(RT_THREADS) void route_bwd_kernel(RouteBwdParams p)

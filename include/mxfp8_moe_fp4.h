@@ -72,9 +72,11 @@ typedef enum mx_score {
  * below every group with more, among such groups by that expert's score, and a
  * group with none ranks last; groups of equal score rank by number.  Where
  * fewer than topk can be chosen, the remaining ids are -1 (which mx_moe_dispatch
- * does not route) and their weights 0, as for a masked token.  Renormalized
- * weights are formed from score ratios, so they sum to scale however small
- * the chosen scores are.
+ * does not route) and their weights 0, as for a masked token.  The dispatched
+ * rows of such a batch end below tokens*topk: mx_grouped_gemm_fp4 takes their
+ * offsets, mx_grouped_gemm asks for an end at M_total.  Renormalized weights are
+ * formed from score ratios, so they sum to scale however small the chosen scores
+ * are.
  * NaN and +inf: a NaN logit ranks above every number and, where logits are
  * compared, +inf next.  Where scores are compared (a bias, or group_top 2), a
  * softmax row that holds a NaN or +inf has no scores and ranks by its logits in

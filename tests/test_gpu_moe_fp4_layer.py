@@ -628,3 +628,59 @@ def test_combine_gradient_refuses_an_output_that_is_not_wanted(gpu_lib):
         mx.mx_moe_combine_bwd(x, y, slot, w, dy=torch.empty_like(y), want_dy=False)
     with pytest.raises(ValueError, match="d_weights"):
         mx.mx_moe_combine_bwd(x, y, slot, w, d_weights=torch.empty_like(w), want_d_weights=False)
+
+
+@pytest.mark.parametrize("T", [6, 40, 700])
+def test_captured_layer_replayed_on_new_inputs(gpu_lib, T):
+    """One capture, replayed with other tokens, logits and masks written into
+    its inputs: experts' loads change, from none to all rows on one expert."""
+    mx = gpu_lib
+    E, k, H, F = 8, 2, 512, 256
+    W = _weights(mx, E, H, F, 5)
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device=dev)
+    logits = torch.zeros(T, E, device=dev)
+    mask = torch.ones(T, dtype=torch.uint8, device=dev)
+    d_out = mxsynth.normal_bf16((T, H), 1e-2, seed=9).to(dev)
+    ws = torch.empty(max(mx.mx_moe_dispatch_workspace_bytes(T, k, E), 1), dtype=torch.uint8, device=dev)
+    o = _buffers(T, E, k, H, F)
+    how = dict(renormalize=False)
+
+    def run(out):
+        _, f = _forward(mx, x, logits, W, E, k, o=out, ws=ws if out else None, mask=mask, **how)
+        return f, _backward(mx, d_out, logits, f, W, o=out, **how)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run(o)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        run(o)
+    for rep in range(5):
+        x.copy_(mxsynth.normal_bf16((T, H), 1.0, seed=20 + rep))
+        logits.copy_(torch.randn(T, E, generator=torch.Generator().manual_seed(rep)))
+        mask.fill_(1)
+        if rep == 1:
+            logits[:, 3], logits[:, 5] = 9.0, 8.0         # every row on two experts
+        if rep == 2:
+            mask.zero_()                                  # no token at all
+            logits.fill_(float("nan"))
+        if rep == 3:
+            mask[T // 3:] = 0                             # padded, the padding's logits anything
+            logits[T // 3:] = float("nan")
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {n: t.clone() for n, t in o.items()}
+        f, b = run(None)
+        torch.cuda.synchronize()
+        n = int(f["off"][-1])
+        assert n == int(mask.sum()) * k
+        for name in ("ids", "w", "off", "slot"):
+            assert torch.equal(got[name], f[name]), f"replay {rep}: {name}"
+        for name in ("q", "gu", "hq", "h", "y"):
+            assert torch.equal(got[name][:n], f[name][:n]), f"replay {rep}: {name}"
+        assert torch.equal(got["dw"], b["dw"]) and torch.equal(got["dx"], b["dx"]), f"replay {rep}"
+        assert torch.equal(got["dh"][:n], b["dh"][:n]) and torch.equal(got["dy"][:n], b["dy"][:n]), f"replay {rep}"
+        assert torch.isfinite(got["dx"]).all() and (got["dx"][mask == 0] == 0).all()

@@ -1,0 +1,537 @@
+"""Measured cases of the sampler's attention step: rotary positions, the paged
+8-bit key/value cache and the attention that reads it.
+
+Every case is one call (or the few that belong together) as a sampler's step,
+a prompt's prefill or a learner's layer makes it.  ``run`` computes it in plain
+torch operations (FP32; angles in 64 bits), or, with ``own`` set, by the
+library's entry points.  Heads follow the layers that the library's benchmark
+uses (Qwen3-8B: 32 query and 8 key/value heads of 128; Qwen3-30B-A3B: 32 and
+4) or are generic.
+
+The cache: E4M3 codes [K, V][pages][kv heads][page][head_dim], one E8M0 scale
+for every 16 consecutive positions of a page and head, [K, V][pages][kv
+heads][page / 16].  Position p of sequence b lies in page table[b][p // page].
+A call's rows of sequence b are starts[b] .. starts[b+1] - 1 and stand at the
+last positions below lens[b].  A block's scale is the least power of two that
+keeps its finite values within 448; it starts anew with the block's first
+position and afterwards only grows, older codes then being rounded again.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+DEV = "cuda"
+NEG = float("-inf")
+BLOCK = 16
+
+# ---------------------------------------------------------------------------
+# cases
+
+
+def listed():
+    rope = dict(op="rope", scaling="plain", base=1e6, inverse=False)
+    kv = dict(base=1e6, style="half")
+    return [
+        # queries of a sampler's step: 32 sequences, one token each, far positions
+        dict(rope, name="rope_token", tokens=32, heads=32, dim=128, rot=128, style="half", dtype="bf16", span=131072),
+        # a learner's micro-batch of 20480 tokens, queries forward and backward
+        dict(rope, name="rope_train", tokens=20480, heads=32, dim=128, rot=128, style="half", dtype="bf16", span=4096,
+             inverse=True),
+        # part of an odd head interleaved, frequencies scaled for a long context, FP32 with its gradient
+        dict(rope, name="rope_partial", tokens=4099, heads=5, dim=80, rot=32, style="interleaved", dtype="f32",
+             span=131072, scaling="yarn", inverse=True),
+        # one token of each of 64 sequences into the cache
+        dict(kv, name="append_token", op="append", batch=64, new=1, ctx=8192, ragged=True, kv_heads=8, dim=128, page=64),
+        # a micro-batch of prompts into an empty cache
+        dict(kv, name="append_prompt", op="append", batch=6, new=4096, ctx=0, ragged=True, kv_heads=4, dim=128, page=64),
+        # short pieces behind odd lengths, small pages
+        dict(name="append_pieces", op="append", batch=96, new=40, ctx=700, ragged=True, kv_heads=2, dim=64, page=16,
+             base=1e4, style="interleaved"),
+        # one sequence, one token
+        dict(name="attention_token", op="attention", batch=1, new=1, ctx=700, ragged=False, heads=32, kv_heads=8,
+             dim=128, page=64, window=0, causal=True),
+        # a sampler's step: 64 sequences of uneven lengths
+        dict(name="attention_step", op="attention", batch=64, new=1, ctx=16384, ragged=True, heads=32, kv_heads=8,
+             dim=128, page=64, window=0, causal=True),
+        # two long sequences
+        dict(name="attention_long", op="attention", batch=2, new=1, ctx=131072, ragged=True, heads=32, kv_heads=4,
+             dim=128, page=128, window=0, causal=True),
+        # up to six drafted tokens a sequence, heads of 64 in odd groups, a window
+        dict(name="attention_draft", op="attention", batch=19, new=6, ctx=5000, ragged=True, heads=14, kv_heads=2,
+             dim=64, page=16, window=2000, causal=True),
+        # prompts of uneven lengths, some behind a part that is in the cache already
+        dict(name="attention_prompt", op="attention", batch=4, new=4096, ctx=2048, ragged=True, heads=32, kv_heads=8,
+             dim=128, page=64, window=0, causal=True),
+        # the whole step of 32 sequences: queries rotated, keys and values appended, attention
+        dict(kv, name="step", op="step", batch=32, new=1, ctx=4096, ragged=True, heads=32, kv_heads=4, dim=128, page=64,
+             window=0, causal=True),
+    ]
+
+
+def _spread(rng, lo, hi):
+    return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    like = listed()
+    while True:
+        case = _draw(rng)
+        if all(a <= max(b) for a, b in zip(_cost(case), zip(*(_cost(c) for c in like if c["op"] == case["op"])))):
+            return case
+
+
+def _cost(case):
+    """The work of a case, and what its plain form has to hold: all scores, all keys."""
+    w = work(case)
+    held = [0, 0]
+    if case["op"] in ("attention", "step"):
+        cells = case["batch"] * (case["ctx"] + case["new"])
+        held = [cells * case["new"] * case["heads"], cells * case["kv_heads"] * case["dim"]]
+    return [max(w["bytes"], w["flops"] / 50)] + held
+
+
+def _draw(rng):
+    op = rng.choice(["rope", "rope", "append", "append", "attention", "attention", "attention", "step"])
+    if op == "rope":
+        dim = rng.choice([64, 80, 96, 128, 128, 256])
+        return dict(op=op, tokens=_spread(rng, 1, 20480), heads=rng.randint(1, 40), dim=dim,
+                    rot=rng.choice([dim, dim, 16 * rng.randint(1, dim // 16)]),
+                    style=rng.choice(["half", "half", "interleaved"]), dtype=rng.choice(["bf16", "bf16", "f32"]),
+                    span=rng.choice([4096, 131072]), scaling=rng.choice(["plain", "yarn"]), base=rng.choice([1e4, 1e6]),
+                    inverse=rng.random() < 0.5)
+    dim = rng.choice([64, 128, 128])
+    kv_heads = rng.choice([1, 2, 3, 4, 8])
+    case = dict(op=op, kv_heads=kv_heads, dim=dim, page=rng.choice([16, 32, 64, 64, 128, 256]), ragged=rng.random() < 0.8)
+    if op != "attention":
+        case.update(base=rng.choice([1e4, 1e6]), style=rng.choice(["half", "half", "interleaved"]))
+    if op == "append":
+        case.update(batch=_spread(rng, 1, 128), new=_spread(rng, 1, 4096), ctx=rng.choice([0, _spread(rng, 16, 8192)]))
+        return case
+    case.update(heads=kv_heads * rng.choice([1, 2, 4, 5, 7, 8]), causal=True, window=0)
+    if op == "step":
+        case.update(batch=_spread(rng, 1, 64), new=1, ctx=_spread(rng, 64, 8192))
+    elif rng.random() < 0.6:
+        case.update(batch=_spread(rng, 1, 96), new=rng.choice([1, 1, 1, rng.randint(2, 8)]), ctx=_spread(rng, 64, 65536))
+        case["window"] = rng.choice([0, 0, _spread(rng, 16, 8192)])
+    else:
+        case.update(batch=rng.randint(1, 8), new=_spread(rng, 16, 4096), ctx=rng.choice([0, _spread(rng, 16, 4096)]),
+                    causal=rng.random() < 0.8)
+        case["window"] = rng.choice([0, 0, _spread(rng, 16, 4096)]) if case["causal"] else 0
+    return case
+
+
+def _lens(case):
+    """(rows of this call, positions in the cache before it) of every sequence."""
+    r = random.Random(case["batch"] * 7919 + case["ctx"] * 31 + case["new"])
+    new, ctx = case["new"], case["ctx"]
+    if not case["ragged"]:
+        return [new] * case["batch"], [ctx] * case["batch"]
+    return ([r.randint(max(1, new // 4), new) for _ in range(case["batch"])],
+            [r.randint(ctx // 8, ctx) for _ in range(case["batch"])])
+
+
+# ---------------------------------------------------------------------------
+# inputs
+
+
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(int(seed))
+    return g
+
+
+def _normal(g, *shape, std=1.0):
+    return (torch.randn(*shape, generator=g, device=DEV) * std).bfloat16()
+
+
+def _frequencies(rot, base, scaling):
+    """Radians a position of every pair, and the factor of the rotated part.
+
+    yarn: slow pairs (less than one turn in 32768 positions) four times slower,
+    fast ones (over 32 turns) as they are, a ramp between."""
+    f = base ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=DEV) / rot)
+    if scaling == "plain":
+        return f, 1.0
+    keep = ((32768 * f / (2 * math.pi) - 1) / (32 - 1)).clamp(0, 1)
+    return f * keep + f / 4 * (1 - keep), 0.1 * math.log(4) + 1
+
+
+def _quantized(x):
+    """FP32 [..., 16 positions, dim] -> (E4M3 codes uint8, E8M0 codes uint8 [...])."""
+    c = _code(x.abs().amax((-1, -2)))
+    return torch.ldexp(x, (127 - c)[..., None, None]).to(torch.float8_e4m3fn).view(torch.uint8), c.to(torch.uint8)
+
+
+def _cache(g, case, lens, s):
+    """A cache whose pages are dealt out of order, with `lens` positions of every
+    sequence filled: keys with a few strong channels, values without."""
+    page, h, d = case["page"], case["kv_heads"], case["dim"]
+    need = [(n + page - 1) // page for n in lens]
+    pages = sum(need) + 3
+    std = torch.ones(2, 1, h, 1, d, device=DEV)
+    std[0, 0, :, 0, torch.randperm(d, generator=g, device=DEV)[:4]] = 6.0
+    codes = torch.empty(2, pages, h, page, d, dtype=torch.uint8, device=DEV)
+    scale = torch.empty(2, pages, h, page // BLOCK, dtype=torch.uint8, device=DEV)
+    step = max(1, (1 << 25) // (h * page * d))
+    for lo in range(0, pages, step):
+        n = min(step, pages - lo)
+        x = torch.randn(2, n, h, page, d, generator=g, device=DEV) * std
+        q, c = _quantized(x.view(2, n, h, page // BLOCK, BLOCK, d))
+        codes[:, lo:lo + n], scale[:, lo:lo + n] = q.view(2, n, h, page, d), c
+    deal = torch.randperm(pages, generator=g, device=DEV).int()
+    table = torch.full((len(lens), max(need) if max(need) else 1), -1, dtype=torch.int32, device=DEV)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = deal[at:at + n]
+        at += n
+    s.update(kv=codes, kv_scale=scale, table=table)
+
+
+def _starts(counts):
+    return torch.tensor([0] + counts, dtype=torch.int64).cumsum(0).to(DEV)
+
+
+def prepare(case, seed):
+    g = _gen(seed)
+    op = case["op"]
+    s = dict(case=case)
+    if op == "rope":
+        t, h, d = case["tokens"], case["heads"], case["dim"]
+        dtype = torch.bfloat16 if case["dtype"] == "bf16" else torch.float32
+        s["x"] = torch.randn(t, h, d, generator=g, device=DEV).to(dtype)
+        s["positions"] = torch.randint(0, case["span"], (t,), generator=g, device=DEV).int()
+        s["freqs"], s["amplitude"] = _frequencies(case["rot"], case["base"], case["scaling"])
+        if case["inverse"]:
+            s["dy"] = (torch.randn(t, h, d, generator=g, device=DEV) * 1e-2).to(dtype)
+        return s
+    new, ctx = _lens(case)
+    h, d, rows = case["kv_heads"], case["dim"], sum(new)
+    lens = [c + n for c, n in zip(ctx, new)]
+    _cache(g, case, lens, s)
+    s["starts"], s["lens"] = _starts(new), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    if op != "append":
+        # one projection's output holds queries, keys and values side by side
+        qkv = _normal(g, rows, case["heads"] + 2 * h, d, std=2.0 if op == "attention" else 1.0)
+        s["q"] = qkv[:, :case["heads"]]
+        s["scale"] = d ** -0.5
+        s["longest"] = max(lens)
+        s["most"] = max(new)
+        if op == "step":
+            s["k"], s["v"] = qkv[:, case["heads"]:case["heads"] + h], qkv[:, case["heads"] + h:]
+            s["positions"] = s["lens"] - 1
+    else:
+        kv = _normal(g, rows, 2, h, d)
+        s["k"], s["v"] = kv[:, 0], kv[:, 1]
+    if op != "attention":
+        # what is read back: the blocks that the call's rows lie in, up to their last row
+        back = [n + c % BLOCK for n, c in zip(new, ctx)]
+        s["back"], s["back_rows"] = _starts(back), sum(back)
+        s["freqs"], s["amplitude"] = _frequencies(d, case["base"], "plain")
+    return s
+
+
+# ---------------------------------------------------------------------------
+# plain forms
+
+
+def _code(amax):
+    """Largest finite magnitude -> E8M0 code of the least scale that keeps it within 448 = 0.875 * 2^9."""
+    m, e = torch.frexp(amax)
+    c = (e - 9 + (m > 0.875).int() + 127).clamp(0, 254)
+    return torch.where(amax > 0, c, 0)
+
+
+def _rotated(x, positions, freqs, amplitude, style, sign=1.0):
+    """FP32 rotation of [rows][heads][dim]; the angles and their sines in 64 bits."""
+    a = (positions.double()[:, None] * freqs)[:, None]
+    c, s = (a.cos() * amplitude).float(), (a.sin() * (amplitude * sign)).float()
+    rot = 2 * freqs.numel()
+    x = x.float()
+    y = x.clone()
+    if style == "half":
+        lo, hi = x[..., :rot // 2], x[..., rot // 2:rot]
+        y[..., :rot // 2], y[..., rot // 2:rot] = lo * c - hi * s, hi * c + lo * s
+    else:
+        lo, hi = x[..., 0:rot:2], x[..., 1:rot:2]
+        y[..., 0:rot:2], y[..., 1:rot:2] = lo * c - hi * s, hi * c + lo * s
+    return y
+
+
+def _places(s, starts, rows):
+    """(sequence, position) of every row."""
+    seq = torch.searchsorted(starts, torch.arange(rows, device=DEV), right=True) - 1
+    return seq, s["lens"].long()[seq] - starts[seq + 1] + torch.arange(rows, device=DEV)
+
+
+def _slots(s, seq, pos):
+    page = s["case"]["page"]
+    return s["table"].long()[seq, pos // page], pos % page
+
+
+def _append(s):
+    case, k, v = s["case"], s["k"], s["v"]
+    rows, h, d = k.shape
+    seq, pos = _places(s, s["starts"], rows)
+    pg, slot = _slots(s, seq, pos)
+    x = torch.stack([_rotated(k, pos, s["freqs"], s["amplitude"], case["style"]), v.float()])
+    per = case["page"] // BLOCK
+    blk = pg * per + slot // BLOCK  # number of the row's block among all pages'
+    heads = torch.arange(h, device=DEV)
+    scale = s["kv_scale"].permute(0, 1, 3, 2).reshape(2, -1, h).int()  # [2][pages * per][heads]
+    top = torch.zeros(2, scale.shape[1], h, device=DEV)
+    top.scatter_reduce_(1, blk[None, :, None].expand(2, rows, h), x.abs().amax(-1), "amax")
+    first = torch.full((scale.shape[1],), BLOCK, device=DEV).scatter_reduce_(0, blk, slot % BLOCK, "amin")
+    touched = (first < BLOCK)[None, :, None]
+    old = torch.where(touched & (first > 0)[None, :, None], scale, 0)
+    now = torch.where(touched, torch.maximum(_code(top), old), scale)
+    # the codes that the touched blocks hold before their first new row, rounded to the block's scale as it is now
+    at = torch.nonzero((first < BLOCK) & (first > 0)).flatten()
+    cells = s["kv"].view(2, -1, h, per, BLOCK, d)
+    was = cells[:, at // per, :, at % per].transpose(0, 1)  # (indexing puts the blocks first)
+    val = torch.ldexp(was.view(torch.float8_e4m3fn).float(), (old - now)[:, at, :, None, None]).to(torch.float8_e4m3fn)
+    keep = (torch.arange(BLOCK, device=DEV) < first[at, None])[None, :, None, :, None]
+    fresh = torch.where(keep, val.view(torch.uint8), was)
+    cells[:, at // per, :, at % per] = fresh.transpose(0, 1)
+    code = torch.ldexp(x, (127 - now[:, blk])[..., None]).to(torch.float8_e4m3fn).view(torch.uint8)
+    s["kv"][:, pg[:, None], heads, slot[:, None]] = code
+    s["kv_scale"].copy_(now.view(2, -1, per, h).permute(0, 1, 3, 2).to(torch.uint8))
+
+
+def _values(s, pg, slot):
+    """FP32 values [2][...][heads][dim] of the cache at the given pages and slots."""
+    h = torch.arange(s["kv"].shape[2], device=DEV)
+    q = s["kv"][:, pg[..., None], h, slot[..., None]].view(torch.float8_e4m3fn).float()
+    return torch.ldexp(q, (s["kv_scale"][:, pg[..., None], h, slot[..., None] // BLOCK].int() - 127)[..., None])
+
+
+def _read(s):
+    return list(_values(s, *_slots(s, *_places(s, s["back"], s["back_rows"]))).bfloat16())
+
+
+def _attention(s, q):
+    case = s["case"]
+    rows, heads, d = q.shape
+    hk, g = case["kv_heads"], heads // case["kv_heads"]
+    seq, pos = _places(s, s["starts"], rows)
+    i = torch.arange(rows, device=DEV) - s["starts"][seq]
+    t = torch.arange(s["longest"], device=DEV)
+    b = s["lens"].numel()
+    pg = s["table"].long()[:, t // case["page"]].clamp(min=0)
+    k, v = _values(s, pg, (t % case["page"]).expand(b, -1))  # [b][t][hk][d]
+    live = (t < s["lens"][:, None])[:, :, None, None]
+    k, v = torch.where(live, k, 0).permute(0, 2, 3, 1).contiguous(), torch.where(live, v, 0).permute(0, 2, 1, 3).contiguous()
+    wide = torch.zeros(b, s["most"], hk, g, d, device=DEV)
+    wide[seq, i] = q.float().view(rows, hk, g, d)
+    at = torch.full((b, s["most"]), -1, dtype=torch.long, device=DEV)
+    at[seq, i] = pos
+    see = (t < s["lens"][:, None])[:, None, :] & (at >= 0)[:, :, None]
+    if case["causal"]:
+        see = see & (t <= at[:, :, None])
+        if case["window"]:
+            see = see & (t > at[:, :, None] - case["window"])
+    see = see[:, None, :, None, :]  # [b][1][n][1][t]
+    x = (wide.permute(0, 2, 1, 3, 4).reshape(b, hk, -1, d) @ k).view(b, hk, s["most"], g, -1) * s["scale"]
+    x = torch.where(see, x, NEG)
+    m = x.amax(-1, keepdim=True)
+    p = torch.where(see, torch.exp(x - torch.where(m == NEG, 0, m)), 0)
+    total = p.sum(-1, keepdim=True)
+    o = (p.view(b, hk, -1, p.shape[-1]) @ v).view(b, hk, s["most"], g, d) / torch.where(total > 0, total, 1)
+    lse = (m + torch.log(total)).squeeze(-1)
+    return [o.permute(0, 2, 1, 3, 4)[seq, i].reshape(rows, heads, d).bfloat16(),
+            lse.permute(0, 2, 1, 3)[seq, i].reshape(rows, heads)]
+
+
+def _plain(s):
+    case = s["case"]
+    if case["op"] == "rope":
+        how = (s["positions"], s["freqs"], s["amplitude"], case["style"])
+        out = [_rotated(s["x"], *how).to(s["x"].dtype)]
+        if case["inverse"]:
+            out.append(_rotated(s["dy"], *how, sign=-1.0).to(s["x"].dtype))
+        return out
+    if case["op"] == "attention":
+        return _attention(s, s["q"])
+    _append(s)
+    if case["op"] == "append":
+        return _read(s)
+    q = _rotated(s["q"], s["positions"], s["freqs"], s["amplitude"], case["style"]).bfloat16()
+    return _attention(s, q) + _read(s)
+
+
+# ---------------------------------------------------------------------------
+# the library's calls
+
+
+def _own(s):
+    import mxfp8_block_scaled_08_amd as mx
+
+    case = s["case"]
+    op = case["op"]
+    if op != "attention":
+        how = dict(style=case["style"], amplitude=s["amplitude"])
+    if op == "rope":
+        out = [mx.mx_rope(s["x"], s["positions"], s["freqs"], **how)]
+        if case["inverse"]:
+            out.append(mx.mx_rope_bwd(s["dy"], s["positions"], s["freqs"], **how))
+        return out
+    cache = (s["kv"], s["kv_scale"], s["table"], s["lens"])
+    out, q = [], s.get("q")
+    if op != "attention":
+        if op == "step":
+            q = mx.mx_rope(q, s["positions"], s["freqs"], **how)
+        mx.mx_kv_append(s["k"], s["v"], *cache, s["starts"], freqs=s["freqs"], **how)
+    if op != "append":
+        out += mx.mx_kv_attention(q, *cache, s["starts"], scale=s["scale"], causal=case["causal"],
+                                  window=case["window"], want_lse=True)
+    if op != "attention":
+        out += mx.mx_kv_read(*cache, s["back"], s["back_rows"])
+    return out
+
+
+def run(state):
+    return _own(state) if own else _plain(state)
+
+
+# ---------------------------------------------------------------------------
+# least work, and the definition in 64 bits
+
+
+def work(case):
+    op, d = case["op"], case["dim"]
+    if op == "rope":
+        n = case["tokens"] * case["heads"] * d * (2 if case["inverse"] else 1)
+        return dict(bytes=n * 2 * (2 if case["dtype"] == "bf16" else 4) + 4 * case["tokens"], flops=3 * n)
+    new, ctx = _lens(case)
+    h, rows = case["kv_heads"], sum(new)
+    cell = 2 * h * (d + 1 / BLOCK)  # a position's codes and scales
+    n = f = 0
+    if op != "attention":
+        # the rows in, their codes out; the blocks' codes back in and their values out
+        back = sum(a + c % BLOCK for a, c in zip(new, ctx))
+        n += rows * (4 * h * d + cell) + back * (4 * h * d + cell)
+        f += rows * 10 * h * d
+    if op != "append":
+        w = case["window"] or 1 << 40
+        pairs = read = 0
+        for a, c in zip(new, ctx):
+            if case["causal"]:
+                full = max(0, min(a, w - c))  # rows whose whole past lies in the window
+                pairs += full * c + full * (full + 1) // 2 + (a - full) * w
+                read += min(c + a, w + a - 1)
+            else:
+                pairs += a * (a + c)
+                read += a + c
+        n += read * cell + rows * case["heads"] * (4 * d + 4)
+        f += pairs * case["heads"] * 4 * d
+        if op == "step":
+            n += rows * case["heads"] * 4 * d
+    return dict(bytes=n, flops=f)
+
+
+def _e4m3_table():
+    c = torch.arange(256, device=DEV)
+    e, m = (c >> 3 & 15).double(), (c & 7).double()
+    mag = torch.where(e > 0, (8 + m) * torch.exp2(e - 10), m * 2.0 ** -9)
+    mag[127] = mag[255] = float("nan")
+    return torch.where(c > 127, -mag, mag)
+
+
+def _to_grid(v, e):
+    """v rounded to the E4M3 values times 2^e (|v| <= 448 * 2^e), ties to even."""
+    u = v / torch.exp2(e)
+    lead = (torch.frexp(u).exponent - 1).clamp(min=-6)
+    step = torch.exp2((lead - 3).double())
+    return torch.round(u / step) * step * torch.exp2(e)
+
+
+def _turned(x, positions, freqs, amplitude, style, back=False):
+    """The rotation as a product of complex numbers."""
+    rot = 2 * freqs.numel()
+    a = positions.double()[:, None, None] * freqs
+    z = torch.polar(torch.full_like(a, amplitude), -a if back else a)
+    x = x.double()
+    part = x[..., :rot]
+    pair = part.unflatten(-1, (2, rot // 2)).transpose(-1, -2) if style == "half" else part.unflatten(-1, (rot // 2, 2))
+    y = torch.view_as_real(torch.view_as_complex(pair.contiguous()) * z)
+    y = (y.transpose(-1, -2) if style == "half" else y).reshape(part.shape)
+    return torch.cat([y, x[..., rot:]], -1)
+
+
+def _held(s, b, n):
+    """The first n positions' values of sequence b, [2][n][heads][dim], and their scales' exponents [2][n][heads]."""
+    page = s["case"]["page"]
+    t = torch.arange(n, device=DEV)
+    pg = s["table"][b].long()[t // page]
+    e = s["kv_scale"].transpose(2, 3)[:, pg, t % page // BLOCK].double() - 127
+    return _e4m3_table()[s["kv"].transpose(2, 3)[:, pg, t % page].long()] * torch.exp2(e)[..., None], e
+
+
+def _exact_append(case, s):
+    """Sequence by sequence: the values that the blocks in reach hold afterwards, and those behind `ctx` to be attended to."""
+    new, ctx = _lens(case)
+    seqs, back, lo = [], [], 0
+    for b, (n, c) in enumerate(zip(new, ctx)):
+        pos = torch.arange(c, c + n, device=DEV)
+        k = _turned(s["k"][lo:lo + n], pos, s["freqs"], s["amplitude"], case["style"])
+        x = torch.stack([k, s["v"][lo:lo + n].double()])
+        lo += n
+        before, e_old = _held(s, b, c)
+        a = c // BLOCK * BLOCK  # the first block in reach
+        pad = -(c + n) % BLOCK
+        zeros = x.new_zeros(2, c - a, *x.shape[2:])
+        fresh = torch.cat([zeros, x, x.new_zeros(2, pad, *x.shape[2:])], 1)
+        blocks = fresh.unflatten(1, (-1, BLOCK))
+        top = blocks.abs().amax((2, 4))
+        m, e = torch.frexp(top)
+        e = torch.where(top > 0, (e - 9 + (m > 0.875).int()).clamp(min=-127), -127).double()
+        if c > a:
+            e[:, 0] = torch.maximum(e[:, 0], e_old[:, a])
+            blocks[:, 0, :c - a] = before[:, a:]
+        held = _to_grid(blocks, e[:, :, None, :, None]).flatten(1, 2)[:, :c - a + n]
+        back.append(held)
+        seqs.append(torch.cat([before[:, :a], held], 1))
+    return seqs, list(torch.cat(back, 1))
+
+
+def _exact_attention(case, s, q, seqs):
+    new, ctx = _lens(case)
+    g = case["heads"] // case["kv_heads"]
+    outs, lses, lo = [], [], 0
+    for b, (n, c) in enumerate(zip(new, ctx)):
+        kv = seqs[b] if seqs is not None else _held(s, b, c + n)[0]
+        t, p = torch.arange(c + n, device=DEV), torch.arange(c, c + n, device=DEV)[:, None]
+        hide = torch.zeros(n, c + n, dtype=torch.bool, device=DEV)
+        if case["causal"]:
+            hide = t > p
+            if case["window"]:
+                hide = hide | (t <= p - case["window"])
+        o = torch.empty(n, case["heads"], case["dim"], dtype=torch.float64, device=DEV)
+        lse = torch.empty(n, case["heads"], dtype=torch.float64, device=DEV)
+        for h in range(case["heads"]):
+            x = (q[lo:lo + n, h].double() @ kv[0, :, h // g].t().contiguous()) * s["scale"]
+            x.masked_fill_(hide, NEG)
+            lse[:, h] = torch.logsumexp(x, 1)
+            o[:, h] = torch.exp(x - lse[:, h, None]) @ kv[1, :, h // g].contiguous()
+        outs.append(o)
+        lses.append(lse)
+        lo += n
+    return [torch.cat(outs), torch.cat(lses)]
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] == "rope":
+        how = (s["positions"], s["freqs"], s["amplitude"], case["style"])
+        out = [_turned(s["x"], *how)]
+        return out + [_turned(s["dy"], *how, back=True)] if case["inverse"] else out
+    if case["op"] == "attention":
+        return _exact_attention(case, s, s["q"], None)
+    seqs, back = _exact_append(case, s)
+    if case["op"] == "append":
+        return back
+    # the queries reach the attention as BF16
+    q = _turned(s["q"], s["positions"], s["freqs"], s["amplitude"], case["style"]).to(torch.bfloat16)
+    return _exact_attention(case, s, q, seqs) + back

@@ -385,7 +385,7 @@ def _own(s):
         mx.mx_kv_append(s["k"], s["v"], *cache, s["starts"], freqs=s["freqs"], **how)
     if op != "append":
         out += mx.mx_kv_attention(q, *cache, s["starts"], scale=s["scale"], causal=case["causal"],
-                                  window=case["window"], want_lse=True)
+                                  window=case["window"], max_new=s["most"], want_lse=True)
     if op != "attention":
         out += mx.mx_kv_read(*cache, s["back"], s["back_rows"])
     return out

@@ -12,7 +12,9 @@ the weights with the learner's quantizer, MXFP8 GEMMs; Table 6: GEMM,
 quantization and scale-rearrangement kernels; Table 2: dense Qwen3-8B and
 the 128-expert Qwen3-30B-A3B MoE).  ``moe_fp4.py`` holds the second part's
 functions (``include/mxfp8_moe_fp4.h``: routing to experts and its gradient,
-the combine's gradient, MXFP4), which are exported here with the others.
+the combine's gradient, MXFP4) and ``kv.py`` the third's
+(``include/mxfp8_kv.h``: rotary positions, the 8-bit paged cache and its
+attention); they are exported here with the others.
 """
 from __future__ import annotations
 
@@ -35,6 +37,9 @@ __all__ = [
     "mx_moe_route", "mx_moe_route_bwd", "mx_moe_combine_bwd", "mx_quantize_rowwise_fp4", "mx_quantize_colwise_fp4",
     "mx_dequantize_fp4", "mx_moe_dispatch_fp4", "mx_swiglu_quantize_fp4", "mx_gemm_fp4", "mx_gemm_fp4_workspace_bytes",
     "mx_grouped_gemm_fp4", "MX_SCORE_SOFTMAX", "MX_SCORE_SIGMOID",
+    "mx_rope_frequencies", "mx_rope", "mx_rope_bwd", "mx_kv_append", "mx_kv_read", "mx_kv_attention",
+    "mx_kv_attention_workspace_bytes", "MX_KV_BLOCK", "MX_ROPE_HALF", "MX_ROPE_INTERLEAVED", "MX_ROPE_PLAIN",
+    "MX_ROPE_LINEAR", "MX_ROPE_NTK", "MX_ROPE_YARN",
 ]
 
 MX_OK, MX_ERR_INVALID_ARG, MX_ERR_SHAPE, MX_ERR_ALIGN = 0, 1, 2, 3
@@ -787,3 +792,8 @@ from .moe_fp4 import (MX_SCORE_SIGMOID, MX_SCORE_SOFTMAX, mx_dequantize_fp4, mx_
                       mx_gemm_fp4_workspace_bytes, mx_grouped_gemm_fp4, mx_moe_combine_bwd, mx_moe_dispatch_fp4,
                       mx_moe_route, mx_moe_route_bwd, mx_quantize_colwise_fp4, mx_quantize_rowwise_fp4,
                       mx_swiglu_quantize_fp4)
+
+# rotary positions, the 8-bit paged cache and its attention (include/mxfp8_kv.h)
+from .kv import (MX_KV_BLOCK, MX_ROPE_HALF, MX_ROPE_INTERLEAVED, MX_ROPE_LINEAR, MX_ROPE_NTK, MX_ROPE_PLAIN,  # noqa: E402
+                 MX_ROPE_YARN, mx_kv_append, mx_kv_attention, mx_kv_attention_workspace_bytes, mx_kv_read, mx_rope,
+                 mx_rope_bwd, mx_rope_frequencies)

@@ -8,8 +8,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build", "mxfp8")
 LIB = os.path.join(PKG, "libmxfp8.so")
-SOURCES = ["mx_api.cpp", "mx_api_route.cpp", "mx_api_fp4.cpp", "mx_quantize.hip", "mx_gemm.hip", "mx_moe.hip",
-           "mx_moe_bwd.hip", "mx_route.hip", "mx_fp4.hip", "mx_gemm_fp4.hip", "mx_debug.hip"]
+SOURCES = ["mx_api.cpp", "mx_api_route.cpp", "mx_api_fp4.cpp", "mx_api_kv.cpp", "mx_quantize.hip", "mx_gemm.hip",
+           "mx_moe.hip", "mx_moe_bwd.hip", "mx_route.hip", "mx_fp4.hip", "mx_gemm_fp4.hip", "mx_rope.hip", "mx_kv.hip",
+           "mx_kv_attention.hip", "mx_debug.hip"]
 ARCH = "gfx950"
 
 # -packed-fp32-ops: keep the compiler from forming packed FP32 VALU ops.

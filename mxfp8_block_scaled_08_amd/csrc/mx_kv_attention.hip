@@ -1,0 +1,1101 @@
+// Attention over the paged 8-bit cache (gfx950).
+//
+//   out = softmax(scale q K^T) V,  K = E4M3 codes * 2^k, V likewise
+//
+// Rows of a (sequence, key/value head) are its new tokens times the query heads that
+// share the head: one read of keys and values serves the whole group.  Products go through
+// the BF16 matrix cores: an E4M3 value times a power of two is exact in BF16, and the
+// conversion (v_cvt_scalef32_pk_bf16_fp8) applies the block's scale on the way.  Both kernels
+// form S^T = K Q^T, so that a lane holds one row's scores, and O^T = V^T P^T with the
+// positions of a product's k axis in the order in which the first product leaves them: the
+// weights go from one product into the next in registers.
+//
+// One pass with a running maximum m and sum l per row.  The maximum is raised only where a
+// score passes it by more than 2^8 (weights stay below 2^8: neither FP32 nor BF16 minds), so the
+// accumulators are rarely rescaled.  Weights are rounded to BF16 for the product with V, the
+// sum takes them unrounded.
+//
+// Few rows (up to 64 a sequence and head; a sampler's step): kv_rows_kernel.  Bound by reading the
+// cache.  A wave reads 32 positions' codes straight into registers in the matrix cores' layout, V
+// transposed there by byte permutes; no LDS but for the four waves' join.  The work, chunks of 128
+// positions of every (sequence, head, tile of rows), lies on one line that is cut into equal pieces,
+// one a workgroup, so uneven sequences load the chip evenly; pieces of one item meet in
+// kv_join_kernel.
+//
+// Many rows (prompts): kv_tiles_kernel.  Bound by the matrix cores and the exponentials.  128 rows
+// a workgroup, 64 positions a step, converted once into LDS (double buffered).
+#include "mx_kv_device.h"
+
+#include <algorithm>
+
+namespace mx {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+constexpr int KVA_THREADS = 256;
+constexpr int KVA_CHUNK = 128;      // positions of a piece of work, 32 a wave
+constexpr int KVA_FEW = 64;         // rows of a sequence and head that the few-row kernel takes
+constexpr int KVA_TILE = 128;       // rows of a workgroup of the other
+constexpr int KVA_STEP = 64;        // positions of its steps
+constexpr float KVA_SLACK = 8.0f;   // log2 of what a weight may exceed 1 by
+constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
+#define KVA_NEG (-__builtin_inff())
+
+// Read-only tables through the scalar unit: the constant address space.
+typedef const int32_t __attribute__((address_space(4))) *ConstI32;
+
+struct KvPlan {
+    char *ws;          // see KvSpace
+    int64_t off_first; // byte offsets in ws
+    int64_t off_ml, off_acc;
+    int32_t few;       // rows up to which a sequence is the few-row kernel's
+    int32_t groups;    // workgroups of the few-row kernel
+    int32_t splits;    // ranges of positions of the other
+    int32_t tiles;     // its tiles of rows, at most
+};
+
+// What a row of a tile sees: positions [lo, hi].
+struct Seen {
+    int32_t lo, hi;
+};
+
+__device__ __forceinline__ Seen seen_by(const KvQueries &q, const SeqRows &s, int32_t token)
+{
+    const int64_t p = s.pos + token;
+    Seen r{0, s.kv_len - 1};
+    if (q.causal) {
+        r.hi = (int32_t)min(p, (int64_t)r.hi);
+        if (q.window)
+            r.lo = (int32_t)max(p - q.window + 1, (int64_t)0);
+    }
+    return r;
+}
+
+// First position that any row of the sequence sees, down to a whole block.
+__device__ __forceinline__ int32_t first_seen(const KvQueries &q, const SeqRows &s)
+{
+    return q.window ? (int32_t)max(s.pos - q.window + 1, (int64_t)0) & ~15 : 0;
+}
+
+__device__ __forceinline__ int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v)
+{
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+__device__ __forceinline__ SeqRows uniform(SeqRows s)
+{
+    s.row = uniform(s.row);
+    s.n = uniform(s.n);
+    s.pos = uniform(s.pos);
+    s.kv_len = uniform(s.kv_len);
+    return s;
+}
+
+__device__ __forceinline__ float max_xor32(float v)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    return fmaxf(__builtin_bit_cast(float, r[0]), __builtin_bit_cast(float, r[1]));
+}
+
+__device__ __forceinline__ float max_xor16(float v)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    return fmaxf(__builtin_bit_cast(float, r[0]), __builtin_bit_cast(float, r[1]));
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// m * c with -inf kept (0 * -inf is NaN where the scale is 0).
+__device__ __forceinline__ float scaled_max(float m, float c) { return m == KVA_NEG ? KVA_NEG : m * c; }
+
+// Whether a word holds a NaN code.
+__device__ __forceinline__ bool nan_codes(uint32_t w)
+{
+    return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+}
+
+// Scale codes from here on can take a finite code past BF16's range.
+constexpr uint32_t KVA_BIG_SCALE = 247;
+
+// ---------------------------------------------------------------------------
+// few rows
+
+// A page's part for one block of 16 positions, the same for every lane of the wave.
+struct BlockAt {
+    int64_t codes;  // offset of the block's first row
+    int64_t scale;
+    bool ok;
+};
+
+__device__ __forceinline__ BlockAt block_at(const KvView &c, int b, int32_t h, int32_t blk)
+{
+    const int32_t shift = c.page_shift - 4;
+    const int32_t i = blk >> shift;
+    const ConstI32 table = (ConstI32)(uintptr_t)c.table;
+    const int32_t p = table[(int64_t)b * c.max_pages + min(max(i, 0), c.max_pages - 1)];
+    BlockAt r;
+    r.ok = (uint32_t)p < (uint32_t)c.num_pages && i < c.max_pages;
+    const int64_t page = r.ok ? p : 0;
+    const int32_t in = blk & ((1 << shift) - 1);
+    r.codes = page * c.ld_page + h * c.ld_head + (int64_t)(in * 16) * c.ld_token;
+    r.scale = ((page * c.kv_heads + h) << shift) + in;
+    return r;
+}
+
+// 32 positions' codes in a wave: K rows t = 16 j + (lane & 15), bytes 64 i + 16 (lane >> 4) ..; V rows
+// t = 16 (e >> 2) + 4 (lane >> 4) + (e & 3), bytes (D / 16) (lane & 15) ..
+template <int D> struct Codes {
+    uint4 k[2][D / 64];
+    uint32_t v[8][D / 64];
+    uint32_t ks[2], vs[2];
+    bool ok[2];
+};
+
+template <int D>
+__device__ __forceinline__ void load_codes(const KvView &c, const BlockAt (&at)[2], uint32_t koff, uint32_t voff, Codes<D> &t)
+{
+    const uint32_t ld = (uint32_t)c.ld_token;
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+        const uint8_t *kb = c.k + at[j].codes, *vb = c.v + at[j].codes;
+#pragma unroll
+        for (int i = 0; i < D / 64; i++)
+            t.k[j][i] = *reinterpret_cast<const uint4 *>(kb + koff + 64 * i);
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            if constexpr (D == 128) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(vb + voff + e * ld);
+                t.v[4 * j + e][0] = w.x;
+                t.v[4 * j + e][1] = w.y;
+            } else {
+                t.v[4 * j + e][0] = *reinterpret_cast<const uint32_t *>(vb + voff + e * ld);
+            }
+        t.ks[j] = c.k_scale[at[j].scale];
+        t.vs[j] = c.v_scale[at[j].scale];
+        t.ok[j] = at[j].ok;
+    }
+}
+
+union Frag {
+    uint32_t w[4];
+    bf16x8_t f;
+};
+
+// O^T += V^T P^T for every tile of 16 rows; V's words as in Codes.
+template <int D, int NT>
+__device__ __forceinline__ void values_product(const uint32_t (&v)[8][D / 64], const uint32_t (&vs)[2], const Frag (&p)[NT],
+                                               f32x4_t (&o)[NT][D / 16])
+{
+    const float s0 = cvt_scale(vs[0]), s1 = cvt_scale(vs[1]);
+#pragma unroll
+    for (int w = 0; w < D / 64; w++) {
+        Frag a[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            // (rows 2e, 2e + 1): bytes 0 and 1 of both, then bytes 2 and 3
+            const uint32_t lo = __builtin_amdgcn_perm(v[2 * e + 1][w], v[2 * e][w], 0x05010400u);
+            const uint32_t hi = __builtin_amdgcn_perm(v[2 * e + 1][w], v[2 * e][w], 0x07030602u);
+            const float s = e < 2 ? s0 : s1;
+            a[0].w[e] = e4m3_bf16<false>(lo, s);
+            a[1].w[e] = e4m3_bf16<true>(lo, s);
+            a[2].w[e] = e4m3_bf16<false>(hi, s);
+            a[3].w[e] = e4m3_bf16<true>(hi, s);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+                o[n][4 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j].f, p[n].f, o[n][4 * w + j], 0, 0, 0);
+    }
+}
+
+template <int D, int NT> struct RowState {
+    uint4 q[NT][D / 32];
+    f32x4_t o[NT][D / 16];
+    float m[NT], l[NT];
+    Seen see[NT];
+};
+
+// One wave's 32 positions from t0 on.  masked: some row does not see some of them.
+template <int D, int NT>
+__device__ __forceinline__ void rows_step(const KvView &c, RowState<D, NT> &r, Codes<D> &t, int32_t t0, int32_t kv_len,
+                                          float c2, bool masked)
+{
+    const int g = (threadIdx.x & 63) >> 4;
+    f32x4_t s[2][NT];
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+        const float ks = cvt_scale(t.ks[j]);
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+            s[j][n] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < D / 64; i++) {
+            const uint32_t w[4] = {t.k[j][i].x, t.k[j][i].y, t.k[j][i].z, t.k[j][i].w};
+#pragma unroll
+            for (int hh = 0; hh < 2; hh++) {
+                Frag a;
+                a.w[0] = e4m3_bf16<false>(w[2 * hh], ks);
+                a.w[1] = e4m3_bf16<true>(w[2 * hh], ks);
+                a.w[2] = e4m3_bf16<false>(w[2 * hh + 1], ks);
+                a.w[3] = e4m3_bf16<true>(w[2 * hh + 1], ks);
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+                    s[j][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.f, __builtin_bit_cast(bf16x8_t, r.q[n][2 * i + hh]),
+                                                                      s[j][n], 0, 0, 0);
+            }
+        }
+    }
+    // (a scale code of 0xFF is NaN, whatever the code)
+#pragma unroll
+    for (int j = 0; j < 2; j++)
+        if (t.ks[j] == 0xFFu)
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+                s[j][n] = __builtin_nanf("") + s[j][n];
+    uint32_t vis[NT] = {};  // bit 4 j + i: the row sees position t0 + 16 j + 4 g + i
+    if (masked) {
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int32_t p = t0 + 16 * j + 4 * g + i;
+                    const bool y = t.ok[j] && p >= r.see[n].lo && p <= r.see[n].hi;
+                    vis[n] |= y ? 1u << (4 * j + i) : 0u;
+                    s[j][n][i] = y ? s[j][n][i] : KVA_NEG;
+                }
+    }
+    Frag p[NT];
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+        float mt = fmaxf(fmaxf(fmaxf(s[0][n][0], s[0][n][1]), fmaxf(s[0][n][2], s[0][n][3])),
+                         fmaxf(fmaxf(s[1][n][0], s[1][n][1]), fmaxf(s[1][n][2], s[1][n][3])));
+        mt = max_xor16(max_xor32(mt));
+        if (__any(mt > r.m[n] && !((mt - r.m[n]) * c2 <= KVA_SLACK))) {
+            const float now = fmaxf(r.m[n], mt);
+            const float f = r.m[n] == KVA_NEG ? 0.0f : exp2_fast((r.m[n] - now) * c2);
+            r.m[n] = now;
+            r.l[n] *= f;
+#pragma unroll
+            for (int j = 0; j < D / 16; j++)
+                r.o[n][j] *= f;
+        }
+        const float mc = r.m[n] == KVA_NEG ? 0.0f : r.m[n] * c2;
+        float e[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            e[i] = exp2_fast(fmaf(s[i >> 2][n][i & 3], c2, -mc));
+        if (masked)
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                e[i] = (vis[n] >> i & 1) ? e[i] : 0.0f;
+        r.l[n] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            p[n].w[i] = pack_bf16(e[2 * i], e[2 * i + 1]);
+    }
+    bool odd = false;
+    if (masked) {
+        // what no row sees behind the last position may hold anything
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            if (!t.ok[j] || t0 + 16 * j >= kv_len)
+                t.vs[j] = 127;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const bool in = t.ok[j] && t0 + 16 * j + 4 * g + e < kv_len;
+#pragma unroll
+                for (int w = 0; w < D / 64; w++) {
+                    t.v[4 * j + e][w] = in ? t.v[4 * j + e][w] : 0u;
+                    odd = odd || nan_codes(t.v[4 * j + e][w]);
+                }
+            }
+            odd = odd || t.vs[j] >= KVA_BIG_SCALE;
+        }
+        odd = __any(odd);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; j++)
+        if (t.vs[j] == 0xFFu)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+#pragma unroll
+                for (int w = 0; w < D / 64; w++)
+                    t.v[4 * j + e][w] = 0x7F7F7F7Fu;
+    if (!odd) {
+        values_product<D, NT>(t.v, t.vs, p, r.o);
+        return;
+    }
+    // NaN or infinite values that some row does not see: a weight of 0 does not keep them out of a
+    // sum, so each position goes by itself, into the rows that see it
+#pragma unroll 1
+    for (int at = 0; at < 32; at++) {
+        const int mine = (at & 15) >> 2 == g ? 4 * (at >> 4) + (at & 3) : -1;
+        uint32_t v[8][D / 64];
+        Frag one[NT];
+        f32x4_t o[NT][D / 16];
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+#pragma unroll
+            for (int w = 0; w < D / 64; w++)
+                v[e][w] = e == mine ? t.v[e][w] : 0u;
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                one[n].w[i] = mine == 2 * i ? p[n].w[i] & 0xFFFFu : mine == 2 * i + 1 ? p[n].w[i] & 0xFFFF0000u : 0u;
+#pragma unroll
+            for (int j = 0; j < D / 16; j++)
+                o[n][j] = f32x4_t{0, 0, 0, 0};
+        }
+        values_product<D, NT>(v, t.vs, one, o);
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            const bool y = t.ok[at >> 4] && t0 + at >= r.see[n].lo && t0 + at <= r.see[n].hi;
+#pragma unroll
+            for (int j = 0; j < D / 16; j++)
+                r.o[n][j] += y ? o[n][j] : f32x4_t{0, 0, 0, 0};
+        }
+    }
+}
+
+// Work of a sequence on the line: chunks of an item, and items.
+struct SeqWork {
+    int32_t chunks, tiles;  // tiles of 16 NT rows
+    int64_t all;            // chunks * tiles * kv_heads
+};
+
+template <int NT>
+__device__ __forceinline__ SeqWork seq_work(const KvView &c, const KvQueries &q, const SeqRows &s, int32_t few)
+{
+    SeqWork w{0, 0, 0};
+    const int64_t rows = s.n * q.group;
+    if (rows < 1 || rows > few)
+        return w;
+    w.tiles = (int32_t)((rows + 16 * NT - 1) / (16 * NT));
+    w.chunks = max((s.kv_len - first_seen(q, s) + KVA_CHUNK - 1) / KVA_CHUNK, 1);  // (an item of none still writes its zeros)
+    w.all = (int64_t)w.chunks * w.tiles * c.kv_heads;
+    return w;
+}
+
+// Inclusive sum over the workgroup's threads, and the whole.
+__device__ __forceinline__ int64_t scan_sum(int64_t v, int64_t &total, int64_t *lds)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t o = __shfl_up(v, d, 64);
+        v += lane >= d ? o : 0;
+    }
+    if (lane == 63)
+        lds[wave] = v;
+    __syncthreads();
+    total = 0;
+    int64_t before = 0;
+#pragma unroll
+    for (int w = 0; w < KVA_THREADS / 64; w++) {
+        before += w < wave ? lds[w] : 0;
+        total += lds[w];
+    }
+    __syncthreads();
+    return before + v;
+}
+
+template <int D> struct Join {
+    float ml[4][16][2];
+    float acc[4][16][D + 4];
+};
+
+__device__ __forceinline__ void store_out(const KvQueries &q, int64_t row, int32_t head, int32_t d, const float *v, int n)
+{
+    uint16_t *p = q.out + row * q.ld_ot + head * q.ld_oh + d;
+    for (int i = 0; i < n; i += 4)
+        *reinterpret_cast<uint2 *>(p + i) = make_uint2(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]));
+}
+
+template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS) void kv_rows_kernel(KvView c, KvQueries q, KvPlan plan)
+{
+    __shared__ Join<D> lds;
+    __shared__ int64_t lds_sum[4], lds_at[2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int g = lane >> 4, col = lane & 15;
+    const float c2 = q.scale * LOG2E;
+    int64_t *first = (int64_t *)(plan.ws + plan.off_first);  // [batch] starts on the line, then pieces' length
+
+    // the line's length, and where this workgroup's piece starts
+    int64_t all = 0, here = 0, mine = 0;
+    for (int b0 = 0; b0 < c.batch; b0 += KVA_THREADS) {
+        const int b = b0 + tid;
+        const int64_t w = b < c.batch ? seq_work<NT>(c, q, seq_rows(c, b), plan.few).all : 0;
+        int64_t sum;
+        const int64_t upto = scan_sum(w, sum, lds_sum);
+        if (b0 == 0) {
+            here = upto;
+            mine = w;
+        }
+        if (blockIdx.x == 0 && b < c.batch)
+            first[b] = all + upto - w;
+        all += sum;
+    }
+    const int64_t piece = max((all + plan.groups - 1) / plan.groups, (int64_t)1);
+    if (blockIdx.x == 0 && tid == 0)
+        first[c.batch] = piece;
+    int64_t at = (int64_t)blockIdx.x * piece;
+    const int64_t end = min(at + piece, all);
+    if (at >= end)
+        return;
+    int64_t before = 0;
+    for (int b0 = 0;; b0 += KVA_THREADS) {
+        int64_t sum = 0;
+        if (b0 > 0) {
+            const int b = b0 + tid;
+            mine = b < c.batch ? seq_work<NT>(c, q, seq_rows(c, b), plan.few).all : 0;
+            here = scan_sum(mine, sum, lds_sum);
+        }
+        if (at >= before + here - mine && at < before + here) {
+            lds_at[0] = b0 + tid;
+            lds_at[1] = before + here - mine;
+        }
+        // (only the first 256 sequences' sum is not at hand)
+        if (__syncthreads_or(at >= before + here - mine && at < before + here))
+            break;
+        if (b0 == 0)
+            here = scan_sum(mine, sum, lds_sum);
+        before += sum;
+        if (b0 + KVA_THREADS >= c.batch)
+            return;
+    }
+    int b = uniform((int32_t)lds_at[0]);
+    int64_t start = uniform(lds_at[1]);
+    SeqRows s = uniform(seq_rows(c, b));
+    SeqWork w = seq_work<NT>(c, q, s, plan.few);
+    bool head_piece = true;
+
+    while (at < end) {
+        while (at >= start + w.all) {
+            start += w.all;
+            if (++b >= c.batch)
+                return;
+            s = uniform(seq_rows(c, b));
+            w = seq_work<NT>(c, q, s, plan.few);
+        }
+        const int64_t off = at - start;
+        const int32_t item = uniform((int32_t)(off / w.chunks));
+        const int32_t c0 = uniform((int32_t)(off - (int64_t)item * w.chunks));
+        const int32_t c1 = uniform((int32_t)min((int64_t)w.chunks, c0 + (end - at)));
+        const int32_t h = item / w.tiles, tile = item - h * w.tiles;
+        const int32_t rows = (int32_t)s.n * q.group;
+
+        RowState<D, NT> r;
+        int32_t all_lo = 0, all_hi = 0x7FFFFFFF;  // what every row sees
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            const int32_t row = min((tile * NT + n) * 16 + col, rows - 1);
+            const int32_t token = row / q.group, head = h * q.group + row - token * q.group;
+            const uint16_t *p = q.q + (s.row + token) * q.ld_qt + head * q.ld_qh + 16 * g;
+#pragma unroll
+            for (int i = 0; i < D / 32; i++)
+                r.q[n][i] = *reinterpret_cast<const uint4 *>(p + 64 * (i >> 1) + 8 * (i & 1));
+#pragma unroll
+            for (int j = 0; j < D / 16; j++)
+                r.o[n][j] = f32x4_t{0, 0, 0, 0};
+            r.m[n] = KVA_NEG;
+            r.l[n] = 0.0f;
+            r.see[n] = seen_by(q, s, token);
+        }
+        {
+            const Seen a = seen_by(q, s, min(tile * NT * 16, rows - 1) / q.group);
+            const Seen z = seen_by(q, s, min((tile + 1) * NT * 16 - 1, rows - 1) / q.group);
+            all_lo = z.lo;
+            all_hi = a.hi;
+        }
+        const int32_t t_first = first_seen(q, s) + wave * 32;
+        const uint32_t koff = (uint32_t)(col * c.ld_token) + 16 * g;
+        const uint32_t voff = (uint32_t)(4 * g * c.ld_token) + (D / 16) * col;
+        auto at_chunk = [&](int32_t i, BlockAt (&x)[2]) {
+            const int32_t blk = (t_first + min(i, c1 - 1) * KVA_CHUNK) >> 4;
+            x[0] = block_at(c, b, h, blk);
+            x[1] = block_at(c, b, h, blk + 1);
+        };
+        BlockAt x[2];
+        Codes<D> cur, next;
+        at_chunk(c0, x);
+        load_codes<D>(c, x, koff, voff, cur);
+        at_chunk(c0 + 1, x);
+        for (int32_t i = c0; i < c1; i++) {
+            if (i + 1 < c1) {
+                load_codes<D>(c, x, koff, voff, next);
+                at_chunk(i + 2, x);
+            }
+            const int32_t t0 = t_first + i * KVA_CHUNK;
+            if (t0 < s.kv_len) {
+                const bool masked = !(cur.ok[0] && cur.ok[1] && t0 >= all_lo && t0 + 31 <= all_hi);
+                rows_step<D, NT>(c, r, cur, t0, s.kv_len, c2, masked);
+            }
+            cur = next;
+        }
+
+        // the four waves' rows together
+        const bool whole = c0 == 0 && c1 == w.chunks;
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (head_piece ? 0 : 1);
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            float l = r.l[n];
+            l += __shfl_xor(l, 16, 64);
+            l += __shfl_xor(l, 32, 64);
+            const float m = scaled_max(r.m[n], c2);
+            if (g == 0) {
+                lds.ml[wave][col][0] = m;
+                lds.ml[wave][col][1] = l;
+            }
+            __syncthreads();
+            const float top = fmaxf(fmaxf(lds.ml[0][col][0], lds.ml[1][col][0]), fmaxf(lds.ml[2][col][0], lds.ml[3][col][0]));
+            const float f = m == KVA_NEG ? 0.0f : exp2_fast(m - top);
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int j = 0; j < D / 16; j += 4)
+                    *reinterpret_cast<float4 *>(&lds.acc[wave][col][(D / 16) * (4 * g + i) + j]) =
+                        make_float4(r.o[n][j][i] * f, r.o[n][j + 1][i] * f, r.o[n][j + 2][i] * f, r.o[n][j + 3][i] * f);
+            __syncthreads();
+            const int row16 = tid >> 4, d0 = (tid & 15) * (D / 16);
+            const int32_t row = (tile * NT + n) * 16 + row16;
+            if (row < rows) {
+                float mw = KVA_NEG, lw = 0.0f, v[D / 16] = {};
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    mw = fmaxf(mw, lds.ml[i][row16][0]);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float mi = lds.ml[i][row16][0];
+                    lw += mi == KVA_NEG ? 0.0f : lds.ml[i][row16][1] * exp2_fast(mi - mw);
+#pragma unroll
+                    for (int j = 0; j < D / 16; j++)
+                        v[j] += lds.acc[i][row16][d0 + j];
+                }
+                if (whole) {
+                    const int32_t token = row / q.group, head = h * q.group + row - token * q.group;
+                    const float inv = lw == 0.0f ? 0.0f : 1.0f / lw;
+#pragma unroll
+                    for (int j = 0; j < D / 16; j++)
+                        v[j] *= inv;
+                    store_out(q, s.row + token, head, d0, v, D / 16);
+                    if (q.lse && (tid & 15) == 0)
+                        q.lse[(s.row + token) * q.heads + head] = mw == KVA_NEG ? KVA_NEG : (mw + __log2f(lw)) * LN2;
+                } else {
+                    const int64_t p = slot * (16 * NT) + n * 16 + row16;
+                    float *acc = (float *)(plan.ws + plan.off_acc) + p * D + d0;
+#pragma unroll
+                    for (int j = 0; j < D / 16; j += 4)
+                        *reinterpret_cast<float4 *>(acc + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    if ((tid & 15) == 0)
+                        ((float2 *)(plan.ws + plan.off_ml))[p] = make_float2(mw, lw);
+                }
+            }
+            __syncthreads();
+        }
+        at += c1 - c0;
+        head_piece = false;
+    }
+}
+
+// Partial sums of one row from `count` slots, slot i's row at index at(i) of ml and acc: groups of
+// D / 4 threads take slots in turn and meet in LDS.
+template <int D, typename F>
+__device__ __forceinline__ void join_row(const KvQueries &q, const KvPlan &plan, int32_t count, F at, int64_t token, int32_t head)
+{
+    constexpr int LANES = D / 4, GROUPS = KVA_THREADS / LANES;
+    __shared__ float lds_l[GROUPS], lds_m[GROUPS];
+    __shared__ float lds_acc[GROUPS][D];
+    const int tid = threadIdx.x, lane = tid % LANES, grp = tid / LANES;
+    const float2 *ml = (const float2 *)(plan.ws + plan.off_ml);
+    const float *acc = (const float *)(plan.ws + plan.off_acc);
+    float m = KVA_NEG, l = 0.0f;
+    float4 v = make_float4(0, 0, 0, 0);
+    for (int32_t i0 = grp; i0 < count; i0 += 4 * GROUPS) {
+        float2 x[4];
+        float4 a[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const int64_t p = at(min(i0 + k * GROUPS, count - 1));
+            x[k] = ml[p];
+            if (i0 + k * GROUPS >= count)
+                x[k] = make_float2(KVA_NEG, 0.0f);
+            a[k] = *reinterpret_cast<const float4 *>(acc + p * D + 4 * lane);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            if (x[k].x == KVA_NEG)
+                continue;  // (a piece that the row sees nothing of: its sums may not be written)
+            const float now = fmaxf(m, x[k].x);
+            const float f = m == KVA_NEG ? 0.0f : exp2_fast(m - now), e = exp2_fast(x[k].x - now);
+            l = l * f + x[k].y * e;
+            v.x = v.x * f + a[k].x * e;
+            v.y = v.y * f + a[k].y * e;
+            v.z = v.z * f + a[k].z * e;
+            v.w = v.w * f + a[k].w * e;
+            m = now;
+        }
+    }
+    if (lane == 0) {
+        lds_m[grp] = m;
+        lds_l[grp] = l;
+    }
+    *reinterpret_cast<float4 *>(&lds_acc[grp][4 * lane]) = v;
+    __syncthreads();
+    if (tid < LANES) {
+        float top = KVA_NEG, sum = 0.0f, o[4] = {};
+        for (int i = 0; i < GROUPS; i++)
+            top = fmaxf(top, lds_m[i]);
+        for (int i = 0; i < GROUPS; i++) {
+            if (lds_m[i] == KVA_NEG)
+                continue;
+            const float f = exp2_fast(lds_m[i] - top);
+            sum += lds_l[i] * f;
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                o[j] += lds_acc[i][4 * lane + j] * f;
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            o[j] *= inv;
+        store_out(q, token, head, 4 * lane, o, 4);
+        if (q.lse && lane == 0)
+            q.lse[token * q.heads + head] = top == KVA_NEG ? KVA_NEG : (top + __log2f(sum)) * LN2;
+    }
+}
+
+// One workgroup a row of an item that several pieces of the line hold parts of.
+template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS) void kv_join_kernel(KvView c, KvQueries q, KvPlan plan)
+{
+    const int32_t b = blockIdx.x / c.kv_heads, h = blockIdx.x - b * c.kv_heads;
+    const int32_t row = blockIdx.y;
+    const SeqRows s = seq_rows(c, b);
+    const SeqWork w = seq_work<NT>(c, q, s, plan.few);
+    if (!w.all || row >= s.n * q.group)
+        return;
+    const int64_t *first = (const int64_t *)(plan.ws + plan.off_first);
+    const int64_t piece = first[c.batch];
+    const int32_t tile = row / (16 * NT);
+    const int64_t from = first[b] + ((int64_t)h * w.tiles + tile) * w.chunks, to = from + w.chunks;
+    const int64_t g0 = from / piece, g1 = (to - 1) / piece;
+    if (g0 == g1)
+        return;  // one workgroup had it whole
+    const int32_t in = row - tile * 16 * NT;
+    const bool late = from > g0 * piece;  // its first piece started with another item
+    const int32_t token = row / q.group, head = h * q.group + row - token * q.group;
+    join_row<D>(q, plan, (int32_t)(g1 - g0 + 1),
+                [&](int32_t i) { return (2 * (g0 + i) + (i == 0 && late ? 1 : 0)) * (16 * NT) + in; }, s.row + token, head);
+}
+
+// ---------------------------------------------------------------------------
+// many rows
+
+// Swizzled 16-byte unit u of row d of the transposed values in LDS (8 units of 8 positions a row): the eight
+// rows that eight lanes read, and the eight that they write (4 or 2 rows apart), fall on eight banks' groups.
+template <int D> __device__ __forceinline__ int value_unit(int d, int u)
+{
+    const int f = D == 128 ? (d & 4) | ((d >> 3 ^ d) & 2) | ((d >> 3 ^ d) & 1) : (d & 6) | ((d >> 3 ^ d) & 1);
+    return d * 8 + (u ^ f);
+}
+
+template <int D> struct Step {
+    uint4 k[KVA_STEP * D / 8];  // [position][unit of 8 elements ^ position & 7]
+    uint4 v[KVA_STEP * D / 8];  // [element][unit of 8 positions, swizzled]
+};
+
+template <int D> __global__ __launch_bounds__(KVA_THREADS) void kv_tiles_kernel(KvView c, KvQueries q, KvPlan plan)
+{
+    constexpr int DT = D / 32;   // tiles of 32 elements
+    constexpr int KW = D / 64;   // 16-byte loads of keys a thread and step
+    constexpr int VB = D / 32;   // bytes of a value row a thread takes
+    __shared__ Step<D> lds[2];
+    __shared__ int lds_odd[2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int col = lane & 31, half = lane >> 5;
+    const int32_t h = blockIdx.x % c.kv_heads;
+    const int32_t u = blockIdx.x / c.kv_heads;
+    const int b = uniform(find_seq<KVA_THREADS>(c.batch, u, [&](int j) { return seq_start(c, j) * q.group / KVA_TILE + j; }));
+    const SeqRows s = uniform(seq_rows(c, b));
+    const int64_t rows64 = s.n * q.group;
+    const int64_t tiles = (rows64 + KVA_TILE - 1) / KVA_TILE;
+    const int64_t in_seq = u - (s.row * q.group / KVA_TILE + b);
+    if (rows64 <= plan.few || in_seq < 0 || in_seq >= tiles)
+        return;
+    const int32_t rows = (int32_t)rows64;
+    const int32_t tile = (int32_t)(tiles - 1 - in_seq);  // the longest first
+    const float c2 = q.scale * LOG2E;
+
+    // this lane's row
+    const int32_t row = tile * KVA_TILE + wave * 32 + col;
+    const int32_t token = min(row, rows - 1) / q.group;
+    const int32_t head = h * q.group + min(row, rows - 1) - token * q.group;
+    const Seen see = seen_by(q, s, token);
+    // what every row of the wave sees
+    const int32_t w0 = min(tile * KVA_TILE + wave * 32, rows - 1) / q.group, w1 = min(tile * KVA_TILE + wave * 32 + 31, rows - 1) / q.group;
+    const int32_t all_lo = uniform(seen_by(q, s, w1).lo), all_hi = uniform(seen_by(q, s, w0).hi);
+    // and what any row of the wave, and of the workgroup, does
+    const int32_t any_lo = uniform(seen_by(q, s, w0).lo), any_hi = uniform(seen_by(q, s, w1).hi);
+    const int32_t last = min((tile + 1) * KVA_TILE, rows) - 1;
+    const int32_t lo = seen_by(q, s, tile * KVA_TILE / q.group).lo & ~(KVA_STEP - 1);
+    const int32_t hi = seen_by(q, s, last / q.group).hi;
+    const int32_t steps = hi >= lo ? (hi - lo) / KVA_STEP + 1 : 0;
+    const int32_t each = (steps + plan.splits - 1) / plan.splits;
+    const int32_t i0 = min((int32_t)blockIdx.y * each, steps), i1 = min(i0 + each, steps);
+
+    uint4 qf[D / 16];
+    {
+        const uint16_t *p = q.q + (s.row + token) * q.ld_qt + head * q.ld_qh + 8 * half;
+#pragma unroll
+        for (int i = 0; i < D / 16; i++)
+            qf[i] = *reinterpret_cast<const uint4 *>(p + 16 * i);
+    }
+    f32x16_t o[DT];
+#pragma unroll
+    for (int j = 0; j < DT; j++)
+#pragma unroll
+        for (int i = 0; i < 16; i++)
+            o[j][i] = 0.0f;
+    float m = KVA_NEG, l = 0.0f;
+
+    // A step's codes: wave w takes block w of its four, 16 rows of keys by 4 lanes, and values as (half block, VB
+    // elements): positions 4 hv + 0..3 and 8 + 4 hv + 0..3, the order in which a row's weights come out.
+    uint4 kc[KW];
+    uint32_t vc[8];
+    uint32_t ks, vs;
+    const int kr = lane >> 2, kq = lane & 3, hv = lane >> 5, vd = (lane & 31) * VB;
+    auto load = [&](int32_t i) {
+        const int32_t t0 = lo + i * KVA_STEP;
+        const BlockAt x = block_at(c, b, h, (t0 >> 4) + wave);
+        const uint8_t *kb = c.k + x.codes + (int64_t)kr * c.ld_token + 16 * KW * kq;
+        const uint8_t *vb = c.v + x.codes + (int64_t)(4 * hv) * c.ld_token + vd;
+#pragma unroll
+        for (int j = 0; j < KW; j++)
+            kc[j] = reinterpret_cast<const uint4 *>(kb)[j];
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const uint8_t *p = vb + (int64_t)((e & 3) + 8 * (e >> 2)) * c.ld_token;
+            vc[e] = VB == 4 ? *reinterpret_cast<const uint32_t *>(p) : *reinterpret_cast<const uint16_t *>(p);
+        }
+        ks = c.k_scale[x.scale];
+        vs = x.ok ? c.v_scale[x.scale] : 0x1FFu;  // (0x1FF: no page)
+    };
+    auto stage = [&](int32_t i, int buf) {
+        const int32_t t0 = lo + i * KVA_STEP + wave * 16;
+        const float kf = cvt_scale(ks);
+#pragma unroll
+        for (int j = 0; j < KW; j++) {
+            const uint32_t w[4] = {kc[j].x, kc[j].y, kc[j].z, kc[j].w};
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                uint4 x = make_uint4(e4m3_bf16<false>(w[2 * e], kf), e4m3_bf16<true>(w[2 * e], kf),
+                                     e4m3_bf16<false>(w[2 * e + 1], kf), e4m3_bf16<true>(w[2 * e + 1], kf));
+                if (ks == 0xFFu)
+                    x = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+                const int t = wave * 16 + kr;
+                lds[buf].k[t * (D / 8) + ((2 * KW * kq + 2 * j + e) ^ (t & 7))] = x;
+            }
+        }
+        bool odd = false;
+        uint32_t sc = vs;
+        if (sc == 0x1FFu || t0 + 16 > s.kv_len) {
+            // behind the last position, or no page: zeros
+            if (sc == 0x1FFu || t0 >= s.kv_len)
+                sc = 127;
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                vc[e] = vs != 0x1FFu && t0 + 4 * hv + (e & 3) + 8 * (e >> 2) < s.kv_len ? vc[e] : 0u;
+        }
+        if (sc == 0xFFu)
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                vc[e] = 0x7F7F7F7Fu;
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            odd = odd || nan_codes(vc[e]);
+        if (__any(odd || sc >= KVA_BIG_SCALE) && lane == 0)
+            lds_odd[buf] = i + 1;
+        const float vf = cvt_scale(sc);
+        uint32_t x[VB][4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const uint32_t a = __builtin_amdgcn_perm(vc[2 * e + 1], vc[2 * e], 0x05010400u);
+            x[0][e] = e4m3_bf16<false>(a, vf);
+            x[1][e] = e4m3_bf16<true>(a, vf);
+            if constexpr (VB == 4) {
+                const uint32_t z = __builtin_amdgcn_perm(vc[2 * e + 1], vc[2 * e], 0x07030602u);
+                x[2][e] = e4m3_bf16<false>(z, vf);
+                x[3][e] = e4m3_bf16<true>(z, vf);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < VB; j++)
+            lds[buf].v[value_unit<D>(vd + j, 2 * wave + hv)] = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
+    };
+
+    if (tid < 2)
+        lds_odd[tid] = 0;
+    __syncthreads();
+    if (i0 < i1) {
+        load(i0);
+        stage(i0, 0);
+    }
+    __syncthreads();
+    for (int32_t i = i0; i < i1; i++) {
+        const int buf = (i - i0) & 1;
+        if (i + 1 < i1)
+            load(i + 1);
+        const int32_t t0 = lo + i * KVA_STEP;
+        if (t0 + KVA_STEP > any_lo && t0 <= any_hi) {  // (else nothing for this wave)
+            f32x16_t sc[2];
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+#pragma unroll
+                for (int k = 0; k < 16; k++)
+                    sc[j][k] = 0.0f;
+                const int t = 32 * j + col;
+#pragma unroll
+                for (int k = 0; k < D / 16; k++) {
+                    const uint4 a = lds[buf].k[t * (D / 8) + ((2 * k + half) ^ (t & 7))];
+                    sc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, qf[k]),
+                                                                    sc[j], 0, 0, 0);
+                }
+            }
+            // a page that is not there hides its positions from every row: their flags, one bit a block
+            uint32_t gone = 0;
+            {
+                const ConstI32 table = (ConstI32)(uintptr_t)c.table;
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const int32_t pg = min(((t0 >> 4) + k) >> (c.page_shift - 4), c.max_pages - 1);
+                    gone |= (uint32_t)table[(int64_t)b * c.max_pages + pg] < (uint32_t)c.num_pages ? 0u : 1u << k;
+                }
+            }
+            const bool masked = gone || t0 < all_lo || t0 + KVA_STEP - 1 > all_hi;
+            if (masked) {
+#pragma unroll
+                for (int j = 0; j < 2; j++)
+#pragma unroll
+                    for (int k = 0; k < 16; k++) {
+                        const int32_t t = 32 * j + 8 * (k >> 2) + 4 * half + (k & 3);
+                        const bool y = t0 + t >= see.lo && t0 + t <= see.hi && !(gone >> (2 * j + (k >> 3)) & 1);
+                        sc[j][k] = y ? sc[j][k] : KVA_NEG;
+                    }
+            }
+            float mt = KVA_NEG;
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int k = 0; k < 16; k++)
+                    mt = fmaxf(mt, sc[j][k]);
+            mt = max_xor32(mt);
+            if (__any(mt > m && !((mt - m) * c2 <= KVA_SLACK))) {
+                const float now = fmaxf(m, mt);
+                const float f = m == KVA_NEG ? 0.0f : exp2_fast((m - now) * c2);
+                m = now;
+                l *= f;
+#pragma unroll
+                for (int j = 0; j < DT; j++)
+                    o[j] *= f;
+            }
+            const float mc = m == KVA_NEG ? 0.0f : m * c2;
+            Frag p[4];
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                    float e0 = exp2_fast(fmaf(sc[j][k], c2, -mc)), e1 = exp2_fast(fmaf(sc[j][k + 1], c2, -mc));
+                    if (masked) {
+                        e0 = sc[j][k] == KVA_NEG ? 0.0f : e0;
+                        e1 = sc[j][k + 1] == KVA_NEG ? 0.0f : e1;
+                    }
+                    l += e0 + e1;
+                    p[2 * j + (k >> 3)].w[(k & 7) >> 1] = pack_bf16(e0, e1);
+                }
+            if (!(masked && lds_odd[buf] == i + 1)) {
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+#pragma unroll
+                    for (int j = 0; j < DT; j++) {
+                        const uint4 a = lds[buf].v[value_unit<D>(32 * j + col, 2 * k + half)];
+                        o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), p[k].f, o[j], 0, 0, 0);
+                    }
+            } else {
+                // (as in rows_step: position by position, into the rows that see it)
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+#pragma unroll 1
+                    for (int at = 0; at < 16; at++) {
+                        const int e = (at >> 2 & 1) == half ? 4 * (at >> 3) + (at & 3) : -1;
+                        const int32_t t = t0 + 16 * k + at;
+                        const bool y = t >= see.lo && t <= see.hi && !(gone >> k & 1);
+                        Frag one;
+#pragma unroll
+                        for (int w = 0; w < 4; w++)
+                            one.w[w] = e == 2 * w ? p[k].w[w] & 0xFFFFu : e == 2 * w + 1 ? p[k].w[w] & 0xFFFF0000u : 0u;
+#pragma unroll
+                        for (int j = 0; j < DT; j++) {
+                            const uint4 x = lds[buf].v[value_unit<D>(32 * j + col, 2 * k + half)];
+                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                            Frag a;
+#pragma unroll
+                            for (int z = 0; z < 4; z++)
+                                a.w[z] = e == 2 * z ? w[z] & 0xFFFFu : e == 2 * z + 1 ? w[z] & 0xFFFF0000u : 0u;
+                            f32x16_t r;
+#pragma unroll
+                            for (int z = 0; z < 16; z++)
+                                r[z] = 0.0f;
+                            r = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.f, one.f, r, 0, 0, 0);
+#pragma unroll
+                            for (int z = 0; z < 16; z++)
+                                o[j][z] += y ? r[z] : 0.0f;
+                        }
+                    }
+            }
+        }
+        if (i + 1 < i1)
+            stage(i + 1, buf ^ 1);
+        __syncthreads();
+    }
+
+    l += __shfl_xor(l, 32, 64);
+    if (row >= rows)
+        return;
+    const float top = scaled_max(m, c2);
+    if (plan.splits == 1) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int j = 0; j < DT; j++)
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+                const float v[4] = {o[j][k] * inv, o[j][k + 1] * inv, o[j][k + 2] * inv, o[j][k + 3] * inv};
+                store_out(q, s.row + token, head, 32 * j + 2 * k + 4 * half, v, 4);
+            }
+        if (q.lse && half == 0)
+            q.lse[(s.row + token) * q.heads + head] = top == KVA_NEG ? KVA_NEG : (top + __log2f(l)) * LN2;
+        return;
+    }
+    const int64_t at = (((int64_t)u * c.kv_heads + h) * plan.splits + blockIdx.y) * KVA_TILE + wave * 32 + col;
+    if (half == 0)
+        ((float2 *)(plan.ws + plan.off_ml))[at] = make_float2(top, l);
+    if (i0 == i1)
+        return;  // (its sums are not read)
+    float *acc = (float *)(plan.ws + plan.off_acc) + at * D;
+#pragma unroll
+    for (int j = 0; j < DT; j++)
+#pragma unroll
+        for (int k = 0; k < 16; k += 4)
+            *reinterpret_cast<float4 *>(acc + 32 * j + 2 * k + 4 * half) = make_float4(o[j][k], o[j][k + 1], o[j][k + 2], o[j][k + 3]);
+}
+
+// The ranges of a tile's rows together: blockIdx as kv_tiles_kernel's, y the row.
+template <int D> __global__ __launch_bounds__(KVA_THREADS) void kv_tiles_join_kernel(KvView c, KvQueries q, KvPlan plan)
+{
+    const int32_t h = blockIdx.x % c.kv_heads;
+    const int32_t u = blockIdx.x / c.kv_heads;
+    const int b = find_seq<KVA_THREADS>(c.batch, u, [&](int j) { return seq_start(c, j) * q.group / KVA_TILE + j; });
+    const SeqRows s = seq_rows(c, b);
+    const int64_t rows = s.n * q.group, tiles = (rows + KVA_TILE - 1) / KVA_TILE;
+    const int64_t in_seq = u - (s.row * q.group / KVA_TILE + b);
+    const int64_t row = (tiles - 1 - in_seq) * KVA_TILE + blockIdx.y;
+    if (rows <= plan.few || in_seq < 0 || in_seq >= tiles || row >= rows)
+        return;
+    const int32_t token = (int32_t)row / q.group, head = h * q.group + (int32_t)row - token * q.group;
+    const int64_t at = ((int64_t)u * c.kv_heads + h) * plan.splits * KVA_TILE + blockIdx.y;
+    join_row<D>(q, plan, plan.splits, [&](int32_t i) { return at + (int64_t)i * KVA_TILE; }, s.row + token, head);
+}
+
+// ---------------------------------------------------------------------------
+// the plan: a function of the sizes and of the compute units
+
+static int compute_units()
+{
+    int dev = 0, n = 0;
+    if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 1)
+        return 256;
+    return n;
+}
+
+struct KvSpace {
+    KvPlan plan;
+    int nt;           // tiles of 16 rows the few-row kernel takes at once
+    int32_t rows_max; // rows of a sequence and head it can meet
+    bool rows, tiles; // which kernels are launched
+    int64_t bytes;
+};
+
+static KvSpace space_of(int64_t tokens, int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t max_new)
+{
+    KvSpace s{};
+    const int64_t group = q_heads / kv_heads;
+    const int64_t most = (max_new ? std::min(max_new, tokens) : tokens) * group;  // rows of a sequence and head
+    const int64_t cus = compute_units();
+    s.rows = true;
+    s.tiles = most > KVA_FEW;
+    s.plan.few = s.tiles ? 32 : KVA_FEW;
+    s.nt = most <= 16 ? 1 : 2;
+    s.rows_max = (int32_t)std::min<int64_t>(most, s.plan.few);
+    s.plan.groups = (int32_t)(cus * (s.nt == 1 ? 4 : 2));
+    s.plan.splits = 1;
+    s.plan.tiles = s.tiles ? (int32_t)(tokens * group / KVA_TILE + batch) : 0;
+    if (s.tiles) {
+        const int64_t wgs = (int64_t)s.plan.tiles * kv_heads;
+        s.plan.splits = (int32_t)std::min<int64_t>(16, std::max<int64_t>(1, 2 * cus / wgs));
+    }
+    // the starts on the line, then (max, sum) and sums of the partial rows; the two kernels run one after
+    // the other, each followed by its join, so they share the space
+    int64_t slots = 2 * (int64_t)s.plan.groups * 16 * s.nt;
+    if (s.plan.splits > 1)
+        slots = std::max(slots, (int64_t)s.plan.tiles * kv_heads * s.plan.splits * KVA_TILE);
+    s.plan.off_first = 0;
+    s.plan.off_ml = ((batch + 1) * 8 + 15) / 16 * 16;
+    s.plan.off_acc = s.plan.off_ml + slots * 8;
+    s.bytes = s.plan.off_acc + slots * dim * 4;
+    return s;
+}
+
+int64_t kv_attention_workspace_bytes(int64_t tokens, int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t max_new)
+{
+    return space_of(tokens, batch, q_heads, kv_heads, dim, max_new).bytes;
+}
+
+template <int D> static hipError_t launch(const KvView &c, const KvQueries &q, KvSpace s, hipStream_t stream)
+{
+    const dim3 block(KVA_THREADS);
+    if (s.tiles) {
+        const dim3 grid((unsigned)((int64_t)s.plan.tiles * c.kv_heads), s.plan.splits);
+        hipLaunchKernelGGL(kv_tiles_kernel<D>, grid, block, 0, stream, c, q, s.plan);
+        if (s.plan.splits > 1)
+            hipLaunchKernelGGL(kv_tiles_join_kernel<D>, dim3(grid.x, KVA_TILE), block, 0, stream, c, q, s.plan);
+    }
+    // no more pieces than there can be chunks
+    const int64_t chunks = ((int64_t)c.max_pages << c.page_shift) / KVA_CHUNK + 2;
+    const int64_t line = chunks * c.batch * c.kv_heads * ((s.rows_max + 16 * s.nt - 1) / (16 * s.nt));
+    s.plan.groups = (int32_t)std::min<int64_t>(s.plan.groups, line);
+    const dim3 join((unsigned)(c.batch * c.kv_heads), (unsigned)s.rows_max);
+    if (s.nt == 1) {
+        hipLaunchKernelGGL((kv_rows_kernel<D, 1>), dim3(s.plan.groups), block, 0, stream, c, q, s.plan);
+        hipLaunchKernelGGL((kv_join_kernel<D, 1>), join, block, 0, stream, c, q, s.plan);
+    } else {
+        hipLaunchKernelGGL((kv_rows_kernel<D, 2>), dim3(s.plan.groups), block, 0, stream, c, q, s.plan);
+        hipLaunchKernelGGL((kv_join_kernel<D, 2>), join, block, 0, stream, c, q, s.plan);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_attention(const KvView &c, const KvQueries &q, void *ws, hipStream_t stream)
+{
+    KvSpace s = space_of(c.tokens, c.batch, q.heads, c.kv_heads, c.dim, q.max_new);
+    s.plan.ws = (char *)ws;
+    return c.dim == 64 ? launch<64>(c, q, s, stream) : launch<128>(c, q, s, stream);
+}
+
+}  // namespace mx

@@ -207,6 +207,59 @@ hipError_t launch_grouped_gemm_fp4(int64_t G, int64_t M_total, int64_t N, int64_
                                    const void *a_q, int64_t ld_a, const void *a_s, const void *b_q, const void *b_s,
                                    void *c, int64_t ld_c, int c_dtype, hipStream_t stream);
 
+// Rotary positions (mx_rope.hip): strides in elements, dtype 0 = BF16, 1 = FP32;
+// sign -1 for the gradient.
+struct RopeArgs {
+    const void *x;
+    void *y;
+    int64_t ld_xt, ld_xh, ld_yt, ld_yh;
+    const int32_t *positions;
+    const double *freqs;
+    int64_t tokens;
+    int32_t heads, dim, rot;
+    float amplitude, sign;
+};
+hipError_t launch_rope(const RopeArgs &a, int dtype, bool interleaved, hipStream_t stream);
+
+// The paged 8-bit cache and a call's sequences, as the kernels take them.
+struct KvView {
+    uint8_t *k, *v, *k_scale, *v_scale;
+    int64_t ld_page, ld_head, ld_token;
+    int32_t num_pages, kv_heads, page_shift, dim, max_pages, batch;
+    const int32_t *table, *lens;
+    const int64_t *starts;
+    int64_t tokens;
+};
+
+// New rows of keys and values (mx_kv.hip); freqs null: keys as they are.
+struct KvNew {
+    const uint16_t *k, *v;
+    int64_t ld_kt, ld_kh, ld_vt, ld_vh;
+    const double *freqs;
+    int32_t rot;
+    float amplitude;
+    bool interleaved;
+};
+hipError_t launch_kv_append(const KvView &c, const KvNew &n, hipStream_t stream);
+hipError_t launch_kv_read(const KvView &c, void *k, void *v, int dtype, hipStream_t stream);
+
+// Attention over the cache (mx_kv_attention.hip).
+struct KvQueries {
+    const uint16_t *q;
+    int64_t ld_qt, ld_qh;
+    uint16_t *out;
+    int64_t ld_ot, ld_oh;
+    float *lse;
+    int32_t heads, group;  // query heads, and those of a key/value head
+    float scale;
+    int32_t window;        // 0: none (a window no position reaches is none too)
+    bool causal;
+    int64_t max_new;       // 0: not known
+};
+int64_t kv_attention_workspace_bytes(int64_t tokens, int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim,
+                                     int64_t max_new);
+hipError_t launch_kv_attention(const KvView &c, const KvQueries &q, void *ws, hipStream_t stream);
+
 // Debug check of device offsets off[0..G] (see mx_debug.hip): waits for the
 // stream (the one wait in the library, under MX_DEBUG only), then *first_bad = the first entry breaking the stated properties
 // (in [0, total], multiple of align, ranges at least min_len long,

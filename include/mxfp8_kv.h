@@ -125,7 +125,7 @@ typedef struct mx_kv_cache {
  * (0 where amax is 0), amax the largest finite magnitude of the block's new values;
  * c_old = 0 where the call writes the block's first position, the stored code
  * otherwise.  New values are rounded to the nearest E4M3 (ties to even) of that
- * scale, NaN and infinities become the NaN code; where c > c_old the older positions' codes
+ * scale, NaN and infinities become the code 0x7F; where c > c_old the older positions' codes
  * of the block are rounded anew.  Other than the MX rule's floor(log2 amax) - 8, c_new
  * clamps nothing, so a block that grows never holds a clamped value.
  *   k, v   BF16 [tokens][kv_heads][head_dim], strides ld_kt, ld_kh / ld_vt, ld_vh

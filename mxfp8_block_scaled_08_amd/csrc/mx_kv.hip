@@ -64,7 +64,13 @@ __device__ __forceinline__ uint32_t kv_scale_code(uint32_t bits)
     return c < 0 ? 0u : (uint32_t)c;
 }
 
-// Eight FP32 -> eight E4M3 codes at the scale; none exceeds 448 times it, NaN gives NaN.
+// The NaN codes of a word as 0x7F (the conversion leaves either sign).
+__device__ __forceinline__ uint32_t one_nan(uint32_t u)
+{
+    return u ^ (((u & 0x7F7F7F7Fu) + 0x01010101u) & u & 0x80808080u);
+}
+
+// Eight FP32 -> eight E4M3 codes at the scale; none exceeds 448 times it, NaN gives 0x7F.
 __device__ __forceinline__ uint2 e4m3_x8(const float *v, float scale)
 {
     i16x2_t a = {0, 0}, b = {0, 0};
@@ -72,7 +78,7 @@ __device__ __forceinline__ uint2 e4m3_x8(const float *v, float scale)
     a = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(a, v[2], v[3], scale, true);
     b = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(b, v[4], v[5], scale, false);
     b = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(b, v[6], v[7], scale, true);
-    return make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+    return make_uint2(one_nan(__builtin_bit_cast(uint32_t, a)), one_nan(__builtin_bit_cast(uint32_t, b)));
 }
 
 __device__ __forceinline__ void f32_x8(uint2 q, float scale, float *v)

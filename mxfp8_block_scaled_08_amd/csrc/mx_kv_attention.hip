@@ -96,22 +96,32 @@ __device__ __forceinline__ SeqRows uniform(SeqRows s)
     return s;
 }
 
+// The larger of a lane's value and of the lane's 32 (16) away.  (The swap's two results are copied before they
+// are cast: a bit cast of the second element itself reads the first.)
 __device__ __forceinline__ float max_xor32(float v)
 {
-    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
-    return fmaxf(__builtin_bit_cast(float, r[0]), __builtin_bit_cast(float, r[1]));
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t a = r[0], b = r[1];
+    return fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
 }
 
 __device__ __forceinline__ float max_xor16(float v)
 {
-    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
-    return fmaxf(__builtin_bit_cast(float, r[0]), __builtin_bit_cast(float, r[1]));
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const uint32_t a = r[0], b = r[1];
+    return fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// m * c with -inf kept (0 * -inf is NaN where the scale is 0).
-__device__ __forceinline__ float scaled_max(float m, float c) { return m == KVA_NEG ? KVA_NEG : m * c; }
+// A finished range's maximum, m times the scale, as its join takes it: -inf where the row sees nothing of it (kept, as 0
+// * -inf is NaN), +inf where it sees a NaN, which the maximum passes over but which has to reach the result.
+__device__ __forceinline__ float scaled_max(float m, float c, float l)
+{
+    return l != l ? -KVA_NEG : m == KVA_NEG ? KVA_NEG : m * c;
+}
 
 // Whether a word holds a NaN code.
 __device__ __forceinline__ bool nan_codes(uint32_t w)
@@ -550,7 +560,7 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS) void kv_rows_
             float l = r.l[n];
             l += __shfl_xor(l, 16, 64);
             l += __shfl_xor(l, 32, 64);
-            const float m = scaled_max(r.m[n], c2);
+            const float m = scaled_max(r.m[n], c2, l);
             if (g == 0) {
                 lds.ml[wave][col][0] = m;
                 lds.ml[wave][col][1] = l;
@@ -969,7 +979,7 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS) void kv_tiles_kernel(
     l += __shfl_xor(l, 32, 64);
     if (row >= rows)
         return;
-    const float top = scaled_max(m, c2);
+    const float top = scaled_max(m, c2, l);
     if (plan.splits == 1) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll

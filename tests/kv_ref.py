@@ -88,7 +88,7 @@ class Cache:
                             cells = self.kv[w, pg, h, s * BLOCK:s * BLOCK + off]
                             was = E4M3[cells] * 2.0 ** (old - 127.0)
                             q, bad = encode(was, c)
-                            cells[:] = np.where(bad, cells, q)
+                            cells[:] = np.where(bad, 0x7F, q)
                         elif off > 0:
                             c = old
                         q, bad = encode(x[w, :, h], c)

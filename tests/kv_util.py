@@ -98,4 +98,5 @@ def check_attention(got, got_lse, ref_result, dim, keys):
         same = (np.isnan(g) == np.isnan(lse)) & (np.isneginf(g) == np.isneginf(lse))
         assert same.all(), np.argwhere(~same)[:4]
         fin = np.isfinite(lse)
-        assert (np.abs(g - lse)[fin] <= lb[fin]).all(), (np.abs(g - lse)[fin] / lb[fin]).max()
+        err = np.abs(g[fin] - lse[fin])
+        assert (err <= lb[fin]).all(), (err / lb[fin]).max()

@@ -196,10 +196,10 @@ union Frag {
     bf16x8_t f;
 };
 
-// O^T += V^T P^T for every tile of 16 rows; V's words as in Codes.
-template <int D, int NT>
-__device__ __forceinline__ void values_product(const uint32_t (&v)[8][D / 64], const uint32_t (&vs)[2], const Frag (&p)[NT],
-                                               f32x4_t (&o)[NT][D / 16])
+// V^T, 16 elements by the wave's 32 positions at a time: into(j, fragment) for the D / 16 tiles of elements
+// (D / 16) m + j; V's words as in Codes.
+template <int D, typename F>
+__device__ __forceinline__ void value_tiles(const uint32_t (&v)[8][D / 64], const uint32_t (&vs)[2], F into)
 {
     const float s0 = cvt_scale(vs[0]), s1 = cvt_scale(vs[1]);
 #pragma unroll
@@ -218,9 +218,7 @@ __device__ __forceinline__ void values_product(const uint32_t (&v)[8][D / 64], c
         }
 #pragma unroll
         for (int j = 0; j < 4; j++)
-#pragma unroll
-            for (int n = 0; n < NT; n++)
-                o[n][4 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j].f, p[n].f, o[n][4 * w + j], 0, 0, 0);
+            into(4 * w + j, a[j]);
     }
 }
 
@@ -231,13 +229,10 @@ template <int D, int NT> struct RowState {
     Seen see[NT];
 };
 
-// One wave's 32 positions from t0 on.  masked: some row does not see some of them.
+// S^T = K Q^T of a wave's 32 positions: s[j][n][i] is row (lane & 15)'s score of position 16 j + 4 (lane >> 4) + i.
 template <int D, int NT>
-__device__ __forceinline__ void rows_step(const KvView &c, RowState<D, NT> &r, Codes<D> &t, int32_t t0, int32_t kv_len,
-                                          float c2, bool masked)
+__device__ __forceinline__ void scores(const RowState<D, NT> &r, const Codes<D> &t, f32x4_t (&s)[2][NT])
 {
-    const int g = (threadIdx.x & 63) >> 4;
-    f32x4_t s[2][NT];
 #pragma unroll
     for (int j = 0; j < 2; j++) {
         const float ks = cvt_scale(t.ks[j]);
@@ -261,28 +256,13 @@ __device__ __forceinline__ void rows_step(const KvView &c, RowState<D, NT> &r, C
             }
         }
     }
-    // (a scale code of 0xFF is NaN, whatever the code)
-#pragma unroll
-    for (int j = 0; j < 2; j++)
-        if (t.ks[j] == 0xFFu)
-#pragma unroll
-            for (int n = 0; n < NT; n++)
-                s[j][n] = __builtin_nanf("") + s[j][n];
-    uint32_t vis[NT] = {};  // bit 4 j + i: the row sees position t0 + 16 j + 4 g + i
-    if (masked) {
-#pragma unroll
-        for (int n = 0; n < NT; n++)
-#pragma unroll
-            for (int j = 0; j < 2; j++)
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int32_t p = t0 + 16 * j + 4 * g + i;
-                    const bool y = t.ok[j] && p >= r.see[n].lo && p <= r.see[n].hi;
-                    vis[n] |= y ? 1u << (4 * j + i) : 0u;
-                    s[j][n][i] = y ? s[j][n][i] : KVA_NEG;
-                }
-    }
-    Frag p[NT];
+}
+
+// The weights of the positions that vis has bits for (4 j + i; all if !MASKED), the running maxima and sums.
+template <int D, int NT, bool MASKED>
+__device__ __forceinline__ void weights(RowState<D, NT> &r, const f32x4_t (&s)[2][NT], const uint32_t (&vis)[NT], float c2,
+                                        Frag (&p)[NT])
+{
 #pragma unroll
     for (int n = 0; n < NT; n++) {
         float mt = fmaxf(fmaxf(fmaxf(s[0][n][0], s[0][n][1]), fmaxf(s[0][n][2], s[0][n][3])),
@@ -300,79 +280,113 @@ __device__ __forceinline__ void rows_step(const KvView &c, RowState<D, NT> &r, C
         const float mc = r.m[n] == KVA_NEG ? 0.0f : r.m[n] * c2;
         float e[8];
 #pragma unroll
-        for (int i = 0; i < 8; i++)
+        for (int i = 0; i < 8; i++) {
             e[i] = exp2_fast(fmaf(s[i >> 2][n][i & 3], c2, -mc));
-        if (masked)
-#pragma unroll
-            for (int i = 0; i < 8; i++)
+            if (MASKED)
                 e[i] = (vis[n] >> i & 1) ? e[i] : 0.0f;
+        }
         r.l[n] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
 #pragma unroll
         for (int i = 0; i < 4; i++)
             p[n].w[i] = pack_bf16(e[2 * i], e[2 * i + 1]);
     }
-    bool odd = false;
-    if (masked) {
-        // what no row sees behind the last position may hold anything
+}
+
+template <int D, int NT>
+__device__ __forceinline__ void add_values(RowState<D, NT> &r, const Codes<D> &t, const Frag (&p)[NT])
+{
+    value_tiles<D>(t.v, t.vs, [&](int j, const Frag &a) {
 #pragma unroll
-        for (int j = 0; j < 2; j++) {
-            if (!t.ok[j] || t0 + 16 * j >= kv_len)
-                t.vs[j] = 127;
+        for (int n = 0; n < NT; n++)
+            r.o[n][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.f, p[n].f, r.o[n][j], 0, 0, 0);
+    });
+}
+
+// Whether a wave's 32 positions need masked_step: a page is not there, or a scale is NaN.
+template <int D> __device__ __forceinline__ bool irregular(const Codes<D> &t)
+{
+    return !t.ok[0] || !t.ok[1] || __any(max(max(t.ks[0], t.ks[1]), max(t.vs[0], t.vs[1])) == 0xFFu);
+}
+
+// 32 positions that every row sees.
+template <int D, int NT> __device__ __forceinline__ void plain_step(RowState<D, NT> &r, const Codes<D> &t, float c2)
+{
+    f32x4_t s[2][NT];
+    Frag p[NT];
+    scores<D, NT>(r, t, s);
+    const uint32_t vis[NT] = {};
+    weights<D, NT, false>(r, s, vis, c2, p);
+    add_values<D, NT>(r, t, p);
+}
+
+// 32 positions from t0 on, of which a row sees what it sees.
+template <int D, int NT>
+__device__ __forceinline__ void masked_step(RowState<D, NT> &r, Codes<D> &t, int32_t t0, int32_t kv_len, float c2)
+{
+    const int g = (threadIdx.x & 63) >> 4;
+    f32x4_t s[2][NT];
+    Frag p[NT];
+    scores<D, NT>(r, t, s);
+    uint32_t vis[NT] = {};  // bit 4 j + i: the row sees position t0 + 16 j + 4 g + i
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const bool in = t.ok[j] && t0 + 16 * j + 4 * g + e < kv_len;
+    for (int n = 0; n < NT; n++)
 #pragma unroll
-                for (int w = 0; w < D / 64; w++) {
-                    t.v[4 * j + e][w] = in ? t.v[4 * j + e][w] : 0u;
-                    odd = odd || nan_codes(t.v[4 * j + e][w]);
-                }
+        for (int j = 0; j < 2; j++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int32_t at = t0 + 16 * j + 4 * g + i;
+                const bool y = t.ok[j] && at >= r.see[n].lo && at <= r.see[n].hi;
+                vis[n] |= y ? 1u << (4 * j + i) : 0u;
+                s[j][n][i] = !y ? KVA_NEG : t.ks[j] == 0xFFu ? __builtin_nanf("") : s[j][n][i];
             }
-            odd = odd || t.vs[j] >= KVA_BIG_SCALE;
+    weights<D, NT, true>(r, s, vis, c2, p);
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+        // what no row sees, behind the last position or without a page, may hold anything
+        if (!t.ok[j] || t0 + 16 * j >= kv_len)
+            t.vs[j] = 127;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const bool in = t.ok[j] && t0 + 16 * j + 4 * g + e < kv_len;
+#pragma unroll
+            for (int w = 0; w < D / 64; w++) {
+                t.v[4 * j + e][w] = !in ? 0u : t.vs[j] == 0xFFu ? 0x7F7F7F7Fu : t.v[4 * j + e][w];
+                odd = odd || nan_codes(t.v[4 * j + e][w]);
+            }
         }
-        odd = __any(odd);
+        odd = odd || t.vs[j] >= KVA_BIG_SCALE;
     }
-#pragma unroll
-    for (int j = 0; j < 2; j++)
-        if (t.vs[j] == 0xFFu)
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-#pragma unroll
-                for (int w = 0; w < D / 64; w++)
-                    t.v[4 * j + e][w] = 0x7F7F7F7Fu;
-    if (!odd) {
-        values_product<D, NT>(t.v, t.vs, p, r.o);
+    if (!__any(odd)) {
+        add_values<D, NT>(r, t, p);
         return;
     }
-    // NaN or infinite values that some row does not see: a weight of 0 does not keep them out of a
+    // NaN or infinite values that some row may not see: a weight of 0 does not keep them out of a
     // sum, so each position goes by itself, into the rows that see it
 #pragma unroll 1
     for (int at = 0; at < 32; at++) {
         const int mine = (at & 15) >> 2 == g ? 4 * (at >> 4) + (at & 3) : -1;
+        const bool there = at < 16 ? t.ok[0] : t.ok[1];
         uint32_t v[8][D / 64];
         Frag one[NT];
-        f32x4_t o[NT][D / 16];
 #pragma unroll
         for (int e = 0; e < 8; e++)
 #pragma unroll
             for (int w = 0; w < D / 64; w++)
                 v[e][w] = e == mine ? t.v[e][w] : 0u;
 #pragma unroll
-        for (int n = 0; n < NT; n++) {
+        for (int n = 0; n < NT; n++)
 #pragma unroll
             for (int i = 0; i < 4; i++)
                 one[n].w[i] = mine == 2 * i ? p[n].w[i] & 0xFFFFu : mine == 2 * i + 1 ? p[n].w[i] & 0xFFFF0000u : 0u;
+        value_tiles<D>(v, t.vs, [&](int j, const Frag &a) {
 #pragma unroll
-            for (int j = 0; j < D / 16; j++)
-                o[n][j] = f32x4_t{0, 0, 0, 0};
-        }
-        values_product<D, NT>(v, t.vs, one, o);
-#pragma unroll
-        for (int n = 0; n < NT; n++) {
-            const bool y = t.ok[at >> 4] && t0 + at >= r.see[n].lo && t0 + at <= r.see[n].hi;
-#pragma unroll
-            for (int j = 0; j < D / 16; j++)
-                r.o[n][j] += y ? o[n][j] : f32x4_t{0, 0, 0, 0};
-        }
+            for (int n = 0; n < NT; n++) {
+                const bool y = there && t0 + at >= r.see[n].lo && t0 + at <= r.see[n].hi;
+                const f32x4_t o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.f, one[n].f, f32x4_t{0, 0, 0, 0}, 0, 0, 0);
+                r.o[n][j] += y ? o : f32x4_t{0, 0, 0, 0};
+            }
+        });
     }
 }
 
@@ -430,7 +444,7 @@ __device__ __forceinline__ void store_out(const KvQueries &q, int64_t row, int32
         *reinterpret_cast<uint2 *>(p + i) = make_uint2(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]));
 }
 
-template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS) void kv_rows_kernel(KvView c, KvQueries q, KvPlan plan)
+template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_rows_kernel(KvView c, KvQueries q, KvPlan plan)
 {
     __shared__ Join<D> lds;
     __shared__ int64_t lds_sum[4], lds_at[2];
@@ -530,26 +544,53 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS) void kv_rows_
         const uint32_t koff = (uint32_t)(col * c.ld_token) + 16 * g;
         const uint32_t voff = (uint32_t)(4 * g * c.ld_token) + (D / 16) * col;
         auto at_chunk = [&](int32_t i, BlockAt (&x)[2]) {
-            const int32_t blk = (t_first + min(i, c1 - 1) * KVA_CHUNK) >> 4;
+            const int32_t blk = (t_first + i * KVA_CHUNK) >> 4;
             x[0] = block_at(c, b, h, blk);
             x[1] = block_at(c, b, h, blk + 1);
         };
-        BlockAt x[2];
-        Codes<D> cur, next;
-        at_chunk(c0, x);
-        load_codes<D>(c, x, koff, voff, cur);
-        at_chunk(c0 + 1, x);
+        // chunks [f0, f1): this wave's positions are seen by every row; one chunk's codes are loaded while the one
+        // before is worked on, page numbers one further ahead
+        const int32_t f0 = uniform(min(max((all_lo - t_first + KVA_CHUNK - 1) >> 7, c0), c1));
+        const int32_t f1 = uniform(max(min(((all_hi - 31 - t_first) >> 7) + 1, c1), f0));
+        bool left = false;
+        if (f0 < f1) {
+            BlockAt x[2];
+            Codes<D> even, odd;
+            auto step = [&](int32_t i, const Codes<D> &now, Codes<D> &next) {
+                if (i + 1 < f1) {
+                    load_codes<D>(c, x, koff, voff, next);
+                    at_chunk(min(i + 2, f1 - 1), x);
+                }
+                if (irregular<D>(now))
+                    left = true;
+                else
+                    plain_step<D, NT>(r, now, c2);
+            };
+            at_chunk(f0, x);
+            load_codes<D>(c, x, koff, voff, even);
+            at_chunk(min(f0 + 1, f1 - 1), x);
+            for (int32_t i = f0; i < f1; i += 2) {
+                step(i, even, odd);
+                if (i + 1 < f1)
+                    step(i + 1, odd, even);
+            }
+        }
+        // and the others
+#pragma unroll 1
         for (int32_t i = c0; i < c1; i++) {
-            if (i + 1 < c1) {
-                load_codes<D>(c, x, koff, voff, next);
-                at_chunk(i + 2, x);
+            if (i >= f0 && i < f1 && !left) {
+                i = f1 - 1;
+                continue;
             }
             const int32_t t0 = t_first + i * KVA_CHUNK;
-            if (t0 < s.kv_len) {
-                const bool masked = !(cur.ok[0] && cur.ok[1] && t0 >= all_lo && t0 + 31 <= all_hi);
-                rows_step<D, NT>(c, r, cur, t0, s.kv_len, c2, masked);
-            }
-            cur = next;
+            if (t0 >= s.kv_len)
+                break;
+            BlockAt x[2];
+            Codes<D> t;
+            at_chunk(i, x);
+            load_codes<D>(c, x, koff, voff, t);
+            if (i < f0 || i >= f1 || irregular<D>(t))
+                masked_step<D, NT>(r, t, t0, s.kv_len, c2);
         }
 
         // the four waves' rows together

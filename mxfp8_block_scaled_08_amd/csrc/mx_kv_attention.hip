@@ -41,6 +41,8 @@ constexpr int KVA_TILE = 128;       // rows of a workgroup of the other
 constexpr int KVA_STEP = 64;        // positions of its steps
 constexpr float KVA_SLACK = 8.0f;   // log2 of what a weight may exceed 1 by
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
+// (a scale of 0 as the least normal number, so that -inf times it stays -inf)
+constexpr float KVA_LEAST = 1.17549435e-38f;
 #define KVA_NEG (-__builtin_inff())
 
 // Read-only tables through the scalar unit: the constant address space.
@@ -131,6 +133,14 @@ __device__ __forceinline__ bool nan_codes(uint32_t w)
 
 // Scale codes from here on can take a finite code past BF16's range.
 constexpr uint32_t KVA_BIG_SCALE = 247;
+
+// A word's codes with those that are not finite at the scale as zeros.
+__device__ __forceinline__ uint32_t finite_codes(uint32_t w, uint32_t scale)
+{
+    const uint32_t lo = e4m3_bf16<false>(w, cvt_scale(scale)), hi = e4m3_bf16<true>(w, cvt_scale(scale));
+    const auto keep = [](uint32_t bf16, uint32_t byte) { return (bf16 & 0x7F80u) == 0x7F80u ? 0u : byte; };
+    return w & (keep(lo & 0xFFFFu, 0xFFu) | keep(lo >> 16, 0xFF00u) | keep(hi & 0xFFFFu, 0xFF0000u) | keep(hi >> 16, 0xFF000000u));
+}
 
 // ---------------------------------------------------------------------------
 // few rows
@@ -450,7 +460,7 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_ro
     __shared__ int64_t lds_sum[4], lds_at[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int g = lane >> 4, col = lane & 15;
-    const float c2 = q.scale * LOG2E;
+    const float c2 = fmaxf(q.scale * LOG2E, KVA_LEAST);
     int64_t *first = (int64_t *)(plan.ws + plan.off_first);  // [batch] starts on the line, then pieces' length
 
     // the line's length, and where this workgroup's piece starts
@@ -750,26 +760,75 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS) void kv_join_
 // ---------------------------------------------------------------------------
 // many rows
 
-// Swizzled 16-byte unit u of row d of the transposed values in LDS (8 units of 8 positions a row): the eight
-// rows that eight lanes read, and the eight that they write (4 or 2 rows apart), fall on eight banks' groups.
-template <int D> __device__ __forceinline__ int value_unit(int d, int u)
+// A step's keys and values in LDS, BF16, in 16-byte units: keys as [position][D / 8 units ^ position & 7], values
+// transposed as [element][8 units of 8 positions ^ value_mix(element)].  The eight rows that eight lanes read, and the
+// eight that they write (4 or 2 rows of values apart), fall on eight different bank groups.
+template <int D> constexpr int KEY_BYTES = KVA_STEP * D * 2;
+
+template <int D> __device__ __forceinline__ int value_mix(int d)
 {
-    const int f = D == 128 ? (d & 4) | ((d >> 3 ^ d) & 2) | ((d >> 3 ^ d) & 1) : (d & 6) | ((d >> 3 ^ d) & 1);
-    return d * 8 + (u ^ f);
+    return D == 128 ? (d & 4) | ((d >> 3 ^ d) & 3) : (d & 6) | ((d >> 3 ^ d) & 1);
 }
 
-template <int D> struct Step {
-    uint4 k[KVA_STEP * D / 8];  // [position][unit of 8 elements ^ position & 7]
-    uint4 v[KVA_STEP * D / 8];  // [element][unit of 8 positions, swizzled]
+// A row tile's state in a wave: lane l has row l & 31; o[j][i] is element 32 j + 8 (i >> 2) + 4 (l >> 5) + (i & 3).
+template <int D> struct TileState {
+    uint4 q[D / 16];
+    f32x16_t o[D / 32];
+    float m, l;
+    Seen see;
 };
 
-template <int D> __global__ __launch_bounds__(KVA_THREADS) void kv_tiles_kernel(KvView c, KvQueries q, KvPlan plan)
+// Values that may not be finite are left out of a step that some row does not see whole (a weight of 0 would not keep
+// them out of its sum); odd_values adds them, position by position, to the rows that see them.
+template <int D>
+__device__ __forceinline__ void odd_values(const KvView &c, TileState<D> &r, const Frag (&p)[4], int b, int32_t h, int32_t t0,
+                                           int32_t kv_len)
 {
-    constexpr int DT = D / 32;   // tiles of 32 elements
+    const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
+#pragma unroll 1
+    for (int at = 0; at < KVA_STEP; at++) {
+        const BlockAt x = block_at(c, b, h, (t0 + at) >> 4);
+        if (!x.ok || t0 + at >= kv_len)
+            continue;
+        const uint32_t vs = c.v_scale[x.scale];
+        const int k = at >> 4;
+        const uint32_t only[4] = {k == 0 ? ~0u : 0u, k == 1 ? ~0u : 0u, k == 2 ? ~0u : 0u, k == 3 ? ~0u : 0u};
+        const int e = (at >> 2 & 1) == half ? 4 * (at >> 3 & 1) + (at & 3) : -1;
+        const bool y = t0 + at >= r.see.lo && t0 + at <= r.see.hi;
+        Frag one;
+#pragma unroll
+        for (int w = 0; w < 4; w++) {
+            const uint32_t z = (p[0].w[w] & only[0]) | (p[1].w[w] & only[1]) | (p[2].w[w] & only[2]) | (p[3].w[w] & only[3]);
+            one.w[w] = e == 2 * w ? z & 0xFFFFu : e == 2 * w + 1 ? z & 0xFFFF0000u : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 32; j++) {
+            const uint32_t code = c.v[x.codes + (int64_t)(at & 15) * c.ld_token + 32 * j + col];
+            const uint32_t v = (vs == 0xFFu ? 0x7FC0u : e4m3_bf16<false>(code, cvt_scale(vs))) & 0xFFFFu;
+            const uint32_t z = (v & 0x7F80u) == 0x7F80u ? v : 0u;
+            Frag a;
+#pragma unroll
+            for (int w = 0; w < 4; w++)
+                a.w[w] = e == 2 * w ? z : e == 2 * w + 1 ? z << 16 : 0u;
+            f32x16_t o;
+#pragma unroll
+            for (int i = 0; i < 16; i++)
+                o[i] = 0.0f;
+            o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.f, one.f, o, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 16; i++)
+                r.o[j][i] += y ? o[i] : 0.0f;
+        }
+    }
+}
+
+template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kernel(KvView c, KvQueries q, KvPlan plan)
+{
     constexpr int KW = D / 64;   // 16-byte loads of keys a thread and step
     constexpr int VB = D / 32;   // bytes of a value row a thread takes
-    __shared__ Step<D> lds[2];
-    __shared__ int lds_odd[2];
+    constexpr uint32_t BUF = 2 * KEY_BYTES<D>;
+    __shared__ __attribute__((aligned(16))) char lds[2 * BUF];
+    __shared__ uint32_t lds_flags[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
     const int32_t h = blockIdx.x % c.kv_heads;
@@ -783,98 +842,115 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS) void kv_tiles_kernel(
         return;
     const int32_t rows = (int32_t)rows64;
     const int32_t tile = (int32_t)(tiles - 1 - in_seq);  // the longest first
-    const float c2 = q.scale * LOG2E;
+    const float c2 = fmaxf(q.scale * LOG2E, KVA_LEAST);
 
     // this lane's row
+    TileState<D> r;
     const int32_t row = tile * KVA_TILE + wave * 32 + col;
     const int32_t token = min(row, rows - 1) / q.group;
     const int32_t head = h * q.group + min(row, rows - 1) - token * q.group;
-    const Seen see = seen_by(q, s, token);
-    // what every row of the wave sees
-    const int32_t w0 = min(tile * KVA_TILE + wave * 32, rows - 1) / q.group, w1 = min(tile * KVA_TILE + wave * 32 + 31, rows - 1) / q.group;
-    const int32_t all_lo = uniform(seen_by(q, s, w1).lo), all_hi = uniform(seen_by(q, s, w0).hi);
-    // and what any row of the wave, and of the workgroup, does
-    const int32_t any_lo = uniform(seen_by(q, s, w0).lo), any_hi = uniform(seen_by(q, s, w1).hi);
-    const int32_t last = min((tile + 1) * KVA_TILE, rows) - 1;
-    const int32_t lo = seen_by(q, s, tile * KVA_TILE / q.group).lo & ~(KVA_STEP - 1);
-    const int32_t hi = seen_by(q, s, last / q.group).hi;
+    r.see = seen_by(q, s, token);
+    // what every row of the wave sees, and what any does
+    const Seen w0 = seen_by(q, s, min(tile * KVA_TILE + wave * 32, rows - 1) / q.group);
+    const Seen w1 = seen_by(q, s, min(tile * KVA_TILE + wave * 32 + 31, rows - 1) / q.group);
+    const int32_t all_lo = uniform(w1.lo), all_hi = uniform(w0.hi), any_lo = uniform(w0.lo), any_hi = uniform(w1.hi);
+    // and the workgroup's rows
+    const Seen g0 = seen_by(q, s, tile * KVA_TILE / q.group);
+    const Seen g1 = seen_by(q, s, (min((tile + 1) * KVA_TILE, rows) - 1) / q.group);
+    const int32_t lo = uniform(g0.lo & ~(KVA_STEP - 1)), hi = uniform(g1.hi);
+    const int32_t inner_lo = uniform(g1.lo), inner_hi = uniform(g0.hi);
     const int32_t steps = hi >= lo ? (hi - lo) / KVA_STEP + 1 : 0;
     const int32_t each = (steps + plan.splits - 1) / plan.splits;
     const int32_t i0 = min((int32_t)blockIdx.y * each, steps), i1 = min(i0 + each, steps);
 
-    uint4 qf[D / 16];
     {
         const uint16_t *p = q.q + (s.row + token) * q.ld_qt + head * q.ld_qh + 8 * half;
 #pragma unroll
         for (int i = 0; i < D / 16; i++)
-            qf[i] = *reinterpret_cast<const uint4 *>(p + 16 * i);
+            r.q[i] = *reinterpret_cast<const uint4 *>(p + 16 * i);
     }
-    f32x16_t o[DT];
 #pragma unroll
-    for (int j = 0; j < DT; j++)
+    for (int j = 0; j < D / 32; j++)
 #pragma unroll
         for (int i = 0; i < 16; i++)
-            o[j][i] = 0.0f;
-    float m = KVA_NEG, l = 0.0f;
+            r.o[j][i] = 0.0f;
+    r.m = KVA_NEG;
+    r.l = 0.0f;
 
     // A step's codes: wave w takes block w of its four, 16 rows of keys by 4 lanes, and values as (half block, VB
     // elements): positions 4 hv + 0..3 and 8 + 4 hv + 0..3, the order in which a row's weights come out.
+    const int kr = lane >> 2, kq = lane & 3, hv = half, vd = col * VB;
+    const uint32_t koff = (uint32_t)(kr * c.ld_token) + 16 * KW * kq, voff = (uint32_t)(4 * hv * c.ld_token) + vd;
+    uint32_t kst[2 * KW], vst[VB];  // where they go in LDS
+#pragma unroll
+    for (int j = 0; j < 2 * KW; j++)
+        kst[j] = (wave * 16 + kr) * (D * 2) + (((2 * KW * kq + j) ^ (kr & 7)) << 4);
+#pragma unroll
+    for (int j = 0; j < VB; j++)
+        vst[j] = KEY_BYTES<D> + (vd + j) * (KVA_STEP * 2) + (((2 * wave + hv) ^ value_mix<D>(vd + j)) << 4);
+    uint32_t ka[D / 16], va[4];  // and where this lane's parts of the products lie
+#pragma unroll
+    for (int k = 0; k < D / 16; k++)
+        ka[k] = col * (D * 2) + (((2 * k + half) ^ (col & 7)) << 4);
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+        va[k] = KEY_BYTES<D> + col * (KVA_STEP * 2) + (((2 * k + half) ^ value_mix<D>(col)) << 4);
+
     uint4 kc[KW];
-    uint32_t vc[8];
-    uint32_t ks, vs;
-    const int kr = lane >> 2, kq = lane & 3, hv = lane >> 5, vd = (lane & 31) * VB;
+    uint32_t vc[8], ks, vs;
+    bool there;
     auto load = [&](int32_t i) {
-        const int32_t t0 = lo + i * KVA_STEP;
-        const BlockAt x = block_at(c, b, h, (t0 >> 4) + wave);
-        const uint8_t *kb = c.k + x.codes + (int64_t)kr * c.ld_token + 16 * KW * kq;
-        const uint8_t *vb = c.v + x.codes + (int64_t)(4 * hv) * c.ld_token + vd;
+        const BlockAt x = block_at(c, b, h, ((lo + i * KVA_STEP) >> 4) + wave);
+        const uint8_t *kb = c.k + x.codes, *vb = c.v + x.codes;
+        const uint32_t ld = (uint32_t)c.ld_token;
 #pragma unroll
         for (int j = 0; j < KW; j++)
-            kc[j] = reinterpret_cast<const uint4 *>(kb)[j];
+            kc[j] = *reinterpret_cast<const uint4 *>(kb + koff + 16 * j);
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            const uint8_t *p = vb + (int64_t)((e & 3) + 8 * (e >> 2)) * c.ld_token;
+            const uint8_t *p = vb + (voff + ((e & 3) + 8 * (e >> 2)) * ld);
             vc[e] = VB == 4 ? *reinterpret_cast<const uint32_t *>(p) : *reinterpret_cast<const uint16_t *>(p);
         }
         ks = c.k_scale[x.scale];
-        vs = x.ok ? c.v_scale[x.scale] : 0x1FFu;  // (0x1FF: no page)
+        vs = c.v_scale[x.scale];
+        there = x.ok;
     };
-    auto stage = [&](int32_t i, int buf) {
-        const int32_t t0 = lo + i * KVA_STEP + wave * 16;
-        const float kf = cvt_scale(ks);
+    auto stage = [&](int32_t i, uint32_t buf) {
+        const int32_t t0 = lo + i * KVA_STEP;
+        uint32_t flag = there ? 0u : 2u;
+        if (!there || t0 < inner_lo || t0 + KVA_STEP - 1 > inner_hi || __any(max(ks, vs) == 0xFFu)) {
+            // some row may not see all of it: what could not be hidden by a weight of 0 is found here
+            const int32_t at = t0 + wave * 16;
+            vs = !there || at >= s.kv_len ? 127u : vs;  // (behind the last position anything may stand)
+            bool odd = vs >= KVA_BIG_SCALE;
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const bool in = there && at + 4 * hv + (e & 3) + 8 * (e >> 2) < s.kv_len;
+                vc[e] = in ? vc[e] : 0u;
+                odd = odd || nan_codes(vc[e]);
+            }
+            if (__any(odd)) {
+                // (odd_values adds them)
+                flag |= 1u;
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    vc[e] = vs == 0xFFu ? 0u : finite_codes(vc[e], vs);
+                vs = vs == 0xFFu ? 127u : vs;
+            }
+            if (ks == 0xFFu)
+#pragma unroll
+                for (int j = 0; j < KW; j++)
+                    kc[j] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        }
+        const float kf = cvt_scale(ks), vf = cvt_scale(vs);
+        char *to = lds + buf;
 #pragma unroll
         for (int j = 0; j < KW; j++) {
-            const uint32_t w[4] = {kc[j].x, kc[j].y, kc[j].z, kc[j].w};
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-                uint4 x = make_uint4(e4m3_bf16<false>(w[2 * e], kf), e4m3_bf16<true>(w[2 * e], kf),
-                                     e4m3_bf16<false>(w[2 * e + 1], kf), e4m3_bf16<true>(w[2 * e + 1], kf));
-                if (ks == 0xFFu)
-                    x = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
-                const int t = wave * 16 + kr;
-                lds[buf].k[t * (D / 8) + ((2 * KW * kq + 2 * j + e) ^ (t & 7))] = x;
-            }
+            *reinterpret_cast<uint4 *>(to + kst[2 * j]) = make_uint4(e4m3_bf16<false>(kc[j].x, kf), e4m3_bf16<true>(kc[j].x, kf),
+                                                                     e4m3_bf16<false>(kc[j].y, kf), e4m3_bf16<true>(kc[j].y, kf));
+            *reinterpret_cast<uint4 *>(to + kst[2 * j + 1]) = make_uint4(e4m3_bf16<false>(kc[j].z, kf), e4m3_bf16<true>(kc[j].z, kf),
+                                                                         e4m3_bf16<false>(kc[j].w, kf), e4m3_bf16<true>(kc[j].w, kf));
         }
-        bool odd = false;
-        uint32_t sc = vs;
-        if (sc == 0x1FFu || t0 + 16 > s.kv_len) {
-            // behind the last position, or no page: zeros
-            if (sc == 0x1FFu || t0 >= s.kv_len)
-                sc = 127;
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                vc[e] = vs != 0x1FFu && t0 + 4 * hv + (e & 3) + 8 * (e >> 2) < s.kv_len ? vc[e] : 0u;
-        }
-        if (sc == 0xFFu)
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                vc[e] = 0x7F7F7F7Fu;
-#pragma unroll
-        for (int e = 0; e < 8; e++)
-            odd = odd || nan_codes(vc[e]);
-        if (__any(odd || sc >= KVA_BIG_SCALE) && lane == 0)
-            lds_odd[buf] = i + 1;
-        const float vf = cvt_scale(sc);
         uint32_t x[VB][4];
 #pragma unroll
         for (int e = 0; e < 4; e++) {
@@ -889,145 +965,102 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS) void kv_tiles_kernel(
         }
 #pragma unroll
         for (int j = 0; j < VB; j++)
-            lds[buf].v[value_unit<D>(vd + j, 2 * wave + hv)] = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
+            *reinterpret_cast<uint4 *>(to + vst[j]) = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
+        if (lane == 0)
+            reinterpret_cast<uint8_t *>(lds_flags)[(buf ? 4 : 0) + wave] = (uint8_t)flag;
     };
 
-    if (tid < 2)
-        lds_odd[tid] = 0;
-    __syncthreads();
     if (i0 < i1) {
         load(i0);
         stage(i0, 0);
     }
     __syncthreads();
+    uint32_t buf = 0;
     for (int32_t i = i0; i < i1; i++) {
-        const int buf = (i - i0) & 1;
         if (i + 1 < i1)
             load(i + 1);
         const int32_t t0 = lo + i * KVA_STEP;
+        const uint32_t flags = __builtin_amdgcn_readfirstlane(lds_flags[buf ? 1 : 0]);
         if (t0 + KVA_STEP > any_lo && t0 <= any_hi) {  // (else nothing for this wave)
-            f32x16_t sc[2];
+            const char *from = lds + buf;
+            f32x16_t x[2];
 #pragma unroll
             for (int j = 0; j < 2; j++) {
 #pragma unroll
                 for (int k = 0; k < 16; k++)
-                    sc[j][k] = 0.0f;
-                const int t = 32 * j + col;
+                    x[j][k] = 0.0f;
 #pragma unroll
                 for (int k = 0; k < D / 16; k++) {
-                    const uint4 a = lds[buf].k[t * (D / 8) + ((2 * k + half) ^ (t & 7))];
-                    sc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, qf[k]),
-                                                                    sc[j], 0, 0, 0);
+                    const uint4 a = *reinterpret_cast<const uint4 *>(from + ka[k] + 32 * D * 2 * j);
+                    x[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, r.q[k]),
+                                                                   x[j], 0, 0, 0);
                 }
             }
-            // a page that is not there hides its positions from every row: their flags, one bit a block
-            uint32_t gone = 0;
-            {
-                const ConstI32 table = (ConstI32)(uintptr_t)c.table;
-#pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    const int32_t pg = min(((t0 >> 4) + k) >> (c.page_shift - 4), c.max_pages - 1);
-                    gone |= (uint32_t)table[(int64_t)b * c.max_pages + pg] < (uint32_t)c.num_pages ? 0u : 1u << k;
-                }
-            }
-            const bool masked = gone || t0 < all_lo || t0 + KVA_STEP - 1 > all_hi;
-            if (masked) {
+            if (t0 < all_lo || t0 + KVA_STEP - 1 > all_hi || (flags & 0x02020202u)) {
+                // what a row does not see: -inf, of which the exponential makes 0
 #pragma unroll
                 for (int j = 0; j < 2; j++)
 #pragma unroll
                     for (int k = 0; k < 16; k++) {
-                        const int32_t t = 32 * j + 8 * (k >> 2) + 4 * half + (k & 3);
-                        const bool y = t0 + t >= see.lo && t0 + t <= see.hi && !(gone >> (2 * j + (k >> 3)) & 1);
-                        sc[j][k] = y ? sc[j][k] : KVA_NEG;
+                        const int32_t at = t0 + 32 * j + 8 * (k >> 2) + 4 * half + (k & 3);
+                        const bool y = at >= r.see.lo && at <= r.see.hi && !(flags >> (8 * (2 * j + (k >> 3))) & 2);
+                        x[j][k] = y ? x[j][k] : KVA_NEG;
                     }
             }
-            float mt = KVA_NEG;
+            float mt = fmaxf(x[0][0], x[1][0]);
 #pragma unroll
-            for (int j = 0; j < 2; j++)
-#pragma unroll
-                for (int k = 0; k < 16; k++)
-                    mt = fmaxf(mt, sc[j][k]);
+            for (int k = 1; k < 16; k++)
+                mt = fmaxf(fmaxf(mt, x[0][k]), x[1][k]);
             mt = max_xor32(mt);
-            if (__any(mt > m && !((mt - m) * c2 <= KVA_SLACK))) {
-                const float now = fmaxf(m, mt);
-                const float f = m == KVA_NEG ? 0.0f : exp2_fast((m - now) * c2);
-                m = now;
-                l *= f;
+            if (__any(mt > r.m && !((mt - r.m) * c2 <= KVA_SLACK))) {
+                const float now = fmaxf(r.m, mt);
+                const float f = r.m == KVA_NEG ? 0.0f : exp2_fast((r.m - now) * c2);
+                r.m = now;
+                r.l *= f;
 #pragma unroll
-                for (int j = 0; j < DT; j++)
-                    o[j] *= f;
+                for (int j = 0; j < D / 32; j++)
+                    r.o[j] *= f;
             }
-            const float mc = m == KVA_NEG ? 0.0f : m * c2;
+            const float mc = r.m == KVA_NEG ? 0.0f : r.m * c2;
             Frag p[4];
+            float l[4] = {};
 #pragma unroll
             for (int j = 0; j < 2; j++)
 #pragma unroll
                 for (int k = 0; k < 16; k += 2) {
-                    float e0 = exp2_fast(fmaf(sc[j][k], c2, -mc)), e1 = exp2_fast(fmaf(sc[j][k + 1], c2, -mc));
-                    if (masked) {
-                        e0 = sc[j][k] == KVA_NEG ? 0.0f : e0;
-                        e1 = sc[j][k + 1] == KVA_NEG ? 0.0f : e1;
-                    }
-                    l += e0 + e1;
+                    const float e0 = exp2_fast(fmaf(x[j][k], c2, -mc)), e1 = exp2_fast(fmaf(x[j][k + 1], c2, -mc));
+                    l[k >> 2] += e0 + e1;
                     p[2 * j + (k >> 3)].w[(k & 7) >> 1] = pack_bf16(e0, e1);
                 }
-            if (!(masked && lds_odd[buf] == i + 1)) {
+            r.l += (l[0] + l[1]) + (l[2] + l[3]);
 #pragma unroll
-                for (int k = 0; k < 4; k++)
+            for (int k = 0; k < 4; k++)
 #pragma unroll
-                    for (int j = 0; j < DT; j++) {
-                        const uint4 a = lds[buf].v[value_unit<D>(32 * j + col, 2 * k + half)];
-                        o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), p[k].f, o[j], 0, 0, 0);
-                    }
-            } else {
-                // (as in rows_step: position by position, into the rows that see it)
-#pragma unroll
-                for (int k = 0; k < 4; k++)
-#pragma unroll 1
-                    for (int at = 0; at < 16; at++) {
-                        const int e = (at >> 2 & 1) == half ? 4 * (at >> 3) + (at & 3) : -1;
-                        const int32_t t = t0 + 16 * k + at;
-                        const bool y = t >= see.lo && t <= see.hi && !(gone >> k & 1);
-                        Frag one;
-#pragma unroll
-                        for (int w = 0; w < 4; w++)
-                            one.w[w] = e == 2 * w ? p[k].w[w] & 0xFFFFu : e == 2 * w + 1 ? p[k].w[w] & 0xFFFF0000u : 0u;
-#pragma unroll
-                        for (int j = 0; j < DT; j++) {
-                            const uint4 x = lds[buf].v[value_unit<D>(32 * j + col, 2 * k + half)];
-                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                            Frag a;
-#pragma unroll
-                            for (int z = 0; z < 4; z++)
-                                a.w[z] = e == 2 * z ? w[z] & 0xFFFFu : e == 2 * z + 1 ? w[z] & 0xFFFF0000u : 0u;
-                            f32x16_t r;
-#pragma unroll
-                            for (int z = 0; z < 16; z++)
-                                r[z] = 0.0f;
-                            r = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.f, one.f, r, 0, 0, 0);
-#pragma unroll
-                            for (int z = 0; z < 16; z++)
-                                o[j][z] += y ? r[z] : 0.0f;
-                        }
-                    }
-            }
+                for (int j = 0; j < D / 32; j++) {
+                    const uint4 a = *reinterpret_cast<const uint4 *>(from + va[k] + 32 * KVA_STEP * 2 * j);
+                    r.o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), p[k].f, r.o[j], 0, 0, 0);
+                }
+            if (flags & 0x01010101u)
+                odd_values<D>(c, r, p, b, h, t0, s.kv_len);
         }
+        buf ^= BUF;
         if (i + 1 < i1)
-            stage(i + 1, buf ^ 1);
+            stage(i + 1, buf);
         __syncthreads();
     }
 
+    float l = r.l;
     l += __shfl_xor(l, 32, 64);
     if (row >= rows)
         return;
-    const float top = scaled_max(m, c2, l);
+    const float top = scaled_max(r.m, c2, l);
     if (plan.splits == 1) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-        for (int j = 0; j < DT; j++)
+        for (int j = 0; j < D / 32; j++)
 #pragma unroll
             for (int k = 0; k < 16; k += 4) {
-                const float v[4] = {o[j][k] * inv, o[j][k + 1] * inv, o[j][k + 2] * inv, o[j][k + 3] * inv};
+                const float v[4] = {r.o[j][k] * inv, r.o[j][k + 1] * inv, r.o[j][k + 2] * inv, r.o[j][k + 3] * inv};
                 store_out(q, s.row + token, head, 32 * j + 2 * k + 4 * half, v, 4);
             }
         if (q.lse && half == 0)
@@ -1041,10 +1074,10 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS) void kv_tiles_kernel(
         return;  // (its sums are not read)
     float *acc = (float *)(plan.ws + plan.off_acc) + at * D;
 #pragma unroll
-    for (int j = 0; j < DT; j++)
+    for (int j = 0; j < D / 32; j++)
 #pragma unroll
         for (int k = 0; k < 16; k += 4)
-            *reinterpret_cast<float4 *>(acc + 32 * j + 2 * k + 4 * half) = make_float4(o[j][k], o[j][k + 1], o[j][k + 2], o[j][k + 3]);
+            *reinterpret_cast<float4 *>(acc + 32 * j + 2 * k + 4 * half) = make_float4(r.o[j][k], r.o[j][k + 1], r.o[j][k + 2], r.o[j][k + 3]);
 }
 
 // The ranges of a tile's rows together: blockIdx as kv_tiles_kernel's, y the row.

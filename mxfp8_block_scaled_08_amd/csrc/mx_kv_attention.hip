@@ -116,6 +116,10 @@ __device__ __forceinline__ float max_xor16(float v)
     return fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
 }
 
+// Loaded values are there from here on.  (Left open across a loop's start, their wait stays in the loop, where it
+// waits for the loop's own loads instead.)
+__device__ __forceinline__ void arrived(uint4 &v) { asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w)); }
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // A finished range's maximum, m times the scale, as its join takes it: -inf where the row sees nothing of it (kept, as 0
@@ -579,6 +583,11 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_ro
             at_chunk(f0, x);
             load_codes<D>(c, x, koff, voff, even);
             at_chunk(min(f0 + 1, f1 - 1), x);
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int k = 0; k < D / 32; k++)
+                    arrived(r.q[n][k]);
             for (int32_t i = f0; i < f1; i += 2) {
                 step(i, even, odd);
                 if (i + 1 < f1)
@@ -818,6 +827,7 @@ __device__ __forceinline__ void odd_values(const KvView &c, TileState<D> &r, con
 #pragma unroll
             for (int i = 0; i < 16; i++)
                 r.o[j][i] += y ? o[i] : 0.0f;
+            __builtin_amdgcn_sched_barrier(0);  // (one product's registers at a time: the steps' need them)
         }
     }
 }
@@ -881,20 +891,12 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
     // elements): positions 4 hv + 0..3 and 8 + 4 hv + 0..3, the order in which a row's weights come out.
     const int kr = lane >> 2, kq = lane & 3, hv = half, vd = col * VB;
     const uint32_t koff = (uint32_t)(kr * c.ld_token) + 16 * KW * kq, voff = (uint32_t)(4 * hv * c.ld_token) + vd;
-    uint32_t kst[2 * KW], vst[VB];  // where they go in LDS
-#pragma unroll
-    for (int j = 0; j < 2 * KW; j++)
-        kst[j] = (wave * 16 + kr) * (D * 2) + (((2 * KW * kq + j) ^ (kr & 7)) << 4);
-#pragma unroll
-    for (int j = 0; j < VB; j++)
-        vst[j] = KEY_BYTES<D> + (vd + j) * (KVA_STEP * 2) + (((2 * wave + hv) ^ value_mix<D>(vd + j)) << 4);
-    uint32_t ka[D / 16], va[4];  // and where this lane's parts of the products lie
-#pragma unroll
-    for (int k = 0; k < D / 16; k++)
-        ka[k] = col * (D * 2) + (((2 * k + half) ^ (col & 7)) << 4);
-#pragma unroll
-    for (int k = 0; k < 4; k++)
-        va[k] = KEY_BYTES<D> + col * (KVA_STEP * 2) + (((2 * k + half) ^ value_mix<D>(col)) << 4);
+    // Byte addresses in LDS, of which the units' swizzles are exclusive ors: where a thread's codes go (keys: ^ 16 j for
+    // unit j; values: (^ 16 j) + 128 j for element j), and where a lane's parts of the products lie (^ 32 k for part k).
+    const uint32_t kst = (wave * 16 + kr) * (D * 2) + (((2 * KW * kq) ^ (kr & 7)) << 4);
+    const uint32_t vst = KEY_BYTES<D> + vd * (KVA_STEP * 2) + (((2 * wave + hv) ^ value_mix<D>(vd)) << 4);
+    const uint32_t ka = col * (D * 2) + ((half ^ (col & 7)) << 4);
+    const uint32_t va = KEY_BYTES<D> + col * (KVA_STEP * 2) + ((half ^ value_mix<D>(col)) << 4);
 
     uint4 kc[KW];
     uint32_t vc[8], ks, vs;
@@ -943,12 +945,11 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
                     kc[j] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
         }
         const float kf = cvt_scale(ks), vf = cvt_scale(vs);
-        char *to = lds + buf;
 #pragma unroll
         for (int j = 0; j < KW; j++) {
-            *reinterpret_cast<uint4 *>(to + kst[2 * j]) = make_uint4(e4m3_bf16<false>(kc[j].x, kf), e4m3_bf16<true>(kc[j].x, kf),
+            *reinterpret_cast<uint4 *>(lds + ((buf + kst) ^ (32 * j))) = make_uint4(e4m3_bf16<false>(kc[j].x, kf), e4m3_bf16<true>(kc[j].x, kf),
                                                                      e4m3_bf16<false>(kc[j].y, kf), e4m3_bf16<true>(kc[j].y, kf));
-            *reinterpret_cast<uint4 *>(to + kst[2 * j + 1]) = make_uint4(e4m3_bf16<false>(kc[j].z, kf), e4m3_bf16<true>(kc[j].z, kf),
+            *reinterpret_cast<uint4 *>(lds + ((buf + kst) ^ (32 * j + 16))) = make_uint4(e4m3_bf16<false>(kc[j].z, kf), e4m3_bf16<true>(kc[j].z, kf),
                                                                          e4m3_bf16<false>(kc[j].w, kf), e4m3_bf16<true>(kc[j].w, kf));
         }
         uint32_t x[VB][4];
@@ -965,7 +966,7 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
         }
 #pragma unroll
         for (int j = 0; j < VB; j++)
-            *reinterpret_cast<uint4 *>(to + vst[j]) = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
+            *reinterpret_cast<uint4 *>(lds + ((buf + vst) ^ (16 * j)) + KVA_STEP * 2 * j) = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
         if (lane == 0)
             reinterpret_cast<uint8_t *>(lds_flags)[(buf ? 4 : 0) + wave] = (uint8_t)flag;
     };
@@ -974,6 +975,9 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
         load(i0);
         stage(i0, 0);
     }
+#pragma unroll
+    for (int i = 0; i < D / 16; i++)
+        arrived(r.q[i]);
     __syncthreads();
     uint32_t buf = 0;
     for (int32_t i = i0; i < i1; i++) {
@@ -982,7 +986,6 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
         const int32_t t0 = lo + i * KVA_STEP;
         const uint32_t flags = __builtin_amdgcn_readfirstlane(lds_flags[buf ? 1 : 0]);
         if (t0 + KVA_STEP > any_lo && t0 <= any_hi) {  // (else nothing for this wave)
-            const char *from = lds + buf;
             f32x16_t x[2];
 #pragma unroll
             for (int j = 0; j < 2; j++) {
@@ -991,7 +994,7 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
                     x[j][k] = 0.0f;
 #pragma unroll
                 for (int k = 0; k < D / 16; k++) {
-                    const uint4 a = *reinterpret_cast<const uint4 *>(from + ka[k] + 32 * D * 2 * j);
+                    const uint4 a = *reinterpret_cast<const uint4 *>(lds + ((buf + ka) ^ (32 * k)) + 32 * D * 2 * j);
                     x[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, r.q[k]),
                                                                    x[j], 0, 0, 0);
                 }
@@ -1037,7 +1040,7 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
             for (int k = 0; k < 4; k++)
 #pragma unroll
                 for (int j = 0; j < D / 32; j++) {
-                    const uint4 a = *reinterpret_cast<const uint4 *>(from + va[k] + 32 * KVA_STEP * 2 * j);
+                    const uint4 a = *reinterpret_cast<const uint4 *>(lds + ((buf + va) ^ (32 * k)) + 32 * KVA_STEP * 2 * j);
                     r.o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), p[k].f, r.o[j], 0, 0, 0);
                 }
             if (flags & 0x01010101u)

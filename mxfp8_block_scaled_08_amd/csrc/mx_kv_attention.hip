@@ -156,6 +156,16 @@ struct BlockAt {
     bool ok;
 };
 
+// A byte that is the same for every lane, kept in a vector register: as a scalar it would be read out, and waited for,
+// right behind its load.  none: a zero that the compiler does not know.
+__device__ __forceinline__ uint32_t byte_of(const uint8_t *p, uint32_t none) { return p[none]; }
+__device__ __forceinline__ uint32_t unknown_zero()
+{
+    uint32_t z = 0;
+    asm volatile("" : "+v"(z));
+    return z;
+}
+
 __device__ __forceinline__ BlockAt block_at(const KvView &c, int b, int32_t h, int32_t blk)
 {
     const int32_t shift = c.page_shift - 4;
@@ -171,6 +181,12 @@ __device__ __forceinline__ BlockAt block_at(const KvView &c, int b, int32_t h, i
     return r;
 }
 
+// The block's 16 rows as a buffer: one offset register a lane serves all its loads, the rows' steps are scalar.
+template <int D> __device__ __forceinline__ __amdgpu_buffer_rsrc_t block_range(const uint8_t *p, const BlockAt &at, uint32_t ld)
+{
+    return byte_range(p + at.codes, 15 * ld + D);
+}
+
 // 32 positions' codes in a wave: K rows t = 16 j + (lane & 15), bytes 64 i + 16 (lane >> 4) ..; V rows
 // t = 16 (e >> 2) + 4 (lane >> 4) + (e & 3), bytes (D / 16) (lane & 15) ..
 template <int D> struct Codes {
@@ -181,27 +197,30 @@ template <int D> struct Codes {
 };
 
 template <int D>
-__device__ __forceinline__ void load_codes(const KvView &c, const BlockAt (&at)[2], uint32_t koff, uint32_t voff, Codes<D> &t)
+__device__ __forceinline__ void load_codes(const KvView &c, const BlockAt (&at)[2], uint32_t koff, uint32_t voff, uint32_t none, Codes<D> &t)
 {
     const uint32_t ld = (uint32_t)c.ld_token;
 #pragma unroll
     for (int j = 0; j < 2; j++) {
-        const uint8_t *kb = c.k + at[j].codes, *vb = c.v + at[j].codes;
+        t.ks[j] = byte_of(c.k_scale + at[j].scale, none);
+        t.vs[j] = byte_of(c.v_scale + at[j].scale, none);
+        t.ok[j] = at[j].ok;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+        const __amdgpu_buffer_rsrc_t kb = block_range<D>(c.k, at[j], ld), vb = block_range<D>(c.v, at[j], ld);
 #pragma unroll
         for (int i = 0; i < D / 64; i++)
-            t.k[j][i] = *reinterpret_cast<const uint4 *>(kb + koff + 64 * i);
+            t.k[j][i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(kb, koff, 64 * i, 0));
 #pragma unroll
         for (int e = 0; e < 4; e++)
             if constexpr (D == 128) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(vb + voff + e * ld);
+                const uint2 w = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(vb, voff, e * ld, 0));
                 t.v[4 * j + e][0] = w.x;
                 t.v[4 * j + e][1] = w.y;
             } else {
-                t.v[4 * j + e][0] = *reinterpret_cast<const uint32_t *>(vb + voff + e * ld);
+                t.v[4 * j + e][0] = __builtin_amdgcn_raw_buffer_load_b32(vb, voff, e * ld, 0);
             }
-        t.ks[j] = c.k_scale[at[j].scale];
-        t.vs[j] = c.v_scale[at[j].scale];
-        t.ok[j] = at[j].ok;
     }
 }
 
@@ -557,6 +576,7 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_ro
         const int32_t t_first = first_seen(q, s) + wave * 32;
         const uint32_t koff = (uint32_t)(col * c.ld_token) + 16 * g;
         const uint32_t voff = (uint32_t)(4 * g * c.ld_token) + (D / 16) * col;
+        const uint32_t none = unknown_zero();
         auto at_chunk = [&](int32_t i, BlockAt (&x)[2]) {
             const int32_t blk = (t_first + i * KVA_CHUNK) >> 4;
             x[0] = block_at(c, b, h, blk);
@@ -572,7 +592,7 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_ro
             Codes<D> even, odd;
             auto step = [&](int32_t i, const Codes<D> &now, Codes<D> &next) {
                 if (i + 1 < f1) {
-                    load_codes<D>(c, x, koff, voff, next);
+                    load_codes<D>(c, x, koff, voff, none, next);
                     at_chunk(min(i + 2, f1 - 1), x);
                 }
                 if (irregular<D>(now))
@@ -581,7 +601,7 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_ro
                     plain_step<D, NT>(r, now, c2);
             };
             at_chunk(f0, x);
-            load_codes<D>(c, x, koff, voff, even);
+            load_codes<D>(c, x, koff, voff, none, even);
             at_chunk(min(f0 + 1, f1 - 1), x);
 #pragma unroll
             for (int n = 0; n < NT; n++)
@@ -607,7 +627,7 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_ro
             BlockAt x[2];
             Codes<D> t;
             at_chunk(i, x);
-            load_codes<D>(c, x, koff, voff, t);
+            load_codes<D>(c, x, koff, voff, none, t);
             if (i < f0 || i >= f1 || irregular<D>(t))
                 masked_step<D, NT>(r, t, t0, s.kv_len, c2);
         }
@@ -901,21 +921,24 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
     uint4 kc[KW];
     uint32_t vc[8], ks, vs;
     bool there;
-    auto load = [&](int32_t i) {
-        const BlockAt x = block_at(c, b, h, ((lo + i * KVA_STEP) >> 4) + wave);
-        const uint8_t *kb = c.k + x.codes, *vb = c.v + x.codes;
+    const uint32_t none = unknown_zero();
+    BlockAt x;  // of the step that is loaded next
+    auto find = [&](int32_t i) { x = block_at(c, b, h, ((lo + min(i, i1 - 1) * KVA_STEP) >> 4) + wave); };
+    auto load = [&]() {
+        ks = byte_of(c.k_scale + x.scale, none);
+        vs = byte_of(c.v_scale + x.scale, none);
+        there = x.ok;
         const uint32_t ld = (uint32_t)c.ld_token;
+        const __amdgpu_buffer_rsrc_t kb = block_range<D>(c.k, x, ld), vb = block_range<D>(c.v, x, ld);
 #pragma unroll
         for (int j = 0; j < KW; j++)
-            kc[j] = *reinterpret_cast<const uint4 *>(kb + koff + 16 * j);
+            kc[j] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(kb, koff, 16 * j, 0));
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            const uint8_t *p = vb + (voff + ((e & 3) + 8 * (e >> 2)) * ld);
-            vc[e] = VB == 4 ? *reinterpret_cast<const uint32_t *>(p) : *reinterpret_cast<const uint16_t *>(p);
+            const uint32_t step = ((e & 3) + 8 * (e >> 2)) * ld;
+            vc[e] = VB == 4 ? __builtin_amdgcn_raw_buffer_load_b32(vb, voff, step, 0)
+                            : (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(vb, voff, step, 0);
         }
-        ks = c.k_scale[x.scale];
-        vs = c.v_scale[x.scale];
-        there = x.ok;
     };
     auto stage = [&](int32_t i, uint32_t buf) {
         const int32_t t0 = lo + i * KVA_STEP;
@@ -972,7 +995,9 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
     };
 
     if (i0 < i1) {
-        load(i0);
+        find(i0);
+        load();
+        find(i0 + 1);
         stage(i0, 0);
     }
 #pragma unroll
@@ -981,8 +1006,10 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
     __syncthreads();
     uint32_t buf = 0;
     for (int32_t i = i0; i < i1; i++) {
-        if (i + 1 < i1)
-            load(i + 1);
+        if (i + 1 < i1) {
+            load();
+            find(i + 2);
+        }
         const int32_t t0 = lo + i * KVA_STEP;
         const uint32_t flags = __builtin_amdgcn_readfirstlane(lds_flags[buf ? 1 : 0]);
         if (t0 + KVA_STEP > any_lo && t0 <= any_hi) {  // (else nothing for this wave)

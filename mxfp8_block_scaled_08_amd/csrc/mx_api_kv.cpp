@@ -99,8 +99,10 @@ static mx_status check_cache(const char *fn, const mx_kv_cache *c, int64_t token
                     "kv_heads below 2^23, tokens below 2^27", fn);
     const int64_t most = (int64_t)1 << 46;
     if (c->ld_token < 0 || c->ld_head < 0 || c->ld_page < 0 || c->ld_token >= (int64_t)1 << 20 ||
-        (c->num_pages > 1 && c->ld_page >= most / c->num_pages) || (c->kv_heads > 1 && c->ld_head >= most / c->kv_heads))
-        return fail(MX_ERR_UNSUPPORTED, "%s: ld_token must be below 2^20 and the cache below 2^46 bytes", fn);
+        (c->num_pages > 1 && c->ld_page >= (int64_t)1 << 32) || (c->kv_heads > 1 && c->ld_head >= most / c->kv_heads) ||
+        c->num_pages * c->kv_heads >= ((int64_t)1 << 31) / (c->page_size / MX_KV_BLOCK))
+        return fail(MX_ERR_UNSUPPORTED,
+                    "%s: ld_token must be below 2^20, ld_page below 2^32, the cache below 2^46 bytes and 2^31 blocks", fn);
     const int64_t dims[3][2] = {{c->ld_token, c->page_size}, {c->ld_head, c->kv_heads}, {c->ld_page, c->num_pages}};
     const int64_t inside = nested(dims, 3, c->head_dim);
     if (inside < 0)

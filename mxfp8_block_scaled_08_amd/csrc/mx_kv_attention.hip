@@ -149,16 +149,9 @@ __device__ __forceinline__ uint32_t finite_codes(uint32_t w, uint32_t scale)
 // ---------------------------------------------------------------------------
 // few rows
 
-// A page's part for one block of 16 positions, the same for every lane of the wave.
-struct BlockAt {
-    int64_t codes;  // offset of the block's first row
-    int64_t scale;
-    bool ok;
-};
-
 // A byte that is the same for every lane, kept in a vector register: as a scalar it would be read out, and waited for,
 // right behind its load.  none: a zero that the compiler does not know.
-__device__ __forceinline__ uint32_t byte_of(const uint8_t *p, uint32_t none) { return p[none]; }
+__device__ __forceinline__ uint32_t byte_of(const uint8_t *p, uint32_t at, uint32_t none) { return p[at + none]; }
 __device__ __forceinline__ uint32_t unknown_zero()
 {
     uint32_t z = 0;
@@ -166,18 +159,48 @@ __device__ __forceinline__ uint32_t unknown_zero()
     return z;
 }
 
-__device__ __forceinline__ BlockAt block_at(const KvView &c, int b, int32_t h, int32_t blk)
+// A page's part for one block of 16 positions, the same for every lane of the wave.
+struct BlockAt {
+    int64_t codes;   // offset of the block's first row
+    uint32_t scale;
+    bool ok;
+};
+
+// One head of one sequence: what the lookup of a block needs, with as few scalar instructions as it takes (a step of the
+// many-row kernel spent a tenth of its time on 64-bit ones).
+struct HeadCache {
+    ConstI32 table;  // the sequence's row
+    const uint8_t *k, *v, *k_scale, *v_scale;
+    uint32_t ld_page, ld_token, scale_page;
+    int32_t num_pages, last, shift;
+};
+
+__device__ __forceinline__ HeadCache head_cache(const KvView &c, int b, int32_t h)
 {
-    const int32_t shift = c.page_shift - 4;
-    const int32_t i = blk >> shift;
-    const ConstI32 table = (ConstI32)(uintptr_t)c.table;
-    const int32_t p = table[(int64_t)b * c.max_pages + min(max(i, 0), c.max_pages - 1)];
+    HeadCache r;
+    r.shift = c.page_shift - 4;
+    r.table = (ConstI32)(uintptr_t)(c.table + (int64_t)b * c.max_pages);
+    r.k = c.k + h * c.ld_head;
+    r.v = c.v + h * c.ld_head;
+    r.k_scale = c.k_scale + ((int64_t)h << r.shift);
+    r.v_scale = c.v_scale + ((int64_t)h << r.shift);
+    r.ld_page = (uint32_t)c.ld_page;
+    r.ld_token = (uint32_t)c.ld_token;
+    r.scale_page = (uint32_t)c.kv_heads << r.shift;
+    r.num_pages = c.num_pages;
+    r.last = c.max_pages - 1;
+    return r;
+}
+
+// Block blk >= 0 (behind the table's end: its last page's, which no position is in)
+__device__ __forceinline__ BlockAt block_at(const HeadCache &c, int32_t blk)
+{
+    const uint32_t p = (uint32_t)c.table[min(blk >> c.shift, c.last)];
     BlockAt r;
-    r.ok = (uint32_t)p < (uint32_t)c.num_pages && i < c.max_pages;
-    const int64_t page = r.ok ? p : 0;
-    const int32_t in = blk & ((1 << shift) - 1);
-    r.codes = page * c.ld_page + h * c.ld_head + (int64_t)(in * 16) * c.ld_token;
-    r.scale = ((page * c.kv_heads + h) << shift) + in;
+    r.ok = p < (uint32_t)c.num_pages;
+    const uint32_t page = r.ok ? p : 0, in = (uint32_t)blk & ((1u << c.shift) - 1);
+    r.codes = (int64_t)((uint64_t)page * c.ld_page + in * 16 * c.ld_token);
+    r.scale = page * c.scale_page + in;
     return r;
 }
 
@@ -197,13 +220,13 @@ template <int D> struct Codes {
 };
 
 template <int D>
-__device__ __forceinline__ void load_codes(const KvView &c, const BlockAt (&at)[2], uint32_t koff, uint32_t voff, uint32_t none, Codes<D> &t)
+__device__ __forceinline__ void load_codes(const HeadCache &c, const BlockAt (&at)[2], uint32_t koff, uint32_t voff, uint32_t none, Codes<D> &t)
 {
-    const uint32_t ld = (uint32_t)c.ld_token;
+    const uint32_t ld = c.ld_token;
 #pragma unroll
     for (int j = 0; j < 2; j++) {
-        t.ks[j] = byte_of(c.k_scale + at[j].scale, none);
-        t.vs[j] = byte_of(c.v_scale + at[j].scale, none);
+        t.ks[j] = byte_of(c.k_scale, at[j].scale, none);
+        t.vs[j] = byte_of(c.v_scale, at[j].scale, none);
         t.ok[j] = at[j].ok;
     }
 #pragma unroll
@@ -577,10 +600,11 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_ro
         const uint32_t koff = (uint32_t)(col * c.ld_token) + 16 * g;
         const uint32_t voff = (uint32_t)(4 * g * c.ld_token) + (D / 16) * col;
         const uint32_t none = unknown_zero();
+        const HeadCache hc = head_cache(c, b, h);
         auto at_chunk = [&](int32_t i, BlockAt (&x)[2]) {
             const int32_t blk = (t_first + i * KVA_CHUNK) >> 4;
-            x[0] = block_at(c, b, h, blk);
-            x[1] = block_at(c, b, h, blk + 1);
+            x[0] = block_at(hc, blk);
+            x[1] = block_at(hc, blk + 1);
         };
         // chunks [f0, f1): this wave's positions are seen by every row; one chunk's codes are loaded while the one
         // before is worked on, page numbers one further ahead
@@ -592,7 +616,7 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_ro
             Codes<D> even, odd;
             auto step = [&](int32_t i, const Codes<D> &now, Codes<D> &next) {
                 if (i + 1 < f1) {
-                    load_codes<D>(c, x, koff, voff, none, next);
+                    load_codes<D>(hc, x, koff, voff, none, next);
                     at_chunk(min(i + 2, f1 - 1), x);
                 }
                 if (irregular<D>(now))
@@ -601,7 +625,7 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_ro
                     plain_step<D, NT>(r, now, c2);
             };
             at_chunk(f0, x);
-            load_codes<D>(c, x, koff, voff, none, even);
+            load_codes<D>(hc, x, koff, voff, none, even);
             at_chunk(min(f0 + 1, f1 - 1), x);
 #pragma unroll
             for (int n = 0; n < NT; n++)
@@ -627,7 +651,7 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_ro
             BlockAt x[2];
             Codes<D> t;
             at_chunk(i, x);
-            load_codes<D>(c, x, koff, voff, none, t);
+            load_codes<D>(hc, x, koff, voff, none, t);
             if (i < f0 || i >= f1 || irregular<D>(t))
                 masked_step<D, NT>(r, t, t0, s.kv_len, c2);
         }
@@ -789,14 +813,22 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS) void kv_join_
 // ---------------------------------------------------------------------------
 // many rows
 
-// A step's keys and values in LDS, BF16, in 16-byte units: keys as [position][D / 8 units ^ position & 7], values
-// transposed as [element][8 units of 8 positions ^ value_mix(element)].  The eight rows that eight lanes read, and the
-// eight that they write (4 or 2 rows of values apart), fall on eight different bank groups.
+// A step's keys and values in LDS, BF16, in units of 16 bytes: keys as [position][D / 8 units], values transposed as
+// [element][8 units of 8 positions].  LDS has 64 banks: sixteen lanes' units at once, so units are swizzled (and the rows
+// of values paired) such that the sixteen rows that sixteen lanes read, and the sixteen places that they write (values:
+// rows 4 or 2 apart), fall on different banks.  (Swizzled for eight lanes, a third of LDS' busy cycles were conflicts.)
 template <int D> constexpr int KEY_BYTES = KVA_STEP * D * 2;
 
-template <int D> __device__ __forceinline__ int value_mix(int d)
+template <int D> __device__ __forceinline__ uint32_t key_at(int t, int u)
 {
-    return D == 128 ? (d & 4) | ((d >> 3 ^ d) & 3) : (d & 6) | ((d >> 3 ^ d) & 1);
+    return t * (D * 2) + ((u ^ (D == 128 ? t & 15 : t >> 1 & 7)) << 4);
+}
+
+template <int D> __device__ __forceinline__ uint32_t value_at(int d, int u)
+{
+    const int mix = D == 128 ? (d & 4) | ((d >> 3 ^ d) & 3) : (d & 6) | ((d >> 3 ^ d) & 1);
+    const int row = d ^ (d >> (D == 128 ? 5 : 4) & 1);
+    return KEY_BYTES<D> + row * (KVA_STEP * 2) + ((u ^ mix) << 4);
 }
 
 // A row tile's state in a wave: lane l has row l & 31; o[j][i] is element 32 j + 8 (i >> 2) + 4 (l >> 5) + (i & 3).
@@ -810,13 +842,12 @@ template <int D> struct TileState {
 // Values that may not be finite are left out of a step that some row does not see whole (a weight of 0 would not keep
 // them out of its sum); odd_values adds them, position by position, to the rows that see them.
 template <int D>
-__device__ __forceinline__ void odd_values(const KvView &c, TileState<D> &r, const Frag (&p)[4], int b, int32_t h, int32_t t0,
-                                           int32_t kv_len)
+__device__ __forceinline__ void odd_values(const HeadCache &c, TileState<D> &r, const Frag (&p)[4], int32_t t0, int32_t kv_len)
 {
     const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
 #pragma unroll 1
     for (int at = 0; at < KVA_STEP; at++) {
-        const BlockAt x = block_at(c, b, h, (t0 + at) >> 4);
+        const BlockAt x = block_at(c, (t0 + at) >> 4);
         if (!x.ok || t0 + at >= kv_len)
             continue;
         const uint32_t vs = c.v_scale[x.scale];
@@ -832,7 +863,7 @@ __device__ __forceinline__ void odd_values(const KvView &c, TileState<D> &r, con
         }
 #pragma unroll
         for (int j = 0; j < D / 32; j++) {
-            const uint32_t code = c.v[x.codes + (int64_t)(at & 15) * c.ld_token + 32 * j + col];
+            const uint32_t code = c.v[x.codes + (at & 15) * c.ld_token + 32 * j + col];
             const uint32_t v = (vs == 0xFFu ? 0x7FC0u : e4m3_bf16<false>(code, cvt_scale(vs))) & 0xFFFFu;
             const uint32_t z = (v & 0x7F80u) == 0x7F80u ? v : 0u;
             Frag a;
@@ -880,10 +911,10 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
     const int32_t token = min(row, rows - 1) / q.group;
     const int32_t head = h * q.group + min(row, rows - 1) - token * q.group;
     r.see = seen_by(q, s, token);
-    // what every row of the wave sees, and what any does
+    // what every row of the wave sees
     const Seen w0 = seen_by(q, s, min(tile * KVA_TILE + wave * 32, rows - 1) / q.group);
     const Seen w1 = seen_by(q, s, min(tile * KVA_TILE + wave * 32 + 31, rows - 1) / q.group);
-    const int32_t all_lo = uniform(w1.lo), all_hi = uniform(w0.hi), any_lo = uniform(w0.lo), any_hi = uniform(w1.hi);
+    const int32_t all_lo = uniform(w1.lo), all_hi = uniform(w0.hi);
     // and the workgroup's rows
     const Seen g0 = seen_by(q, s, tile * KVA_TILE / q.group);
     const Seen g1 = seen_by(q, s, (min((tile + 1) * KVA_TILE, rows) - 1) / q.group);
@@ -911,36 +942,38 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
     // elements): positions 4 hv + 0..3 and 8 + 4 hv + 0..3, the order in which a row's weights come out.
     const int kr = lane >> 2, kq = lane & 3, hv = half, vd = col * VB;
     const uint32_t koff = (uint32_t)(kr * c.ld_token) + 16 * KW * kq, voff = (uint32_t)(4 * hv * c.ld_token) + vd;
-    // Byte addresses in LDS, of which the units' swizzles are exclusive ors: where a thread's codes go (keys: ^ 16 j for
-    // unit j; values: (^ 16 j) + 128 j for element j), and where a lane's parts of the products lie (^ 32 k for part k).
-    const uint32_t kst = (wave * 16 + kr) * (D * 2) + (((2 * KW * kq) ^ (kr & 7)) << 4);
-    const uint32_t vst = KEY_BYTES<D> + vd * (KVA_STEP * 2) + (((2 * wave + hv) ^ value_mix<D>(vd)) << 4);
-    const uint32_t ka = col * (D * 2) + ((half ^ (col & 7)) << 4);
-    const uint32_t va = KEY_BYTES<D> + col * (KVA_STEP * 2) + ((half ^ value_mix<D>(col)) << 4);
+    // Byte addresses in LDS, where a thread's codes go (keys: ^ 16 j for unit j; values: ^ 144 j for element j) and where
+    // a lane's parts of the products lie (^ 32 k for part k; values of elements 32 j ..: D = 128 pairs odd j's rows the
+    // other way, ^ 128).
+    const uint32_t kst = key_at<D>(wave * 16 + kr, 2 * KW * kq), vst = value_at<D>(vd, 2 * wave + hv);
+    const uint32_t ka = key_at<D>(col, half), va = value_at<D>(col, half);
+    constexpr uint32_t ODD = D == 128 ? 128 : 0;
 
     uint4 kc[KW];
     uint32_t vc[8], ks, vs;
     bool there;
     const uint32_t none = unknown_zero();
-    BlockAt x;  // of the step that is loaded next
-    auto find = [&](int32_t i) { x = block_at(c, b, h, ((lo + min(i, i1 - 1) * KVA_STEP) >> 4) + wave); };
+    const HeadCache hc = head_cache(c, b, h);
+    const uint32_t ld = hc.ld_token, voff8 = voff + 8 * ld;
+    BlockAt at;  // of the step that is loaded next
+    auto find = [&](int32_t i) { at = block_at(hc, ((lo + min(i, i1 - 1) * KVA_STEP) >> 4) + wave); };
     auto load = [&]() {
-        ks = byte_of(c.k_scale + x.scale, none);
-        vs = byte_of(c.v_scale + x.scale, none);
-        there = x.ok;
-        const uint32_t ld = (uint32_t)c.ld_token;
-        const __amdgpu_buffer_rsrc_t kb = block_range<D>(c.k, x, ld), vb = block_range<D>(c.v, x, ld);
+        ks = byte_of(hc.k_scale, at.scale, none);
+        vs = byte_of(hc.v_scale, at.scale, none);
+        there = at.ok;
+        const __amdgpu_buffer_rsrc_t kb = block_range<D>(hc.k, at, ld), vb = block_range<D>(hc.v, at, ld);
 #pragma unroll
         for (int j = 0; j < KW; j++)
             kc[j] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(kb, koff, 16 * j, 0));
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            const uint32_t step = ((e & 3) + 8 * (e >> 2)) * ld;
-            vc[e] = VB == 4 ? __builtin_amdgcn_raw_buffer_load_b32(vb, voff, step, 0)
-                            : (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(vb, voff, step, 0);
+            const uint32_t from = e < 4 ? voff : voff8, step = (e & 3) * ld;
+            vc[e] = VB == 4 ? __builtin_amdgcn_raw_buffer_load_b32(vb, from, step, 0)
+                            : (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(vb, from, step, 0);
         }
     };
-    auto stage = [&](int32_t i, uint32_t buf) {
+    // The loaded step's flag byte (bit 0: odd_values, bit 1: no page), and its codes made fit for it.
+    auto settle = [&](int32_t i, uint32_t buf) {
         const int32_t t0 = lo + i * KVA_STEP;
         uint32_t flag = there ? 0u : 2u;
         if (!there || t0 < inner_lo || t0 + KVA_STEP - 1 > inner_hi || __any(max(ks, vs) == 0xFFu)) {
@@ -967,6 +1000,10 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
                 for (int j = 0; j < KW; j++)
                     kc[j] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
         }
+        if (lane == 0)
+            reinterpret_cast<uint8_t *>(lds_flags)[(buf ? 4 : 0) + wave] = (uint8_t)flag;
+    };
+    auto stage = [&](uint32_t buf) {
         const float kf = cvt_scale(ks), vf = cvt_scale(vs);
 #pragma unroll
         for (int j = 0; j < KW; j++) {
@@ -989,16 +1026,20 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
         }
 #pragma unroll
         for (int j = 0; j < VB; j++)
-            *reinterpret_cast<uint4 *>(lds + ((buf + vst) ^ (16 * j)) + KVA_STEP * 2 * j) = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
-        if (lane == 0)
-            reinterpret_cast<uint8_t *>(lds_flags)[(buf ? 4 : 0) + wave] = (uint8_t)flag;
+            *reinterpret_cast<uint4 *>(lds + ((buf + vst) ^ (144 * j))) = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
     };
 
+    // Step i is worked on out of one buffer while step i + 1 is converted into the other, among the first product's matrix
+    // instructions (behind them it cost a quarter of the time), and step i + 2 is on its way.  (Past the last step the
+    // last one is staged again, which nobody reads.)
     if (i0 < i1) {
         find(i0);
         load();
         find(i0 + 1);
-        stage(i0, 0);
+        settle(i0, 0);
+        stage(0);
+        load();
+        find(i0 + 2);
     }
 #pragma unroll
     for (int i = 0; i < D / 16; i++)
@@ -1006,76 +1047,72 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
     __syncthreads();
     uint32_t buf = 0;
     for (int32_t i = i0; i < i1; i++) {
-        if (i + 1 < i1) {
-            load();
-            find(i + 2);
-        }
         const int32_t t0 = lo + i * KVA_STEP;
         const uint32_t flags = __builtin_amdgcn_readfirstlane(lds_flags[buf ? 1 : 0]);
-        if (t0 + KVA_STEP > any_lo && t0 <= any_hi) {  // (else nothing for this wave)
-            f32x16_t x[2];
+        settle(min(i + 1, i1 - 1), buf ^ BUF);
+        f32x16_t x[2];
 #pragma unroll
-            for (int j = 0; j < 2; j++) {
+        for (int j = 0; j < 2; j++) {
 #pragma unroll
-                for (int k = 0; k < 16; k++)
-                    x[j][k] = 0.0f;
+            for (int k = 0; k < 16; k++)
+                x[j][k] = 0.0f;
 #pragma unroll
-                for (int k = 0; k < D / 16; k++) {
-                    const uint4 a = *reinterpret_cast<const uint4 *>(lds + ((buf + ka) ^ (32 * k)) + 32 * D * 2 * j);
-                    x[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, r.q[k]),
-                                                                   x[j], 0, 0, 0);
-                }
+            for (int k = 0; k < D / 16; k++) {
+                const uint4 a = *reinterpret_cast<const uint4 *>(lds + ((buf + ka) ^ (32 * k)) + 32 * D * 2 * j);
+                x[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, r.q[k]),
+                                                               x[j], 0, 0, 0);
             }
-            if (t0 < all_lo || t0 + KVA_STEP - 1 > all_hi || (flags & 0x02020202u)) {
-                // what a row does not see: -inf, of which the exponential makes 0
-#pragma unroll
-                for (int j = 0; j < 2; j++)
-#pragma unroll
-                    for (int k = 0; k < 16; k++) {
-                        const int32_t at = t0 + 32 * j + 8 * (k >> 2) + 4 * half + (k & 3);
-                        const bool y = at >= r.see.lo && at <= r.see.hi && !(flags >> (8 * (2 * j + (k >> 3))) & 2);
-                        x[j][k] = y ? x[j][k] : KVA_NEG;
-                    }
-            }
-            float mt = fmaxf(x[0][0], x[1][0]);
-#pragma unroll
-            for (int k = 1; k < 16; k++)
-                mt = fmaxf(fmaxf(mt, x[0][k]), x[1][k]);
-            mt = max_xor32(mt);
-            if (__any(mt > r.m && !((mt - r.m) * c2 <= KVA_SLACK))) {
-                const float now = fmaxf(r.m, mt);
-                const float f = r.m == KVA_NEG ? 0.0f : exp2_fast((r.m - now) * c2);
-                r.m = now;
-                r.l *= f;
-#pragma unroll
-                for (int j = 0; j < D / 32; j++)
-                    r.o[j] *= f;
-            }
-            const float mc = r.m == KVA_NEG ? 0.0f : r.m * c2;
-            Frag p[4];
-            float l[4] = {};
+        }
+        stage(buf ^ BUF);
+        load();
+        if (t0 < all_lo || t0 + KVA_STEP - 1 > all_hi || (flags & 0x02020202u)) {
+            // what a row does not see: -inf, of which the exponential makes 0
 #pragma unroll
             for (int j = 0; j < 2; j++)
 #pragma unroll
-                for (int k = 0; k < 16; k += 2) {
-                    const float e0 = exp2_fast(fmaf(x[j][k], c2, -mc)), e1 = exp2_fast(fmaf(x[j][k + 1], c2, -mc));
-                    l[k >> 2] += e0 + e1;
-                    p[2 * j + (k >> 3)].w[(k & 7) >> 1] = pack_bf16(e0, e1);
+                for (int k = 0; k < 16; k++) {
+                    const int32_t at = t0 + 32 * j + 8 * (k >> 2) + 4 * half + (k & 3);
+                    const bool y = at >= r.see.lo && at <= r.see.hi && !(flags >> (8 * (2 * j + (k >> 3))) & 2);
+                    x[j][k] = y ? x[j][k] : KVA_NEG;
                 }
-            r.l += (l[0] + l[1]) + (l[2] + l[3]);
-#pragma unroll
-            for (int k = 0; k < 4; k++)
-#pragma unroll
-                for (int j = 0; j < D / 32; j++) {
-                    const uint4 a = *reinterpret_cast<const uint4 *>(lds + ((buf + va) ^ (32 * k)) + 32 * KVA_STEP * 2 * j);
-                    r.o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), p[k].f, r.o[j], 0, 0, 0);
-                }
-            if (flags & 0x01010101u)
-                odd_values<D>(c, r, p, b, h, t0, s.kv_len);
         }
+        float mt = fmaxf(x[0][0], x[1][0]);
+#pragma unroll
+        for (int k = 1; k < 16; k++)
+            mt = fmaxf(fmaxf(mt, x[0][k]), x[1][k]);
+        mt = max_xor32(mt);
+        if (__any(mt > r.m && !((mt - r.m) * c2 <= KVA_SLACK))) {
+            const float now = fmaxf(r.m, mt);
+            const float f = r.m == KVA_NEG ? 0.0f : exp2_fast((r.m - now) * c2);
+            r.m = now;
+            r.l *= f;
+#pragma unroll
+            for (int j = 0; j < D / 32; j++)
+                r.o[j] *= f;
+        }
+        const float mc = r.m == KVA_NEG ? 0.0f : r.m * c2;
+        Frag p[4];
+        float l[4] = {};
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+                const float e0 = exp2_fast(fmaf(x[j][k], c2, -mc)), e1 = exp2_fast(fmaf(x[j][k + 1], c2, -mc));
+                l[k >> 2] += e0 + e1;
+                p[2 * j + (k >> 3)].w[(k & 7) >> 1] = pack_bf16(e0, e1);
+            }
+        r.l += (l[0] + l[1]) + (l[2] + l[3]);
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+#pragma unroll
+            for (int j = 0; j < D / 32; j++) {
+                const uint4 a = *reinterpret_cast<const uint4 *>(lds + ((buf + va) ^ (32 * k) ^ (j & 1 ? ODD : 0)) + 32 * KVA_STEP * 2 * j);
+                r.o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), p[k].f, r.o[j], 0, 0, 0);
+            }
+        if (flags & 0x01010101u)
+            odd_values<D>(hc, r, p, t0, s.kv_len);
+        find(i + 3);
         buf ^= BUF;
-        if (i + 1 < i1)
-            stage(i + 1, buf);
         __syncthreads();
     }
 
@@ -1097,12 +1134,12 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
             q.lse[(s.row + token) * q.heads + head] = top == KVA_NEG ? KVA_NEG : (top + __log2f(l)) * LN2;
         return;
     }
-    const int64_t at = (((int64_t)u * c.kv_heads + h) * plan.splits + blockIdx.y) * KVA_TILE + wave * 32 + col;
+    const int64_t part = (((int64_t)u * c.kv_heads + h) * plan.splits + blockIdx.y) * KVA_TILE + wave * 32 + col;
     if (half == 0)
-        ((float2 *)(plan.ws + plan.off_ml))[at] = make_float2(top, l);
+        ((float2 *)(plan.ws + plan.off_ml))[part] = make_float2(top, l);
     if (i0 == i1)
         return;  // (its sums are not read)
-    float *acc = (float *)(plan.ws + plan.off_acc) + at * D;
+    float *acc = (float *)(plan.ws + plan.off_acc) + part * D;
 #pragma unroll
     for (int j = 0; j < D / 32; j++)
 #pragma unroll

@@ -27,6 +27,7 @@
 #include "mx_kv_device.h"
 
 #include <algorithm>
+#include <atomic>
 
 namespace mx {
 
@@ -37,6 +38,7 @@ typedef float f32x16_t __attribute__((ext_vector_type(16)));
 constexpr int KVA_THREADS = 256;
 constexpr int KVA_CHUNK = 128;      // positions of a piece of work, 32 a wave
 constexpr int KVA_FEW = 64;         // rows of a sequence and head that the few-row kernel takes
+constexpr int64_t KVA_WHOLE = 1024; // positions a sequence can have where items are not cut
 constexpr int KVA_TILE = 128;       // rows of a workgroup of the other
 constexpr int KVA_STEP = 64;        // positions of its steps
 constexpr float KVA_SLACK = 8.0f;   // log2 of what a weight may exceed 1 by
@@ -52,6 +54,7 @@ struct KvPlan {
     char *ws;          // see KvSpace
     int64_t off_first; // byte offsets in ws
     int64_t off_ml, off_acc;
+    int32_t whole;     // nonzero: items of the few-row kernel are not cut
     int32_t few;       // rows up to which a sequence is the few-row kernel's
     int32_t groups;    // workgroups of the few-row kernel
     int32_t splits;    // ranges of positions of the other
@@ -446,22 +449,24 @@ __device__ __forceinline__ void masked_step(RowState<D, NT> &r, Codes<D> &t, int
     }
 }
 
-// Work of a sequence on the line: chunks of an item, and items.
+// Work of a sequence on the line: an item (a head and a tile of rows) has `chunks` chunks and takes `cut` places, one a
+// chunk, or one in all where items stay whole.
 struct SeqWork {
-    int32_t chunks, tiles;  // tiles of 16 NT rows
-    int64_t all;            // chunks * tiles * kv_heads
+    int32_t chunks, cut, tiles;  // tiles of 16 NT rows
+    int64_t all;                 // cut * tiles * kv_heads
 };
 
 template <int NT>
-__device__ __forceinline__ SeqWork seq_work(const KvView &c, const KvQueries &q, const SeqRows &s, int32_t few)
+__device__ __forceinline__ SeqWork seq_work(const KvView &c, const KvQueries &q, const SeqRows &s, const KvPlan &plan)
 {
-    SeqWork w{0, 0, 0};
+    SeqWork w{0, 0, 0, 0};
     const int64_t rows = s.n * q.group;
-    if (rows < 1 || rows > few)
+    if (rows < 1 || rows > plan.few)
         return w;
     w.tiles = (int32_t)((rows + 16 * NT - 1) / (16 * NT));
     w.chunks = max((s.kv_len - first_seen(q, s) + KVA_CHUNK - 1) / KVA_CHUNK, 1);  // (an item of none still writes its zeros)
-    w.all = (int64_t)w.chunks * w.tiles * c.kv_heads;
+    w.cut = plan.whole ? 1 : w.chunks;
+    w.all = (int64_t)w.cut * w.tiles * c.kv_heads;
     return w;
 }
 
@@ -503,7 +508,12 @@ __device__ __forceinline__ void store_out(const KvQueries &q, int64_t row, int32
 template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_rows_kernel(KvView c, KvQueries q, KvPlan plan)
 {
     __shared__ Join<D> lds;
-    __shared__ int64_t lds_sum[4], lds_at[2];
+    __shared__ int64_t lds_sum[4];
+    __shared__ struct {
+        int32_t b;
+        int64_t start;
+        SeqRows rows;
+    } lds_found;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int g = lane >> 4, col = lane & 15;
     const float c2 = fmaxf(q.scale * LOG2E, KVA_LEAST);
@@ -511,14 +521,19 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_ro
 
     // the line's length, and where this workgroup's piece starts
     int64_t all = 0, here = 0, mine = 0;
+    SeqRows own{};
     for (int b0 = 0; b0 < c.batch; b0 += KVA_THREADS) {
         const int b = b0 + tid;
-        const int64_t w = b < c.batch ? seq_work<NT>(c, q, seq_rows(c, b), plan.few).all : 0;
+        SeqRows rows{};
+        if (b < c.batch)
+            rows = seq_rows(c, b);
+        const int64_t w = seq_work<NT>(c, q, rows, plan).all;
         int64_t sum;
         const int64_t upto = scan_sum(w, sum, lds_sum);
         if (b0 == 0) {
             here = upto;
             mine = w;
+            own = rows;
         }
         if (blockIdx.x == 0 && b < c.batch)
             first[b] = all + upto - w;
@@ -536,26 +551,30 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_ro
         int64_t sum = 0;
         if (b0 > 0) {
             const int b = b0 + tid;
-            mine = b < c.batch ? seq_work<NT>(c, q, seq_rows(c, b), plan.few).all : 0;
+            own = SeqRows{};
+            if (b < c.batch)
+                own = seq_rows(c, b);
+            mine = seq_work<NT>(c, q, own, plan).all;
             here = scan_sum(mine, sum, lds_sum);
         }
-        if (at >= before + here - mine && at < before + here) {
-            lds_at[0] = b0 + tid;
-            lds_at[1] = before + here - mine;
+        const bool found = at >= before + here - mine && at < before + here;
+        if (found) {
+            lds_found.b = b0 + tid;
+            lds_found.start = before + here - mine;
+            lds_found.rows = own;
         }
-        // (only the first 256 sequences' sum is not at hand)
-        if (__syncthreads_or(at >= before + here - mine && at < before + here))
+        if (__syncthreads_or(found))
             break;
-        if (b0 == 0)
+        if (b0 == 0)  // (only the first sequences' sum is not at hand)
             here = scan_sum(mine, sum, lds_sum);
         before += sum;
         if (b0 + KVA_THREADS >= c.batch)
             return;
     }
-    int b = uniform((int32_t)lds_at[0]);
-    int64_t start = uniform(lds_at[1]);
-    SeqRows s = uniform(seq_rows(c, b));
-    SeqWork w = seq_work<NT>(c, q, s, plan.few);
+    int b = uniform(lds_found.b);
+    int64_t start = uniform(lds_found.start);
+    SeqRows s = uniform(lds_found.rows);
+    SeqWork w = seq_work<NT>(c, q, s, plan);
     bool head_piece = true;
 
     while (at < end) {
@@ -564,12 +583,12 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_ro
             if (++b >= c.batch)
                 return;
             s = uniform(seq_rows(c, b));
-            w = seq_work<NT>(c, q, s, plan.few);
+            w = seq_work<NT>(c, q, s, plan);
         }
         const int64_t off = at - start;
-        const int32_t item = uniform((int32_t)(off / w.chunks));
-        const int32_t c0 = uniform((int32_t)(off - (int64_t)item * w.chunks));
-        const int32_t c1 = uniform((int32_t)min((int64_t)w.chunks, c0 + (end - at)));
+        const int32_t item = uniform((int32_t)(off / w.cut));
+        const int32_t from = (int32_t)(off - (int64_t)item * w.cut), upto = (int32_t)min((int64_t)w.cut, from + (end - at));
+        const int32_t c0 = uniform(plan.whole ? 0 : from), c1 = uniform(plan.whole ? w.chunks : upto);
         const int32_t h = item / w.tiles, tile = item - h * w.tiles;
         const int32_t rows = (int32_t)s.n * q.group;
 
@@ -715,7 +734,7 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_ro
             }
             __syncthreads();
         }
-        at += c1 - c0;
+        at += upto - from;
         head_piece = false;
     }
 }
@@ -793,7 +812,7 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS) void kv_join_
     const int32_t b = blockIdx.x / c.kv_heads, h = blockIdx.x - b * c.kv_heads;
     const int32_t row = blockIdx.y;
     const SeqRows s = seq_rows(c, b);
-    const SeqWork w = seq_work<NT>(c, q, s, plan.few);
+    const SeqWork w = seq_work<NT>(c, q, s, plan);
     if (!w.all || row >= s.n * q.group)
         return;
     const int64_t *first = (const int64_t *)(plan.ws + plan.off_first);
@@ -1169,9 +1188,16 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS) void kv_tiles_join_ke
 
 static int compute_units()
 {
+    static std::atomic<int> known[64];  // by device; a property of it, asked for once
     int dev = 0, n = 0;
-    if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 1)
+    if (hipGetDevice(&dev) != hipSuccess)
         return 256;
+    if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0)
+        return n;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 1)
+        return 256;
+    if (dev >= 0 && dev < 64)
+        known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
@@ -1194,7 +1220,7 @@ static KvSpace space_of(int64_t tokens, int64_t batch, int64_t q_heads, int64_t 
     s.plan.few = s.tiles ? 32 : KVA_FEW;
     s.nt = most <= 16 ? 1 : 2;
     s.rows_max = (int32_t)std::min<int64_t>(most, s.plan.few);
-    s.plan.groups = (int32_t)(cus * (s.nt == 1 ? 4 : 2));
+    s.plan.groups = (int32_t)(cus * 2);  // (as many as run at once)
     s.plan.splits = 1;
     s.plan.tiles = s.tiles ? (int32_t)(tokens * group / KVA_TILE + batch) : 0;
     if (s.tiles) {
@@ -1231,13 +1257,17 @@ template <int D> static hipError_t launch(const KvView &c, const KvQueries &q, K
     const int64_t chunks = ((int64_t)c.max_pages << c.page_shift) / KVA_CHUNK + 2;
     const int64_t line = chunks * c.batch * c.kv_heads * ((s.rows_max + 16 * s.nt - 1) / (16 * s.nt));
     s.plan.groups = (int32_t)std::min<int64_t>(s.plan.groups, line);
+    // a cache of few positions: whole items save the join's launch (one sequence of 701, 32 heads over 8: ... us)
+    s.plan.whole = ((int64_t)c.max_pages << c.page_shift) <= KVA_WHOLE;
     const dim3 join((unsigned)(c.batch * c.kv_heads), (unsigned)s.rows_max);
     if (s.nt == 1) {
         hipLaunchKernelGGL((kv_rows_kernel<D, 1>), dim3(s.plan.groups), block, 0, stream, c, q, s.plan);
-        hipLaunchKernelGGL((kv_join_kernel<D, 1>), join, block, 0, stream, c, q, s.plan);
+        if (!s.plan.whole)
+            hipLaunchKernelGGL((kv_join_kernel<D, 1>), join, block, 0, stream, c, q, s.plan);
     } else {
         hipLaunchKernelGGL((kv_rows_kernel<D, 2>), dim3(s.plan.groups), block, 0, stream, c, q, s.plan);
-        hipLaunchKernelGGL((kv_join_kernel<D, 2>), join, block, 0, stream, c, q, s.plan);
+        if (!s.plan.whole)
+            hipLaunchKernelGGL((kv_join_kernel<D, 2>), join, block, 0, stream, c, q, s.plan);
     }
     return hipGetLastError();
 }

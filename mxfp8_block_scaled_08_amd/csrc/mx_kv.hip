@@ -18,6 +18,8 @@
 // first, since n rows touch at most floor(n / 16) + 2 blocks; units left over return.
 #include "mx_kv_device.h"
 
+#include <algorithm>
+
 namespace mx {
 
 constexpr int KV_THREADS = 256;
@@ -70,7 +72,16 @@ __device__ __forceinline__ uint32_t one_nan(uint32_t u)
     return u ^ (((u & 0x7F7F7F7Fu) + 0x01010101u) & u & 0x80808080u);
 }
 
-// Eight FP32 -> eight E4M3 codes at the scale; none exceeds 448 times it, NaN gives 0x7F.
+// Four BF16 (two words) -> four E4M3 codes at the scale; none exceeds 448 times it.
+__device__ __forceinline__ uint32_t e4m3_x4(uint32_t w0, uint32_t w1, float scale)
+{
+    i16x2_t r = {0, 0};
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, w0), scale, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, w1), scale, true);
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+// Eight FP32 likewise; NaN gives one of the two NaN codes.
 __device__ __forceinline__ uint2 e4m3_x8(const float *v, float scale)
 {
     i16x2_t a = {0, 0}, b = {0, 0};
@@ -78,7 +89,7 @@ __device__ __forceinline__ uint2 e4m3_x8(const float *v, float scale)
     a = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(a, v[2], v[3], scale, true);
     b = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(b, v[4], v[5], scale, false);
     b = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(b, v[6], v[7], scale, true);
-    return make_uint2(one_nan(__builtin_bit_cast(uint32_t, a)), one_nan(__builtin_bit_cast(uint32_t, b)));
+    return make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
 }
 
 __device__ __forceinline__ void f32_x8(uint2 q, float scale, float *v)
@@ -97,7 +108,42 @@ __device__ __forceinline__ int2 chunks_of(int u, int rot, bool interleaved)
     return split ? make_int2(8 * u, 8 * u + rot / 2) : make_int2(16 * u, 16 * u + 8);
 }
 
-template <int D> __global__ __launch_bounds__(KV_THREADS) void kv_append_kernel(KvView c, KvNew n)
+// Place of pair p's sine and cosine among those of the block's position t.  Lanes read the pairs 8 apart of rows half
+// apart, all in two of LDS' sixteen 16-byte banks: the swizzle spreads sixteen lanes over all of them (15 k rows of 4
+// heads 35 -> ... us).
+__device__ __forceinline__ int angle_at(int t, int p) { return p ^ ((p >> 4 & 1) | (t & 3) << 1); }
+
+// A plane's 16 rows in a wave: two chunks of 8 elements for each of the lane's units, as they come from memory.
+template <int D> struct Plane {
+    uint4 w[D / 64][2];
+};
+
+// The scale's code of a block whose new values need c_new: the older positions' codes are rounded anew where it grows.
+template <int D>
+__device__ __forceinline__ uint32_t settle_scale(const KvUnit &u, uint32_t code, uint8_t *sp, uint8_t *cell)
+{
+    if (u.lo == 0)
+        return code;
+    const int q = threadIdx.x & 3, t = (threadIdx.x & 63) >> 2;
+    const uint32_t old = *sp;
+    if (code <= old)
+        return old;
+    if (t < u.lo) {
+#pragma unroll
+        for (int k = 0; k < D / 64; k++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                uint2 *p = reinterpret_cast<uint2 *>(cell + 16 * (q + 4 * k) + 8 * e);
+                float w[8];
+                f32_x8(*p, cvt_scale(old), w);
+                const uint2 x = e4m3_x8(w, cvt_scale(code));
+                *p = make_uint2(one_nan(x.x), one_nan(x.y));
+            }
+    }
+    return code;
+}
+
+template <int D> __global__ __launch_bounds__(KV_THREADS, 4) void kv_append_kernel(KvView c, KvNew n, Div pairs)
 {
     constexpr int UNITS = D / 64;  // units of 16 elements a lane
     __shared__ double2 lds_cs[KV_BLOCK * (D / 2)];
@@ -110,91 +156,133 @@ template <int D> __global__ __launch_bounds__(KV_THREADS) void kv_append_kernel(
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int q = lane & 3, t = lane >> 2;
     const int half = n.freqs ? n.rot / 2 : 0;
+    const bool live = t >= u.lo && t < u.hi;
+    const int32_t slot = (u.blk & ((1 << (c.page_shift - 4)) - 1)) * KV_BLOCK;
+    // planes: the keys of every head, then the values (so that a workgroup's waves share the rotations evenly)
+    const int planes = 2 * c.kv_heads, step = gridDim.y * 4;
+    auto fetch = [&](int pl, Plane<D> &x) {
+        const bool is_v = pl >= c.kv_heads;
+        const int h = is_v ? pl - c.kv_heads : pl;
+        const uint16_t *p = is_v ? n.v + (u.row + t) * n.ld_vt + h * n.ld_vh : n.k + (u.row + t) * n.ld_kt + h * n.ld_kh;
+#pragma unroll
+        for (int k = 0; k < UNITS; k++) {
+            const int2 at = chunks_of(q + 4 * k, is_v ? 0 : 2 * half, n.interleaved);
+            x.w[k][0] = x.w[k][1] = make_uint4(0, 0, 0, 0);
+            if (live) {
+                x.w[k][0] = *reinterpret_cast<const uint4 *>(p + at.x);
+                x.w[k][1] = *reinterpret_cast<const uint4 *>(p + at.y);
+            }
+        }
+    };
+    int pl = blockIdx.y * 4 + wave;
+    Plane<D> now, next;
+    if (pl < planes)
+        fetch(pl, now);
     if (half) {
         const int first = u.lo * half, last = u.hi * half;
         for (int i = first + (int)threadIdx.x; i < last; i += KV_THREADS) {
-            const int p = i / half;
+            const int p = (int)pairs((uint32_t)i);
             double sn, cs;
             sincos_turns(turns(u.blk * KV_BLOCK + p, n.freqs[i - p * half]), sn, cs);
-            lds_cs[i] = make_double2(cs * n.amplitude, sn * n.amplitude);
+            lds_cs[p * half + angle_at(p, i - p * half)] = make_double2(cs * n.amplitude, sn * n.amplitude);
         }
         __syncthreads();
     }
-    const bool live = t >= u.lo && t < u.hi;
-    const int32_t slot = (u.blk & ((1 << (c.page_shift - 4)) - 1)) * KV_BLOCK;
-    const int planes = 2 * c.kv_heads;
-    for (int pl = blockIdx.y * 4 + wave; pl < planes; pl += gridDim.y * 4) {
-        const int h = pl >> 1;
-        const bool is_v = pl & 1;
-        const uint16_t *x = is_v ? n.v + (u.row + t) * n.ld_vt + h * n.ld_vh
-                                 : n.k + (u.row + t) * n.ld_kt + h * n.ld_kh;
+    for (; pl < planes; pl += step, now = next) {
+        if (pl + step < planes)
+            fetch(pl + step, next);
+        const bool is_v = pl >= c.kv_heads;
+        const int h = is_v ? pl - c.kv_heads : pl;
         const int rot = is_v ? 0 : 2 * half;
-        float v[UNITS][16];
-        uint32_t top = 0;
-#pragma unroll
-        for (int k = 0; k < UNITS; k++) {
-            const int un = q + 4 * k;
-            const int2 at = chunks_of(un, rot, n.interleaved);
-            uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-            if (live) {
-                w0 = *reinterpret_cast<const uint4 *>(x + at.x);
-                w1 = *reinterpret_cast<const uint4 *>(x + at.y);
-            }
-            unpack_bf16x8(w0, v[k]);
-            unpack_bf16x8(w1, v[k] + 8);
-            if (live && un < rot / 16) {
-                const double2 *cs = lds_cs + t * half + 8 * un;
-                auto turn = [&](float &a, float &b, double2 r) {
-                    const double p = a, s = b;
-                    a = (float)(p * r.x - s * r.y);
-                    b = (float)(s * r.x + p * r.y);
-                };
-                if (n.interleaved) {
-#pragma unroll
-                    for (int j = 0; j < 8; j++)
-                        turn(v[k][2 * j], v[k][2 * j + 1], cs[j]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; j++)
-                        turn(v[k][j], v[k][j + 8], cs[j]);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 16; j++) {
-                const uint32_t m = __builtin_bit_cast(uint32_t, v[k][j]) & 0x7FFFFFFFu;
-                top = max(top, m < 0x7F800000u ? m : 0u);
-                v[k][j] = m < 0x7F800000u ? v[k][j] : __builtin_nanf("");
-            }
-        }
-        uint32_t code = kv_scale_code(wave_max(top));
         uint8_t *sp = (is_v ? c.v_scale : c.k_scale) +
                       (((int64_t)page * c.kv_heads + h) << (c.page_shift - 4)) + (slot >> 4);
         uint8_t *cell = (is_v ? c.v : c.k) + page * c.ld_page + h * c.ld_head + (slot + t) * c.ld_token;
-        if (u.lo > 0) {
-            const uint32_t old = *sp;
-            if (code > old) {
-                // the block's older positions at its new scale
-                if (t < u.lo) {
+        uint32_t code;
+        uint2 out[UNITS][2];
+        // Magnitudes are compared as integers, so that a NaN or an infinity shows in the plane's maximum; only then are
+        // they looked for one by one.
+        uint32_t top = 0;
+        if (rot == 0) {
+            uint32_t m = 0;
 #pragma unroll
-                    for (int k = 0; k < UNITS; k++)
+            for (int k = 0; k < UNITS; k++)
 #pragma unroll
-                        for (int e = 0; e < 2; e++) {
-                            uint2 *p = reinterpret_cast<uint2 *>(cell + 16 * (q + 4 * k) + 8 * e);
-                            float w[8];
-                            f32_x8(*p, cvt_scale(old), w);
-                            *p = e4m3_x8(w, cvt_scale(code));
-                        }
+                for (int e = 0; e < 2; e++) {
+                    const uint4 w = now.w[k][e];
+                    m = pk_max_u16(m, pk_max_u16(pk_max_u16(mag2(w.x), mag2(w.y)), pk_max_u16(mag2(w.z), mag2(w.w))));
                 }
-            } else {
-                code = old;
+            top = wave_max(max(m << 16, m & 0xFFFF0000u));
+            if (top < 0x7F800000u) {
+                code = settle_scale<D>(u, kv_scale_code(top), sp, cell);
+#pragma unroll
+                for (int k = 0; k < UNITS; k++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const uint4 w = now.w[k][e];
+                        out[k][e] = make_uint2(e4m3_x4(w.x, w.y, cvt_scale(code)), e4m3_x4(w.z, w.w, cvt_scale(code)));
+                    }
             }
+        }
+        if (rot != 0 || top >= 0x7F800000u) {
+            float v[UNITS][16];
+            top = 0;
+#pragma unroll
+            for (int k = 0; k < UNITS; k++) {
+                const int un = q + 4 * k;
+                unpack_bf16x8(now.w[k][0], v[k]);
+                unpack_bf16x8(now.w[k][1], v[k] + 8);
+                if (live && un < rot / 16) {
+                    const double2 *cs = lds_cs + t * half;
+                    const auto pair = [&](int j) { return cs[angle_at(t, 8 * un + j)]; };
+                    auto turn = [&](float &a, float &b, double2 r) {
+                        const double p = a, s = b;
+                        a = (float)(p * r.x - s * r.y);
+                        b = (float)(s * r.x + p * r.y);
+                    };
+                    if (n.interleaved) {
+#pragma unroll
+                        for (int j = 0; j < 8; j++)
+                            turn(v[k][2 * j], v[k][2 * j + 1], pair(j));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; j++)
+                            turn(v[k][j], v[k][j + 8], pair(j));
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 16; j++)
+                    top = max(top, __builtin_bit_cast(uint32_t, v[k][j]) << 1);
+            }
+            top = wave_max(top);
+            const bool odd = top >= 0xFF000000u;
+            if (odd) {
+                top = 0;
+#pragma unroll
+                for (int k = 0; k < UNITS; k++)
+#pragma unroll
+                    for (int j = 0; j < 16; j++) {
+                        const uint32_t m = __builtin_bit_cast(uint32_t, v[k][j]) << 1;
+                        top = max(top, m < 0xFF000000u ? m : 0u);
+                        v[k][j] = m < 0xFF000000u ? v[k][j] : __builtin_nanf("");
+                    }
+                top = wave_max(top);
+            }
+            code = settle_scale<D>(u, kv_scale_code(top >> 1), sp, cell);
+#pragma unroll
+            for (int k = 0; k < UNITS; k++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    out[k][e] = e4m3_x8(v[k] + 8 * e, cvt_scale(code));
+                    if (odd)
+                        out[k][e] = make_uint2(one_nan(out[k][e].x), one_nan(out[k][e].y));
+                }
         }
         if (live) {
 #pragma unroll
             for (int k = 0; k < UNITS; k++) {
                 const int2 at = chunks_of(q + 4 * k, rot, n.interleaved);
-                *reinterpret_cast<uint2 *>(cell + at.x) = e4m3_x8(v[k], cvt_scale(code));
-                *reinterpret_cast<uint2 *>(cell + at.y) = e4m3_x8(v[k] + 8, cvt_scale(code));
+                *reinterpret_cast<uint2 *>(cell + at.x) = out[k][0];
+                *reinterpret_cast<uint2 *>(cell + at.y) = out[k][1];
             }
         }
         if (lane == 0)
@@ -216,10 +304,11 @@ hipError_t launch_kv_append(const KvView &c, const KvNew &n, hipStream_t stream)
 {
     const unsigned units = unit_count(c);
     const dim3 grid(units, plane_groups(c, units));
+    const Div pairs((uint32_t)std::max(n.rot / 2, 1));
     if (c.dim == 64)
-        hipLaunchKernelGGL(kv_append_kernel<64>, grid, dim3(KV_THREADS), 0, stream, c, n);
+        hipLaunchKernelGGL(kv_append_kernel<64>, grid, dim3(KV_THREADS), 0, stream, c, n, pairs);
     else
-        hipLaunchKernelGGL(kv_append_kernel<128>, grid, dim3(KV_THREADS), 0, stream, c, n);
+        hipLaunchKernelGGL(kv_append_kernel<128>, grid, dim3(KV_THREADS), 0, stream, c, n, pairs);
     return hipGetLastError();
 }
 

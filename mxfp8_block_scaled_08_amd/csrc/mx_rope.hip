@@ -6,48 +6,52 @@
 // workgroup takes a few tokens with all their heads, forms each token's sines and
 // cosines once (64-bit angle, reduced to a fraction of a turn, 64-bit series; about 30
 // instructions) and keeps them in LDS as FP32 pairs, times the amplitude.
-// A thread takes a unit of 16 elements that is closed under the rotation: chunks of 8
-// from both halves (HALF) or 16 in a row, so that y may be x.
+// A thread takes a unit that is closed under the rotation, so that y may be x: 16 bytes of both halves (HALF), or 16
+// bytes in a row.  Every access is 16 bytes a lane, lanes side by side: streaming stores of less than whole lines cost
+// (FP32 rows of 80 in 32-byte units 14.5 us, so 11).
 #include "mx_kv_device.h"
+
+#include <algorithm>
 
 namespace mx {
 
-constexpr int ROPE_THREADS = 256;
+constexpr uint32_t ROPE_THREADS = 256;
 
 struct RopeGrid {
     int32_t per_block;  // tokens a workgroup
     Div pairs;          // rot / 2
-    Div units;          // units of a row: rot / 16 rotated ones, then chunks of 8 copied
+    Div units;          // units of a row: rotated ones, then copied ones
     Div token_units;    // units of a token
+    uint32_t turned;    // rotated units of a row
 };
 
-template <typename T> struct Chunk;  // 8 elements of a row
+// 16 bytes of a row as FP32.
+template <typename T> struct Chunk;
 template <> struct Chunk<uint16_t> {
-    static __device__ __forceinline__ void load(const uint16_t *p, float *v)
-    {
-        unpack_bf16x8(*reinterpret_cast<const uint4 *>(p), v);
-    }
-    static __device__ __forceinline__ void store(uint16_t *p, const float *v)
-    {
-        *reinterpret_cast<uint4 *>(p) = pack_bf16x8(v);
-    }
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void load(const uint16_t *p, float (&v)[N]) { unpack_bf16x8(ld_stream(p), v); }
+    static __device__ __forceinline__ void store(uint16_t *p, const float (&v)[N]) { st_stream(p, pack_bf16x8(v)); }
 };
 template <> struct Chunk<float> {
-    static __device__ __forceinline__ void load(const float *p, float *v)
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void load(const float *p, float (&v)[N])
     {
-        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        const uint4 w = ld_stream(p);
+        const uint32_t a = w.x, b = w.y, c = w.z, d = w.w;
+        v[0] = __builtin_bit_cast(float, a), v[1] = __builtin_bit_cast(float, b);
+        v[2] = __builtin_bit_cast(float, c), v[3] = __builtin_bit_cast(float, d);
     }
-    static __device__ __forceinline__ void store(float *p, const float *v)
+    static __device__ __forceinline__ void store(float *p, const float (&v)[N])
     {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        st_stream(p, make_uint4(__builtin_bit_cast(uint32_t, v[0]), __builtin_bit_cast(uint32_t, v[1]),
+                                __builtin_bit_cast(uint32_t, v[2]), __builtin_bit_cast(uint32_t, v[3])));
     }
 };
 
 template <typename T, bool INTERLEAVED>
 __global__ __launch_bounds__(ROPE_THREADS) void rope_kernel(RopeArgs a, RopeGrid g)
 {
+    constexpr int N = Chunk<T>::N;
     extern __shared__ float2 lds_cs[];  // [token][pair] (cos, sin)
     const int64_t t0 = (int64_t)blockIdx.x * g.per_block;
     const uint32_t nt = (uint32_t)min((int64_t)g.per_block, a.tokens - t0);
@@ -64,35 +68,46 @@ __global__ __launch_bounds__(ROPE_THREADS) void rope_kernel(RopeArgs a, RopeGrid
         const uint32_t h = g.units(hu), u = hu - h * g.units.d;
         const T *x = (const T *)a.x + (t0 + t) * a.ld_xt + h * a.ld_xh;
         T *y = (T *)a.y + (t0 + t) * a.ld_yt + h * a.ld_yh;
-        if (u >= half / 8) {
-            const uint32_t d = a.rot + (u - half / 8) * 8;
-            float v[8];
+        const float2 *cs = lds_cs + t * half + (INTERLEAVED ? N / 2 : N) * u;
+        float v[N], w[N];
+        if (u >= g.turned) {
+            const uint32_t d = a.rot + (u - g.turned) * N;
             Chunk<T>::load(x + d, v);
             Chunk<T>::store(y + d, v);
-            continue;
-        }
-        const uint32_t d0 = INTERLEAVED ? 16 * u : 8 * u, d1 = d0 + (INTERLEAVED ? 8 : half);
-        const float2 *cs = lds_cs + t * half + 8 * u;
-        float v[16], w[16];
-        Chunk<T>::load(x + d0, v);
-        Chunk<T>::load(x + d1, v + 8);
+        } else if (INTERLEAVED) {
+            Chunk<T>::load(x + N * u, v);
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const int p = INTERLEAVED ? 2 * j : j, q = INTERLEAVED ? 2 * j + 1 : j + 8;
-            const float2 r = cs[j];
-            w[p] = v[p] * r.x - v[q] * r.y;
-            w[q] = v[q] * r.x + v[p] * r.y;
+            for (int j = 0; j < N; j += 2) {
+                const float2 r = cs[j / 2];
+                w[j] = v[j] * r.x - v[j + 1] * r.y;
+                w[j + 1] = v[j + 1] * r.x + v[j] * r.y;
+            }
+            Chunk<T>::store(y + N * u, w);
+        } else {
+            float z[N];
+            Chunk<T>::load(x + N * u, v);
+            Chunk<T>::load(x + N * u + half, w);
+#pragma unroll
+            for (int j = 0; j < N; j++) {
+                const float2 r = cs[j];
+                z[j] = v[j] * r.x - w[j] * r.y;
+                w[j] = w[j] * r.x + v[j] * r.y;
+            }
+            Chunk<T>::store(y + N * u, z);
+            Chunk<T>::store(y + N * u + half, w);
         }
-        Chunk<T>::store(y + d0, w);
-        Chunk<T>::store(y + d1, w + 8);
     }
 }
 
 hipError_t launch_rope(const RopeArgs &a, int dtype, bool interleaved, hipStream_t stream)
 {
-    const uint32_t half = a.rot / 2, units = a.rot / 16 + (a.dim - a.rot) / 8;
-    const int32_t per = a.tokens >= 4096 ? 4 : 1;
-    const RopeGrid g{per, Div(half), Div(units), Div(units * (uint32_t)a.heads)};
+    const uint32_t half = a.rot / 2, n = dtype == 0 ? 8 : 4;
+    const uint32_t turned = interleaved ? a.rot / n : half / n, units = turned + (a.dim - a.rot) / n;
+    // a unit for every thread, but no more: 20480 x 32 heads of 128 forward and back took 124 us with four units a
+    // thread, 117 with one, 107 with streaming accesses too
+    const uint32_t token_units = units * (uint32_t)a.heads;
+    const int32_t per = (int32_t)std::min(std::max(ROPE_THREADS / token_units, 1u), 8u);
+    const RopeGrid g{per, Div(half), Div(units), Div(token_units), turned};
     const dim3 grid((unsigned)((a.tokens + per - 1) / per));
     const size_t lds = (size_t)per * half * sizeof(float2);
     if (dtype == 0 && interleaved)

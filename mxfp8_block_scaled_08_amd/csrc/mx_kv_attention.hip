@@ -73,7 +73,7 @@ __device__ __forceinline__ Seen seen_by(const KvQueries &q, const SeqRows &s, in
     if (q.causal) {
         r.hi = (int32_t)min(p, (int64_t)r.hi);
         if (q.window)
-            r.lo = (int32_t)max(p - q.window + 1, (int64_t)0);
+            r.lo = (int32_t)min(max(p - q.window + 1, (int64_t)0), (int64_t)s.kv_len);
     }
     return r;
 }
@@ -81,7 +81,7 @@ __device__ __forceinline__ Seen seen_by(const KvQueries &q, const SeqRows &s, in
 // First position that any row of the sequence sees, down to a whole block.
 __device__ __forceinline__ int32_t first_seen(const KvQueries &q, const SeqRows &s)
 {
-    return q.window ? (int32_t)max(s.pos - q.window + 1, (int64_t)0) & ~15 : 0;
+    return q.window ? (int32_t)min(max(s.pos - q.window + 1, (int64_t)0), (int64_t)s.kv_len) & ~15 : 0;
 }
 
 __device__ __forceinline__ int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }

@@ -20,7 +20,7 @@ def _run(mx, B, q_heads, std=1.0, scale=None, causal=True, window=0, max_new=0, 
     assert (out[n:] == 7.0).all() and (lse[n:] == 7.0).all()  # rows behind the last sequence
     if want is None:
         want = B.ref.attention(q.double().numpy()[:n], B.starts, B.lens, B.dim ** -0.5 if scale is None else scale, causal, window)
-    check_attention(out[:n], lse[:n], want, B.dim, int(max(B.lens.max(), 1)))
+    check_attention(out[:n], lse[:n], want, B.dim, int(min(max(B.lens.max(), 1), B.table.shape[1] * B.page)))
     return out[:n], lse[:n], want
 
 
@@ -225,6 +225,16 @@ def test_many_sequences_bad_starts_and_small_max_new(gpu_lib):
         gpu_lib.mx_kv_attention(q, kv, scale, table, lens, bad, **kw)
         gpu_lib.mx_kv_attention(q, kv, scale, table, lens * 1000000, starts, **kw)
     torch.cuda.synchronize()
+
+
+def test_lengths_past_the_table(gpu_lib):
+    """kv_lens far beyond what the table holds: positions from there on are not stored, windows there are empty."""
+    B = Batch(39, [2, 70, 1], [30, 0, 5], 1, 64, 16)
+    cap = B.table.shape[1] * 16
+    for lens in ([2 ** 31 - 1, cap + 1, 2 ** 31 - 3], [cap, cap + 40, cap + 2]):
+        B.lens = np.array(lens, np.int32)
+        for kw in (dict(window=1), dict(window=33), dict(window=2 ** 40), dict(causal=False), dict(max_new=70)):
+            _run(gpu_lib, B, 2, **kw)
 
 
 def test_binding_refusals(gpu_lib):

@@ -19,7 +19,8 @@ def rope(x, positions, freqs, style="half", amplitude=1.0, inverse=False):
     n = len(freqs)
     y = x.copy()
     i0, i1 = (slice(0, n), slice(n, 2 * n)) if style == "half" else (slice(0, 2 * n, 2), slice(1, 2 * n, 2))
-    y[..., i0], y[..., i1] = x[..., i0] * c - x[..., i1] * s, x[..., i1] * c + x[..., i0] * s
+    with np.errstate(invalid="ignore"):
+        y[..., i0], y[..., i1] = x[..., i0] * c - x[..., i1] * s, x[..., i1] * c + x[..., i0] * s
     return y
 
 

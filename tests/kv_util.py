@@ -13,17 +13,17 @@ def bf16(rng, *shape, std=1.0):
 
 class Batch:
     """Sequences of new[b] rows behind ctx[b] positions, pages dealt out of order, the rest
-    of the table -1.  Cells that no position holds are filled with any bytes, NaN codes and
+    of the table -1 (room: positions that it has places for at least).  Cells that no position holds are filled with any bytes, NaN codes and
     scales among them."""
 
-    def __init__(self, seed, new, ctx, heads, dim, page, layout="hnd", spare=2, behind=0, filled=True, std=1.0):
+    def __init__(self, seed, new, ctx, heads, dim, page, layout="hnd", spare=2, behind=0, filled=True, std=1.0, room=0):
         self.rng = rng = np.random.default_rng(seed)
         self.new, self.ctx, self.heads, self.dim, self.page = list(new), list(ctx), heads, dim, page
         lens = [n + c for n, c in zip(new, ctx)]
         need = [max(0, -(-n // page)) for n in lens]
         pages = sum(need) + spare
         order = rng.permutation(pages)
-        self.table = np.full((len(new), max(need + [1]) + 1), -1, np.int32)
+        self.table = np.full((len(new), max(max(need + [1]) + 1, -(-room // page))), -1, np.int32)
         at = 0
         for b, n in enumerate(need):
             self.table[b, :n] = order[at:at + n]

@@ -41,15 +41,18 @@ STEPS = [
 ]
 
 
+# a table of up to 1024 positions keeps a sequence's work together, a larger one lets it be cut over the chip
+ROOM = [0, 1500]
+
+
+@pytest.mark.parametrize("room", ROOM)
 @pytest.mark.parametrize("new,ctx,kv_heads,q_heads,dim,page,layout", STEPS)
-def test_few_rows(gpu_lib, new, ctx, kv_heads, q_heads, dim, page, layout):
-    B = Batch(sum(ctx) + dim + q_heads, new, ctx, kv_heads, dim, page, layout, behind=3)
-    a = _run(gpu_lib, B, q_heads, max_new=max(new))
-    q = None
+def test_few_rows(gpu_lib, new, ctx, kv_heads, q_heads, dim, page, layout, room):
+    B = Batch(sum(ctx) + dim + q_heads, new, ctx, kv_heads, dim, page, layout, behind=3, room=room)
+    _run(gpu_lib, B, q_heads, max_new=max(new))
     _run(gpu_lib, B, q_heads, std=4.0, max_new=max(new) + 2)
     _run(gpu_lib, B, q_heads, causal=False, scale=0.3)
     _run(gpu_lib, B, q_heads, window=20, max_new=max(new))
-    assert a is not None and q is None
 
 
 PROMPTS = [
@@ -63,9 +66,10 @@ PROMPTS = [
 ]
 
 
+@pytest.mark.parametrize("room", ROOM)
 @pytest.mark.parametrize("new,ctx,kv_heads,q_heads,dim,page,layout", PROMPTS)
-def test_many_rows(gpu_lib, new, ctx, kv_heads, q_heads, dim, page, layout):
-    B = Batch(sum(ctx) + dim + q_heads, new, ctx, kv_heads, dim, page, layout, behind=2)
+def test_many_rows(gpu_lib, new, ctx, kv_heads, q_heads, dim, page, layout, room):
+    B = Batch(sum(ctx) + dim + q_heads, new, ctx, kv_heads, dim, page, layout, behind=2, room=room)
     _run(gpu_lib, B, q_heads, max_new=max(new))
     _run(gpu_lib, B, q_heads, std=4.0)
     _run(gpu_lib, B, q_heads, causal=False, scale=0.2)
@@ -101,8 +105,8 @@ def test_long_rows_split_over_the_chip(gpu_lib):
 
 def test_rows_that_see_nothing(gpu_lib):
     """Sequences without positions, rows at positions below 0, pages that are not there."""
-    for rows in (2, 90):
-        B = Batch(31, [rows, rows, 3, rows], [0, 30, 0, 20], 2, 64, 16, behind=1)
+    for rows, room in ((2, 0), (90, 0), (2, 1500), (90, 1500)):
+        B = Batch(31, [rows, rows, 3, rows], [0, 30, 0, 20], 2, 64, 16, behind=1, room=room)
         B.lens[0] = 0            # nothing in the cache
         B.lens[2] = 1            # two rows at positions below 0
         B.table[3, :] = -1       # no page at all
@@ -115,11 +119,12 @@ def test_rows_that_see_nothing(gpu_lib):
     assert (out == 0).all() and torch.isneginf(lse).all()
 
 
+@pytest.mark.parametrize("room", ROOM)
 @pytest.mark.parametrize("rows", [1, 5, 70])
-def test_nan_and_infinities_in_masked_places(gpu_lib, rows):
+def test_nan_and_infinities_in_masked_places(gpu_lib, rows, room):
     """A position's NaN reaches the rows that see it, and no other: behind the last position, behind
     a causal row, before a window, in a missing page."""
-    B = Batch(32 + rows, [rows, rows], [33, 0], 2, 64, 16, behind=1)
+    B = Batch(32 + rows, [rows, rows], [33, 0], 2, 64, 16, behind=1, room=room)
     kv, sc = B.ref.kv, B.ref.scale
 
     def cell(b, p):
@@ -186,8 +191,9 @@ def test_strided_queries_and_outputs(gpu_lib):
 
 
 def test_same_call_same_bytes(gpu_lib):
-    for new, ctx in (([1] * 9, [700, 3, 64, 1500, 0, 99, 130, 400, 31]), ([150, 20], [40, 300])):
-        B = Batch(35, new, ctx, 2, 128, 32, filled=False)
+    for new, ctx, room in (([1] * 9, [700, 3, 64, 1500, 0, 99, 130, 400, 31], 0), ([150, 20], [40, 300], 0),
+                           ([150, 3], [40, 300], 1500)):
+        B = Batch(35, new, ctx, 2, 128, 32, filled=False, room=room)
         B.scale.fill_(118)
         B.kv[(B.kv & 127) == 127] = 0x11
         q = bf16(B.rng, B.rows, 8, 128).cuda()
@@ -210,7 +216,7 @@ def test_without_rounding_only_weights_are_lost(gpu_lib):
 def test_many_sequences_bad_starts_and_small_max_new(gpu_lib):
     rng = np.random.default_rng(37)
     new = [int(n) for n in rng.integers(0, 3, 600)]
-    B = Batch(37, new, [int(n) for n in rng.integers(0, 40, 600)], 1, 64, 16, filled=False)
+    B = Batch(37, new, [int(n) for n in rng.integers(0, 40, 600)], 1, 64, 16, filled=False, room=1500)
     B.ref.scale[:] = 120
     B.ref.kv[(B.ref.kv & 127) == 127] = 0x21
     B.kv.copy_(torch.from_numpy(B.ref.kv))
@@ -229,7 +235,7 @@ def test_many_sequences_bad_starts_and_small_max_new(gpu_lib):
 
 def test_lengths_past_the_table(gpu_lib):
     """kv_lens far beyond what the table holds: positions from there on are not stored, windows there are empty."""
-    B = Batch(39, [2, 70, 1], [30, 0, 5], 1, 64, 16)
+    B = Batch(39, [2, 70, 1], [30, 0, 5], 1, 64, 16, room=1100)
     cap = B.table.shape[1] * 16
     for lens in ([2 ** 31 - 1, cap + 1, 2 ** 31 - 3], [cap, cap + 40, cap + 2]):
         B.lens = np.array(lens, np.int32)

@@ -91,12 +91,12 @@ def test_prompt_then_tokens(gpu_lib):
         _check(mx, T, B, _pos(B))
 
 
-@pytest.mark.parametrize("max_new", [1, 0])
-def test_a_captured_step_follows_growing_sequences(gpu_lib, max_new):
+@pytest.mark.parametrize("max_new,room", [(1, 0), (0, 0), (1, 1500), (0, 1500)])
+def test_a_captured_step_follows_growing_sequences(gpu_lib, max_new, room):
     """Captured once; every replay finds longer sequences, other rows, some without a new one (a padded batch)."""
     mx = gpu_lib
-    B = Batch(51 + max_new, [1] * 6, [0, 14, 15, 40, 130, 3], HK, D, 16, spare=8, filled=True)
-    B.table[:, -1] = [p for p in range(B.kv.shape[1]) if p not in B.table][:6]
+    B = Batch(51 + max_new, [1] * 6, [0, 14, 15, 40, 130, 3], HK, D, 16, spare=8, filled=True, room=room)
+    B.table[:, 9] = [p for p in range(B.kv.shape[1]) if p not in B.table][:6]
     B.ref.table = B.table
     S = Step(mx, B, bf16(B.rng, 8, HQ + 2 * HK, D).cuda(), max_new=max_new)
     B.rows = 8
@@ -135,7 +135,7 @@ def test_two_graphs_and_eager_work_share_nothing_but_what_they_are_given(gpu_lib
     mx = gpu_lib
     steps, want, graphs, streams = [], [], [], []
     for i in range(2):
-        B = Batch(60 + i, [1, 40, 3], [300, 0, 61], HK, D, 32, spare=4)
+        B = Batch(60 + i, [1, 40, 3], [300, 0, 61], HK, D, 32, spare=4, room=1500)
         S = Step(mx, B, bf16(B.rng, B.rows, HQ + 2 * HK, D).cuda())
         S.pos.copy_(torch.from_numpy(_pos(B)))
         S.run()
@@ -163,7 +163,7 @@ def test_two_graphs_and_eager_work_share_nothing_but_what_they_are_given(gpu_lib
 def test_streams(gpu_lib):
     """Steps on two streams at once, one given by stream=, equal the same steps one after the other."""
     mx = gpu_lib
-    B = [Batch(70 + i, [1, 1, 70], [200, 5, 33], HK, D, 64) for i in range(2)]
+    B = [Batch(70 + i, [1, 1, 70], [200, 5, 33], HK, D, 64, room=1500) for i in range(2)]
     qkv = [bf16(b.rng, b.rows, HQ + 2 * HK, D).cuda() for b in B]
     S = [Step(mx, b, x) for b, x in zip(B, qkv)]
     for s, b in zip(S, B):

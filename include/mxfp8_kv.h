@@ -130,7 +130,7 @@ typedef struct mx_kv_cache {
  * clamps nothing, so a block that grows never holds a clamped value.
  *   k, v   BF16 [tokens][kv_heads][head_dim], strides ld_kt, ld_kh / ld_vt, ld_vh
  *   freqs  DEVICE double [rot_dim / 2]: keys are rotated (mx_rope's formula, by
- *          their position in the cache) before they are rounded, in 64 bits and once;
+ *          their position in the cache) before they are rounded, in 64 bits and but once (beyond FP32's range: as infinities);
  *          null: as they are (rot_dim, style, amplitude not used)
  * A block may be written by one sequence of a call only (pages that several sequences read,
  * as a shared prefix, are not written).  Deterministic.

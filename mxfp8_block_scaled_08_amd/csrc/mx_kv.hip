@@ -11,8 +11,8 @@
 // K or V), a wave a plane, so that the plane's maximum stays inside a wave.  Lane l holds
 // row l >> 2 of the block and the chunks of 8 elements q, q + 4, .. (in pairs closed
 // under the rotation), q = l & 3.  Sines and cosines of the block's 16 positions are
-// formed once a workgroup, in 64 bits, and the keys are rotated in 64 bits: the codes
-// then are those of the exact rotation but for one rounding to FP32.
+// formed once a workgroup, in 64 bits, and the keys are rotated in 64 bits, so that the
+// rounding to E4M3 is their only one.
 //
 // Units are numbered without knowing the lengths: floor(start / 16) + 2 b is sequence b's
 // first, since n rows touch at most floor(n / 16) + 2 blocks; units left over return.
@@ -112,6 +112,17 @@ __device__ __forceinline__ int2 chunks_of(int u, int rot, bool interleaved)
 // apart, all in two of LDS' sixteen 16-byte banks: the swizzle spreads sixteen lanes over all of them (15 k rows of 4
 // heads 35 -> ... us).
 __device__ __forceinline__ int angle_at(int t, int p) { return p ^ ((p >> 4 & 1) | (t & 3) << 1); }
+
+// A double as FP32 rounded to odd (toward zero, the last bit set where that was not exact): rounded on to E4M3 and compared
+// with 448 times a power of two, it gives what the double would.  Beyond FP32's range: infinite.
+__device__ __forceinline__ float to_odd(double d)
+{
+    const float f = (float)d;
+    const double e = f;
+    const uint32_t b = __builtin_bit_cast(uint32_t, f);
+    const uint32_t odd = (b - (fabs(e) > fabs(d) ? 1u : 0u)) | 1u;
+    return __builtin_bit_cast(float, e != d && (b & 0x7FFFFFFFu) != 0x7F800000u ? odd : b);
+}
 
 // A plane's 16 rows in a wave: two chunks of 8 elements for each of the lane's units, as they come from memory.
 template <int D> struct Plane {
@@ -224,34 +235,36 @@ template <int D> __global__ __launch_bounds__(KV_THREADS, 4) void kv_append_kern
             }
         }
         if (rot != 0 || top >= 0x7F800000u) {
-            float v[UNITS][16];
+            // pairs (a, b): elements j and j + 8 of the unit's chunks, or 2 j and 2 j + 1 of them together
+            const bool by_two = n.interleaved;
+            float v[UNITS][2][8];
             top = 0;
 #pragma unroll
             for (int k = 0; k < UNITS; k++) {
                 const int un = q + 4 * k;
-                unpack_bf16x8(now.w[k][0], v[k]);
-                unpack_bf16x8(now.w[k][1], v[k] + 8);
+                const uint4 w0 = now.w[k][0], w1 = now.w[k][1];
+                const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                if (by_two) {
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        v[k][0][j] = bf16_lo(w[j]), v[k][1][j] = bf16_hi(w[j]);
+                } else {
+                    unpack_bf16x8(w0, v[k][0]);
+                    unpack_bf16x8(w1, v[k][1]);
+                }
                 if (live && un < rot / 16) {
                     const double2 *cs = lds_cs + t * half;
-                    const auto pair = [&](int j) { return cs[angle_at(t, 8 * un + j)]; };
-                    auto turn = [&](float &a, float &b, double2 r) {
-                        const double p = a, s = b;
-                        a = (float)(p * r.x - s * r.y);
-                        b = (float)(s * r.x + p * r.y);
-                    };
-                    if (n.interleaved) {
 #pragma unroll
-                        for (int j = 0; j < 8; j++)
-                            turn(v[k][2 * j], v[k][2 * j + 1], pair(j));
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; j++)
-                            turn(v[k][j], v[k][j + 8], pair(j));
+                    for (int j = 0; j < 8; j++) {
+                        const double2 r = cs[angle_at(t, 8 * un + j)];
+                        const double x = v[k][0][j], y = v[k][1][j];
+                        v[k][0][j] = to_odd(x * r.x - y * r.y);
+                        v[k][1][j] = to_odd(y * r.x + x * r.y);
                     }
                 }
 #pragma unroll
                 for (int j = 0; j < 16; j++)
-                    top = max(top, __builtin_bit_cast(uint32_t, v[k][j]) << 1);
+                    top = max(top, __builtin_bit_cast(uint32_t, v[k][j >> 3][j & 7]) << 1);
             }
             top = wave_max(top);
             const bool odd = top >= 0xFF000000u;
@@ -261,21 +274,33 @@ template <int D> __global__ __launch_bounds__(KV_THREADS, 4) void kv_append_kern
                 for (int k = 0; k < UNITS; k++)
 #pragma unroll
                     for (int j = 0; j < 16; j++) {
-                        const uint32_t m = __builtin_bit_cast(uint32_t, v[k][j]) << 1;
+                        float &f = v[k][j >> 3][j & 7];
+                        const uint32_t m = __builtin_bit_cast(uint32_t, f) << 1;
                         top = max(top, m < 0xFF000000u ? m : 0u);
-                        v[k][j] = m < 0xFF000000u ? v[k][j] : __builtin_nanf("");
+                        f = m < 0xFF000000u ? f : __builtin_nanf("");
                     }
                 top = wave_max(top);
             }
             code = settle_scale<D>(u, kv_scale_code(top >> 1), sp, cell);
+            const float scale = cvt_scale(code);
 #pragma unroll
-            for (int k = 0; k < UNITS; k++)
+            for (int k = 0; k < UNITS; k++) {
+                if (by_two) {
 #pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    out[k][e] = e4m3_x8(v[k] + 8 * e, cvt_scale(code));
-                    if (odd)
-                        out[k][e] = make_uint2(one_nan(out[k][e].x), one_nan(out[k][e].y));
+                    for (int e = 0; e < 2; e++) {
+                        const float *x = v[k][0] + 4 * e, *y = v[k][1] + 4 * e;
+                        const float z[8] = {x[0], y[0], x[1], y[1], x[2], y[2], x[3], y[3]};
+                        out[k][e] = e4m3_x8(z, scale);
+                    }
+                } else {
+                    out[k][0] = e4m3_x8(v[k][0], scale);
+                    out[k][1] = e4m3_x8(v[k][1], scale);
                 }
+                if (odd)
+#pragma unroll
+                    for (int e = 0; e < 2; e++)
+                        out[k][e] = make_uint2(one_nan(out[k][e].x), one_nan(out[k][e].y));
+            }
         }
         if (live) {
 #pragma unroll

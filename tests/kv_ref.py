@@ -76,8 +76,9 @@ class Cache:
                 at = [p % self.page for p, _ in rows]
                 i = [r for _, r in rows]
                 kk = k[i] if freqs is None else rope(k[i], [p for p, _ in rows], freqs, style, amplitude)
+                x = np.stack([kk, v[i]])
                 with np.errstate(over="ignore"):
-                    x = np.stack([kk, v[i]]).astype(np.float32).astype(np.float64)  # one rounding to FP32
+                    x = np.where(np.isinf(x.astype(np.float32)), np.copysign(np.inf, x), x)  # beyond FP32's range
                 s = at[0] // BLOCK
                 off = at[0] % BLOCK
                 for w in range(2):

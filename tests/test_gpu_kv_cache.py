@@ -1,6 +1,6 @@
 """Appending to the paged 8-bit cache and reading it back, against the loops of
 tests/kv_ref.py: codes and scales are whole numbers and must be equal (the
-rotation is formed in 64 bits on both sides and rounded to FP32 once)."""
+rotation is formed in 64 bits on both sides, and E4M3 is its only rounding)."""
 import numpy as np
 import pytest
 import torch
@@ -112,6 +112,18 @@ def test_ties_and_the_top_of_the_range(gpu_lib):
     k = x.to(BF)
     _append(gpu_lib, B, k.cuda(), (-k).cuda())
     assert B.ref.scale[0, B.table[0, 0], 0, 0] == 127 and B.ref.scale[0, B.table[1, 0], 0, 0] == 128
+
+
+def test_rotated_keys_beside_midpoints(gpu_lib):
+    """Rotated by a multiple of a quarter turn to within 2^-50, keys at the midpoints of two codes land just beside them: a
+    rounding to FP32 on the way would make ties of them."""
+    B = Batch(21, [32], [0], 1, 64, 32)
+    mid = torch.from_numpy((ref.E4M3[8:126] + ref.E4M3[9:127]) / 2).float()
+    k = torch.ones(32, 1, 64) * 2.0 ** -9
+    k[:, 0, :32] = mid[torch.randint(0, 118, (32, 32), generator=torch.Generator().manual_seed(2))]
+    k[:, 0, 0] = 448.0
+    f = np.full(32, 2 * np.pi * 2.0 ** -31) * np.arange(32)  # angles of 2^-29 and less
+    _append(gpu_lib, B, k.to(BF).cuda(), k.to(BF).cuda(), f)
 
 
 def test_strided_rows(gpu_lib):

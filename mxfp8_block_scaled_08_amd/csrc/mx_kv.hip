@@ -14,6 +14,12 @@
 // formed once a workgroup, in 64 bits, and the keys are rotated in 64 bits, so that the
 // rounding to E4M3 is their only one.
 //
+// 18 k new rows of 4 heads of 128 (55 MB): 23 us, 2.4 TB/s, 15 us without the rotation; a
+// copy of those bytes takes 11.  What is left is latency: starts, lengths, page, rows and
+// angles each wait for the one before, 5 us for a single row, and 4 workgroups a compute
+// unit (128 registers) leave a short second turn.  5 of them spill (23 us), 6 more so (28);
+// so does fetching a plane ahead of its turn (15 -> 17 without the rotation).
+//
 // Units are numbered without knowing the lengths: floor(start / 16) + 2 b is sequence b's
 // first, since n rows touch at most floor(n / 16) + 2 blocks; units left over return.
 #include "mx_kv_device.h"
@@ -109,8 +115,8 @@ __device__ __forceinline__ int2 chunks_of(int u, int rot, bool interleaved)
 }
 
 // Place of pair p's sine and cosine among those of the block's position t.  Lanes read the pairs 8 apart of rows half
-// apart, all in two of LDS' sixteen 16-byte banks: the swizzle spreads sixteen lanes over all of them (15 k rows of 4
-// heads 35 -> ... us).
+// apart, all in two of LDS' sixteen 16-byte banks: the swizzle spreads sixteen lanes over all of them (18 k rows of 4
+// heads 36 -> 21 us).
 __device__ __forceinline__ int angle_at(int t, int p) { return p ^ ((p >> 4 & 1) | (t & 3) << 1); }
 
 // A double as FP32 rounded to odd (toward zero, the last bit set where that was not exact): rounded on to E4M3 and compared
@@ -140,9 +146,9 @@ __device__ __forceinline__ uint32_t settle_scale(const KvUnit &u, uint32_t code,
     if (code <= old)
         return old;
     if (t < u.lo) {
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < D / 64; k++)
-#pragma unroll
+#pragma unroll 1
             for (int e = 0; e < 2; e++) {
                 uint2 *p = reinterpret_cast<uint2 *>(cell + 16 * (q + 4 * k) + 8 * e);
                 float w[8];
@@ -186,9 +192,9 @@ template <int D> __global__ __launch_bounds__(KV_THREADS, 4) void kv_append_kern
         }
     };
     int pl = blockIdx.y * 4 + wave;
-    Plane<D> now, next;
+    Plane<D> now;
     if (pl < planes)
-        fetch(pl, now);
+        fetch(pl, now);  // the first on its way while the angles are formed
     if (half) {
         const int first = u.lo * half, last = u.hi * half;
         for (int i = first + (int)threadIdx.x; i < last; i += KV_THREADS) {
@@ -199,9 +205,9 @@ template <int D> __global__ __launch_bounds__(KV_THREADS, 4) void kv_append_kern
         }
         __syncthreads();
     }
-    for (; pl < planes; pl += step, now = next) {
-        if (pl + step < planes)
-            fetch(pl + step, next);
+    for (; pl < planes; pl += step) {
+        if (pl >= step)
+            fetch(pl, now);
         const bool is_v = pl >= c.kv_heads;
         const int h = is_v ? pl - c.kv_heads : pl;
         const int rot = is_v ? 0 : 2 * half;
@@ -275,11 +281,11 @@ template <int D> __global__ __launch_bounds__(KV_THREADS, 4) void kv_append_kern
 #pragma unroll
                     for (int j = 0; j < 16; j++) {
                         float &f = v[k][j >> 3][j & 7];
-                        const uint32_t m = __builtin_bit_cast(uint32_t, f) << 1;
-                        top = max(top, m < 0xFF000000u ? m : 0u);
-                        f = m < 0xFF000000u ? f : __builtin_nanf("");
+                        const uint32_t m = __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu;  // not shifted: 32 registers less
+                        top = max(top, m < 0x7F800000u ? m : 0u);
+                        f = m < 0x7F800000u ? f : __builtin_nanf("");
                     }
-                top = wave_max(top);
+                top = wave_max(top) << 1;
             }
             code = settle_scale<D>(u, kv_scale_code(top >> 1), sp, cell);
             const float scale = cvt_scale(code);

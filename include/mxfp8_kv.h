@@ -76,13 +76,15 @@ mx_status mx_rope_frequencies(int64_t rot_dim, double base, int scaling, double 
  *   positions  DEVICE int32 [tokens], any sign
  *   freqs      DEVICE double [rot_dim / 2] (mx_rope_frequencies')
  * The angle is reduced in 64 bits, so far positions lose nothing; products in
- * FP32, rounded once.
- * y may be x itself (same pointer and strides).  Requirements: tokens, heads >= 0;
- * the strides leave the (t, h) rows apart, tokens outside or heads outside; amplitude finite (else
- * MX_ERR_INVALID_ARG); head_dim and rot_dim multiples of 8 and 16, 16 <= rot_dim <=
- * head_dim (else MX_ERR_SHAPE); head_dim <= 512, tokens and heads * head_dim below
- * 2^31 (else MX_ERR_UNSUPPORTED); x, y 16-byte aligned rows, strides included (else
- * MX_ERR_ALIGN); y overlaps nothing unless it is x (else MX_ERR_OVERLAP).
+ * FP32, the result rounded once.
+ * y may be x itself (same pointer and strides).  Requirements: tokens, heads >= 0,
+ * head_dim >= 1, style one of the two, amplitude finite, strides that leave the
+ * (t, h) rows apart, tokens outside or heads outside (else MX_ERR_INVALID_ARG);
+ * head_dim a multiple of 8, rot_dim one of 16 with 16 <= rot_dim <= head_dim (else
+ * MX_ERR_SHAPE); head_dim <= 512, heads <= 65536, tokens < 2^24, strides not
+ * negative and the whole within 2^40 elements (else MX_ERR_UNSUPPORTED); rows of x
+ * and y 16-byte aligned, strides included, positions and freqs to their elements
+ * (else MX_ERR_ALIGN); y overlaps nothing unless it is x (else MX_ERR_OVERLAP).
  */
 mx_status mx_rope(const void *x, int dtype, int64_t tokens, int64_t heads, int64_t head_dim, int64_t ld_xt,
                   int64_t ld_xh, const int32_t *positions, const double *freqs, int64_t rot_dim, int style,
@@ -104,18 +106,21 @@ typedef struct mx_kv_cache {
     int64_t batch;
 } mx_kv_cache;
 /*
- * Requirements of every call with a cache: sizes >= 0, num_pages, max_pages,
- * kv_heads >= 1 (else MX_ERR_INVALID_ARG); head_dim 64 or 128, page_size a power
- * of two in 16..1024, num_pages, kv_heads * page_size and max_pages * page_size below 2^30, batch
- * <= 65536, ld_token below 2^20 (else MX_ERR_UNSUPPORTED); strides that leave the
- * rows of head_dim codes apart (each of the three strides at least the extent of what
- * lies inside it, in one of the six orders; else MX_ERR_INVALID_ARG);
- * k, v and their strides 16-byte aligned, the tables aligned to their elements (else
- * MX_ERR_ALIGN).  The tables are read on the device only.  A page number outside
- * [0, num_pages) holds no positions: nothing is stored there, reads give zeros, the
- * attention passes over it.  Positions below 0 (kv_lens[b] < n_b) and from max_pages *
- * page_size on are not stored either.  seq_starts that break their properties give
- * unspecified but in-bounds results (MX_DEBUG checks them).
+ * Requirements of every call with a cache: tokens, batch >= 0, the other sizes >= 1,
+ * strides that leave the rows of head_dim codes apart (each of the three at least the
+ * extent of what lies inside it, in one of the six orders; else MX_ERR_INVALID_ARG);
+ * head_dim 64 or 128, page_size a power of two in 16..1024, num_pages and max_pages *
+ * page_size below 2^30, kv_heads <= 1024, batch <= 65536, batch * kv_heads below
+ * 2^23, tokens below 2^27, strides not negative, ld_token below 2^20, ld_page below
+ * 2^32, ld_head * kv_heads below 2^46, num_pages * kv_heads * page_size / 16 below
+ * 2^31 (else MX_ERR_UNSUPPORTED); k, v and their strides multiples of 16 bytes, the
+ * tables aligned to their elements (else MX_ERR_ALIGN).  A stride over one element
+ * is not looked at.
+ * The tables are read on the device only.  A page number outside [0, num_pages) holds
+ * no positions: nothing is stored there, reads give zeros, the attention passes over
+ * it.  Positions below 0 (kv_lens[b] < n_b) and from max_pages * page_size on are not
+ * stored either.  seq_starts that break their properties give unspecified but in-bounds
+ * results (MX_DEBUG checks them).
  */
 
 /*
@@ -124,20 +129,22 @@ typedef struct mx_kv_cache {
  *   c = max(c_new, c_old),  c_new = the least code with amax <= 448 * 2^(c - 127)
  * (0 where amax is 0), amax the largest finite magnitude of the block's new values;
  * c_old = 0 where the call writes the block's first position, the stored code
- * otherwise.  New values are rounded to the nearest E4M3 (ties to even) of that
- * scale, NaN and infinities become the code 0x7F; where c > c_old the older positions' codes
- * of the block are rounded anew.  Other than the MX rule's floor(log2 amax) - 8, c_new
+ * otherwise.  New values are rounded to the nearest E4M3 (ties to even) of that scale;
+ * NaN and infinities become the code 0x7F; where c > c_old the older positions' codes of
+ * the block are rounded anew.  Other than the MX rule's floor(log2 amax) - 8, c_new
  * clamps nothing, so a block that grows never holds a clamped value.
  *   k, v   BF16 [tokens][kv_heads][head_dim], strides ld_kt, ld_kh / ld_vt, ld_vh
- *   freqs  DEVICE double [rot_dim / 2]: keys are rotated (mx_rope's formula, by
- *          their position in the cache) before they are rounded, in 64 bits and but once (beyond FP32's range: as infinities);
- *          null: as they are (rot_dim, style, amplitude not used)
- * A block may be written by one sequence of a call only (pages that several sequences read,
- * as a shared prefix, are not written).  Deterministic.
- * Requirements beyond the cache's: tokens >= 0; rot_dim % 16 == 0, 16 <= rot_dim <=
- * head_dim (else MX_ERR_SHAPE); strides of k and v as mx_rope's x (else MX_ERR_INVALID_ARG / MX_ERR_ALIGN);
- * tokens below 2^31 (else MX_ERR_UNSUPPORTED); k, v, freqs and the tables do not overlap the cache, nor the
- * cache's parts each other (else MX_ERR_OVERLAP; k and v may interleave in one buffer).
+ *   freqs  DEVICE double [rot_dim / 2]: keys are turned first, by their position in the
+ *          cache (mx_rope's formula), in 64 bits: the rounding to E4M3 is the only one
+ *          (beyond FP32's range they count as infinite);
+ *          null: keys as they are (rot_dim, style, amplitude not used)
+ * A block may be written by one sequence of a call only (pages that several sequences
+ * read, as a shared prefix, are not written).  Deterministic.
+ * Requirements beyond the cache's: strides of k and v as mx_rope's x; style and amplitude
+ * as mx_rope's (else MX_ERR_INVALID_ARG), rot_dim a multiple of 16, 16 <= rot_dim <=
+ * head_dim (else MX_ERR_SHAPE), if freqs is given; k, v, freqs and the tables do not
+ * overlap the cache, nor the cache's parts each other (else MX_ERR_OVERLAP; codes of
+ * keys and values may alternate in one buffer).
  */
 mx_status mx_kv_append(const mx_kv_cache *cache, const void *k, int64_t ld_kt, int64_t ld_kh, const void *v,
                        int64_t ld_vt, int64_t ld_vh, int64_t tokens, const double *freqs, int64_t rot_dim, int style,
@@ -148,8 +155,8 @@ mx_status mx_kv_append(const mx_kv_cache *cache, const void *k, int64_t ld_kt, i
  * sequences wrote (n_b = kv_lens[b] gives a sequence whole).
  *   k, v  [tokens][kv_heads][head_dim] contiguous, of dtype (MX_BF16 or MX_F32), out;
  *         either may be null.  Exact in both; rows that the cache does not hold are zeros.
- * Requirements beyond the cache's: tokens as mx_kv_append's; k and v 16-byte aligned (else
- * MX_ERR_ALIGN); no overlap (else MX_ERR_OVERLAP).
+ * Requirements beyond the cache's: dtype one of the two (else MX_ERR_INVALID_ARG); k and v
+ * 16-byte aligned (else MX_ERR_ALIGN); they overlap nothing (else MX_ERR_OVERLAP).
  */
 mx_status mx_kv_read(const mx_kv_cache *cache, int64_t tokens, void *k, void *v, int dtype, void *stream);
 
@@ -158,22 +165,27 @@ mx_status mx_kv_read(const mx_kv_cache *cache, int64_t tokens, void *k, void *v,
  * and its key/value head g = h / (q_heads / kv_heads),
  *   s_j = scale * q[t][h] . k_j,  j in [0, kv_lens[b]); causal: j <= p; window w > 0: j > p - w
  *   out[t][h] = sum_j exp(s_j) v_j / sum_j exp(s_j),  lse[t][h] = ln sum_j exp(s_j)
- * A row that sees no position gets zeros and lse -inf.  Keys and values a row does not
- * see take no part, NaN among them.
+ * A row that sees no position, or none with a score above -inf, gets zeros and lse -inf.
+ * Keys and values a row does not see take no part, NaN among them.
  *   q, out   BF16 [tokens][q_heads][head_dim], strides ld_qt, ld_qh / ld_ot, ld_oh
  *   lse      DEVICE float [tokens][q_heads] out, or null
- *   max_new  no sequence has more than max_new rows in this call (0: not known).  Rows of a
- *            sequence with more are unspecified.  Given, a step of few rows saves a launch.
+ *   max_new  no sequence has more than max_new rows in this call (0: not known).  Rows
+ *            of a sequence with more are unspecified.  Given, a step of few rows saves
+ *            launches and workspace.
  *   workspace  DEVICE scratch of mx_kv_attention_workspace_bytes(...) bytes, 16-byte
- *            aligned (partial sums where the cache is split over workgroups)
- * Scores, exponentials, sums and outputs are formed in FP32 (the keys' and queries' products
- * are exact), the weights exp(s_j - max) rounded to BF16 for the product with the
- * values; one rounding of the output.  The order of the sums depends on the sizes, the
- * tables' contents and the device's compute-unit count: the same call gives the same bytes.
- * Requirements beyond the cache's: tokens >= 0, q_heads a multiple of kv_heads, scale finite
- * and >= 0, window >= 0 and 0 unless causal, max_new >= 0 (else MX_ERR_INVALID_ARG); tokens * q_heads
- * below 2^27 and q_heads / kv_heads <= 1024 (else MX_ERR_UNSUPPORTED); q and out as mx_rope's x; out and lse
- * overlap nothing, and the cache is not written (else MX_ERR_OVERLAP).
+ *            aligned (partial sums where the cache is split over workgroups; null if 0)
+ * The cache's values enter as BF16: exact but beyond its range (scales from 2^120 on),
+ * where they are infinite.  Products of queries and keys are exact; scores, exponentials,
+ * sums and outputs are formed in FP32, the weights exp(s_j - max) rounded to BF16 for the
+ * product with the values; one rounding of the output.  A score beyond FP32's range gives
+ * NaN.  The order of the sums depends on the sizes, the tables' contents and the device's
+ * compute-unit count: the same call gives the same bytes.
+ * mx_kv_attention_workspace_bytes is host-only (0 for sizes that the call refuses too).
+ * Requirements beyond the cache's: q_heads a multiple of kv_heads, scale finite and >= 0,
+ * window >= 0 and 0 unless causal, max_new >= 0, the workspace large enough (else
+ * MX_ERR_INVALID_ARG); tokens * q_heads below 2^27 and q_heads / kv_heads <= 1024 (else
+ * MX_ERR_UNSUPPORTED); q and out as mx_rope's x; lse aligned to 4 bytes, the workspace to 16
+ * (else MX_ERR_ALIGN); out, lse and the workspace overlap nothing (else MX_ERR_OVERLAP).
  */
 int64_t mx_kv_attention_workspace_bytes(int64_t tokens, int64_t batch, int64_t q_heads, int64_t kv_heads,
                                         int64_t head_dim, int64_t max_new);

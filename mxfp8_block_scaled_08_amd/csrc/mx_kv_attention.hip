@@ -20,10 +20,20 @@
 // transposed there by byte permutes; no LDS but for the four waves' join.  The work, chunks of 128
 // positions of every (sequence, head, tile of rows), lies on one line that is cut into equal pieces,
 // one a workgroup, so uneven sequences load the chip evenly; pieces of one item meet in
-// kv_join_kernel.
+// kv_join_kernel.  64 sequences of up to 16 k positions, 32 heads over 8 (1.23 GB): 222-229 us, 5.4
+// TB/s, a large copy's 5.0-5.2; two of up to 131 k, 32 heads over 4 (106 MB): 29 us and 6 for the
+// join, most of both the start of a launch and the tail's.  Two pieces a compute unit are as many
+// as run at once (two waves a SIMD of 256 registers); one, three or four, and workgroups of eight
+// waves, were slower.
 //
 // Many rows (prompts): kv_tiles_kernel.  Bound by the matrix cores and the exponentials.  128 rows
-// a workgroup, 64 positions a step, converted once into LDS (double buffered).
+// a workgroup, 64 positions a step, converted once into LDS (double buffered).  Four prompts of up
+// to 4096 rows behind up to 2048 positions, 32 heads over 8 (787 GFLOP): 810-875 us, 0.90-0.97
+// PFLOP/s, a large BF16 product's 1.32: vector instructions take 48 % of the cycles, the matrix
+// cores 44 %, and on one SIMD the two overlap only in part (4 products and 32 fused multiply-adds:
+// 64 and 74 ns alone, 96 together).  64 rows a wave, which halves the reads of LDS a row, leaves
+// one wave a SIMD (1291 us); eight waves on one staging gained nothing, and two groups of waves in
+// opposite phases lost (888 against 853).
 #include "mx_kv_device.h"
 
 #include <algorithm>
@@ -1247,8 +1257,8 @@ template <int D> static hipError_t launch(const KvView &c, const KvQueries &q, K
 {
     const dim3 block(KVA_THREADS);
     const int64_t positions = (int64_t)c.max_pages << c.page_shift;
-    // A cache of few positions: whole items save the join's launch (one sequence of 701, 32 heads over 8: a call of 14.2 us
-    // 12.2, on the GPU 11.4 against 12.0), and beside prompts the few-row kernel's own.
+    // A cache of few positions: whole items save the join's launch (one sequence of 701, 32 heads over 8: a call 12.2 us
+    // instead of 14.2, on the GPU 12.0 against 11.4), and beside prompts the few-row kernel's own.
     s.plan.whole = positions <= KVA_WHOLE;
     if (s.tiles) {
         if (s.plan.whole)

@@ -330,3 +330,27 @@ def test_reference_rotation_is_a_complex_product():
     np.testing.assert_allclose(got[..., 1:32:2], inter.imag, atol=1e-12)
     assert (got[..., 32:] == x[..., 32:]).all()
     np.testing.assert_allclose(ref.rope(ref.rope(x, pos, f), pos, f, inverse=True), x, atol=1e-12)
+
+
+@pytest.mark.parametrize("name,base", CALLS)
+def test_limits_of_the_cache(name, base):
+    """The last sizes that are taken and the first that are refused, where 32-bit offsets would wrap."""
+    def r(status, **kw):
+        none = dict(base, tokens=0, **({"q_heads": 4 * kw.get("kv_heads", 2)} if "q_heads" in base else {}))
+        assert kv._fn(name)(_cache(**kw), *none.values(), None) == status, mx.mx_last_error()
+
+    r(UNSUP, ld_page=1 << 32)
+    r(mx.MX_OK, ld_page=(1 << 32) - 16)
+    r(mx.MX_OK, num_pages=1, ld_page=1 << 50)  # a stride over one page is not looked at
+    r(UNSUP, kv_heads=1, ld_page=64 * 128, page_size=64, num_pages=1 << 29)  # 2^31 blocks
+    r(mx.MX_OK, kv_heads=1, ld_page=64 * 128, page_size=64, num_pages=(1 << 29) - 1)
+    r(UNSUP, kv_heads=1024, num_pages=1, ld_head=1 << 36)
+    r(mx.MX_OK, kv_heads=1024, num_pages=1, ld_head=(1 << 36) - 16)
+    r(UNSUP, batch=1 << 16, kv_heads=128, ld_head=64 * 128, ld_page=1 << 20)
+    r(mx.MX_OK, batch=1 << 16, kv_heads=127, ld_head=64 * 128, ld_page=1 << 20)
+    r(UNSUP, max_pages=1 << 20, page_size=1024, ld_head=1 << 17, ld_page=1 << 18)
+    r(mx.MX_OK, max_pages=(1 << 20) - 1, page_size=1024, ld_head=1 << 17, ld_page=1 << 18)
+    # pages outside or inside the heads, slots outside both
+    r(mx.MX_OK, ld_page=64 * 128, ld_head=10 * 64 * 128)
+    r(mx.MX_OK, ld_page=128, ld_head=1280, ld_token=2560)
+    r(INV, ld_page=128, ld_head=1280, ld_token=2432)

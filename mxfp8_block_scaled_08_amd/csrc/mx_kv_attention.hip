@@ -28,12 +28,14 @@
 //
 // Many rows (prompts): kv_tiles_kernel.  Bound by the matrix cores and the exponentials.  128 rows
 // a workgroup, 64 positions a step, converted once into LDS (double buffered).  Four prompts of up
-// to 4096 rows behind up to 2048 positions, 32 heads over 8 (787 GFLOP): 810-875 us, 0.90-0.97
-// PFLOP/s, a large BF16 product's 1.32: vector instructions take 48 % of the cycles, the matrix
-// cores 44 %, and on one SIMD the two overlap only in part (4 products and 32 fused multiply-adds:
-// 64 and 74 ns alone, 96 together).  64 rows a wave, which halves the reads of LDS a row, leaves
-// one wave a SIMD (1291 us); eight waves on one staging gained nothing, and two groups of waves in
-// opposite phases lost (888 against 853).
+// to 4096 rows behind up to 2048 positions, 32 heads over 8 (787 GFLOP): 810-875 us by card, 0.90-0.97
+// PFLOP/s, a large BF16 product's 1.33.  In the cycles of a busy unit vector instructions issue 57 %,
+// the matrix cores work 47 %, at 1.9 GHz; on one SIMD the two overlap only in part (4 products and
+// 32 fused multiply-adds: 64 and 74 ns alone, 96 together).  Slower: the exponentials of half a
+// step among the products of the other half (866 -> 925 us), 64 rows a wave, which halves LDS' reads
+// a row but leaves one wave a SIMD (875 -> 1291), two groups of waves in opposite phases (853 ->
+// 888).  No gain: eight waves on one staging, the maximum in four chains, the first product's two
+// accumulators in turn.
 #include "mx_kv_device.h"
 
 #include <algorithm>

@@ -14,7 +14,7 @@
 // formed once a workgroup, in 64 bits, and the keys are rotated in 64 bits, so that the
 // rounding to E4M3 is their only one.
 //
-// 18 k new rows of 4 heads of 128 (55 MB): 23 us, 2.4 TB/s, 15 us without the rotation; a
+// 18 k new rows of 4 heads of 128 (55 MB): 21 us, 2.6 TB/s, 15 us without the rotation; a
 // copy of those bytes takes 11.  What is left is latency: starts, lengths, page, rows and
 // angles each wait for the one before, 5 us for a single row, and 4 workgroups a compute
 // unit (128 registers) leave a short second turn.  5 of them spill (23 us), 6 more so (28);
@@ -135,14 +135,12 @@ template <int D> struct Plane {
     uint4 w[D / 64][2];
 };
 
-// The scale's code of a block whose new values need c_new: the older positions' codes are rounded anew where it grows.
+// The scale's code of a block whose new values need `code` and older ones have `old` (0 if there are none): the older
+// positions' codes are rounded anew where it grows.
 template <int D>
-__device__ __forceinline__ uint32_t settle_scale(const KvUnit &u, uint32_t code, uint8_t *sp, uint8_t *cell)
+__device__ __forceinline__ uint32_t settle_scale(const KvUnit &u, uint32_t code, uint32_t old, uint8_t *cell)
 {
-    if (u.lo == 0)
-        return code;
     const int q = threadIdx.x & 3, t = (threadIdx.x & 63) >> 2;
-    const uint32_t old = *sp;
     if (code <= old)
         return old;
     if (t < u.lo) {
@@ -164,15 +162,18 @@ template <int D> __global__ __launch_bounds__(KV_THREADS, 4) void kv_append_kern
 {
     constexpr int UNITS = D / 64;  // units of 16 elements a lane
     __shared__ double2 lds_cs[KV_BLOCK * (D / 2)];
-    KvUnit u;
-    if (!find_unit(c, u))
-        return;
-    const int32_t page = page_of(c, u.b, u.blk);
-    if (page < 0)
-        return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int q = lane & 3, t = lane >> 2;
     const int half = n.freqs ? n.rot / 2 : 0;
+    // Loads that do not need each other are on their way together (one token of 64 sequences 8.4 -> 7.7 us): the first of
+    // a thread's frequencies, then the page's number and the rows, then the old scale.
+    double freq = 0.0;
+    if (half)
+        freq = n.freqs[threadIdx.x - pairs(threadIdx.x) * half];
+    KvUnit u;
+    if (!find_unit(c, u))
+        return;
+    const int32_t page = c.table[(int64_t)u.b * c.max_pages + (u.blk >> (c.page_shift - 4))];
     const bool live = t >= u.lo && t < u.hi;
     const int32_t slot = (u.blk & ((1 << (c.page_shift - 4)) - 1)) * KV_BLOCK;
     // planes: the keys of every head, then the values (so that a workgroup's waves share the rotations evenly)
@@ -194,25 +195,36 @@ template <int D> __global__ __launch_bounds__(KV_THREADS, 4) void kv_append_kern
     int pl = blockIdx.y * 4 + wave;
     Plane<D> now;
     if (pl < planes)
-        fetch(pl, now);  // the first on its way while the angles are formed
+        fetch(pl, now);
+    if ((uint32_t)page >= (uint32_t)c.num_pages)
+        return;
+    auto scale_at = [&](int pl) {
+        const bool is_v = pl >= c.kv_heads;
+        const int h = is_v ? pl - c.kv_heads : pl;
+        return (is_v ? c.v_scale : c.k_scale) + (((int64_t)page * c.kv_heads + h) << (c.page_shift - 4)) + (slot >> 4);
+    };
+    uint32_t old = u.lo > 0 && pl < planes ? *scale_at(pl) : 0;
     if (half) {
         const int first = u.lo * half, last = u.hi * half;
         for (int i = first + (int)threadIdx.x; i < last; i += KV_THREADS) {
             const int p = (int)pairs((uint32_t)i);
             double sn, cs;
-            sincos_turns(turns(u.blk * KV_BLOCK + p, n.freqs[i - p * half]), sn, cs);
+            if (KV_THREADS % half && i >= first + KV_THREADS)
+                freq = n.freqs[i - p * half];
+            sincos_turns(turns(u.blk * KV_BLOCK + p, freq), sn, cs);
             lds_cs[p * half + angle_at(p, i - p * half)] = make_double2(cs * n.amplitude, sn * n.amplitude);
         }
         __syncthreads();
     }
     for (; pl < planes; pl += step) {
-        if (pl >= step)
+        uint8_t *sp = scale_at(pl);
+        if (pl >= step) {
             fetch(pl, now);
+            old = u.lo > 0 ? *sp : 0;
+        }
         const bool is_v = pl >= c.kv_heads;
         const int h = is_v ? pl - c.kv_heads : pl;
         const int rot = is_v ? 0 : 2 * half;
-        uint8_t *sp = (is_v ? c.v_scale : c.k_scale) +
-                      (((int64_t)page * c.kv_heads + h) << (c.page_shift - 4)) + (slot >> 4);
         uint8_t *cell = (is_v ? c.v : c.k) + page * c.ld_page + h * c.ld_head + (slot + t) * c.ld_token;
         uint32_t code;
         uint2 out[UNITS][2];
@@ -230,7 +242,7 @@ template <int D> __global__ __launch_bounds__(KV_THREADS, 4) void kv_append_kern
                 }
             top = wave_max(max(m << 16, m & 0xFFFF0000u));
             if (top < 0x7F800000u) {
-                code = settle_scale<D>(u, kv_scale_code(top), sp, cell);
+                code = settle_scale<D>(u, kv_scale_code(top), old, cell);
 #pragma unroll
                 for (int k = 0; k < UNITS; k++)
 #pragma unroll
@@ -287,7 +299,7 @@ template <int D> __global__ __launch_bounds__(KV_THREADS, 4) void kv_append_kern
                     }
                 top = wave_max(top) << 1;
             }
-            code = settle_scale<D>(u, kv_scale_code(top >> 1), sp, cell);
+            code = settle_scale<D>(u, kv_scale_code(top >> 1), old, cell);
             const float scale = cvt_scale(code);
 #pragma unroll
             for (int k = 0; k < UNITS; k++) {

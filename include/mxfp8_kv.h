@@ -138,8 +138,8 @@ typedef struct mx_kv_cache {
  *          cache (mx_rope's formula), in 64 bits: the rounding to E4M3 is the only one
  *          (beyond FP32's range they count as infinite);
  *          null: keys as they are (rot_dim, style, amplitude not used)
- * A block may be written by one sequence of a call only (pages that several sequences
- * read, as a shared prefix, are not written).  Deterministic.
+ * A block that is written may stand at one place of the call's tables only (pages that
+ * several sequences read, as a shared prefix, are not written).  Deterministic.
  * Requirements beyond the cache's: strides of k and v as mx_rope's x; style and amplitude
  * as mx_rope's (else MX_ERR_INVALID_ARG), rot_dim a multiple of 16, 16 <= rot_dim <=
  * head_dim (else MX_ERR_SHAPE), if freqs is given; k, v, freqs and the tables do not

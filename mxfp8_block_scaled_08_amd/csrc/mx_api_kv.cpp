@@ -86,7 +86,8 @@ static mx_status check_cache(const char *fn, const mx_kv_cache *c, int64_t token
         return fail(MX_ERR_INVALID_ARG, "%s: null pointer cache", fn);
     if (tokens < 0 || c->batch < 0 || c->num_pages < 1 || c->kv_heads < 1 || c->max_pages < 1 || c->page_size < 1 ||
         c->head_dim < 1)
-        return fail(MX_ERR_INVALID_ARG, "%s: need tokens, batch >= 0 and num_pages, kv_heads, page_size, head_dim, max_pages >= 1", fn);
+        return fail(MX_ERR_INVALID_ARG,
+                    "%s: need tokens, batch >= 0 and num_pages, kv_heads, page_size, head_dim, max_pages >= 1", fn);
     if (c->head_dim != 64 && c->head_dim != 128)
         return fail(MX_ERR_UNSUPPORTED, "%s: head_dim=%lld is neither 64 nor 128", fn, (long long)c->head_dim);
     if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)))
@@ -329,7 +330,8 @@ mx_status mx_kv_attention(const mx_kv_cache *cache, const void *q, int64_t ld_qt
     if (window < 0 || (window > 0 && !causal) || max_new < 0)
         return fail(MX_ERR_INVALID_ARG, "%s: need window, max_new >= 0, and no window unless causal", fn);
     if (q_heads / cache->kv_heads > 1024 || tokens >= ((int64_t)1 << 27) / q_heads)
-        return fail(MX_ERR_UNSUPPORTED, "%s: more than 1024 query heads a key/value head, or tokens * q_heads from 2^27", fn);
+        return fail(MX_ERR_UNSUPPORTED, "%s: more than 1024 query heads a key/value head, or tokens * q_heads from 2^27",
+                    fn);
     if (empty)
         return ok();
     const int64_t dim = cache->head_dim;

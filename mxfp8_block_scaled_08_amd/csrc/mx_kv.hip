@@ -383,7 +383,8 @@ __global__ __launch_bounds__(KV_THREADS) void kv_read_kernel(KvView c, T *__rest
         out += (row * c.kv_heads + h) * D;
         float w[CHUNKS][8] = {};
         if (page >= 0) {
-            const uint32_t code = ((is_v ? c.v_scale : c.k_scale) + (((int64_t)page * c.kv_heads + h) << (c.page_shift - 4)))[slot >> 4];
+            const uint8_t *sp = (is_v ? c.v_scale : c.k_scale) + (((int64_t)page * c.kv_heads + h) << (c.page_shift - 4));
+            const uint32_t code = sp[slot >> 4];
             const uint8_t *cell = (is_v ? c.v : c.k) + page * c.ld_page + h * c.ld_head + (slot + t) * c.ld_token;
 #pragma unroll
             for (int j = 0; j < CHUNKS; j++) {

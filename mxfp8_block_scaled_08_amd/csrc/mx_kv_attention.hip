@@ -158,7 +158,8 @@ __device__ __forceinline__ uint32_t finite_codes(uint32_t w, uint32_t scale)
 {
     const uint32_t lo = e4m3_bf16<false>(w, cvt_scale(scale)), hi = e4m3_bf16<true>(w, cvt_scale(scale));
     const auto keep = [](uint32_t bf16, uint32_t byte) { return (bf16 & 0x7F80u) == 0x7F80u ? 0u : byte; };
-    return w & (keep(lo & 0xFFFFu, 0xFFu) | keep(lo >> 16, 0xFF00u) | keep(hi & 0xFFFFu, 0xFF0000u) | keep(hi >> 16, 0xFF000000u));
+    return w & (keep(lo & 0xFFFFu, 0xFFu) | keep(lo >> 16, 0xFF00u) | keep(hi & 0xFFFFu, 0xFF0000u) |
+                keep(hi >> 16, 0xFF000000u));
 }
 
 // ---------------------------------------------------------------------------
@@ -220,7 +221,8 @@ __device__ __forceinline__ BlockAt block_at(const HeadCache &c, int32_t blk)
 }
 
 // The block's 16 rows as a buffer: one offset register a lane serves all its loads, the rows' steps are scalar.
-template <int D> __device__ __forceinline__ __amdgpu_buffer_rsrc_t block_range(const uint8_t *p, const BlockAt &at, uint32_t ld)
+template <int D>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t block_range(const uint8_t *p, const BlockAt &at, uint32_t ld)
 {
     return byte_range(p + at.codes, 15 * ld + D);
 }
@@ -235,7 +237,8 @@ template <int D> struct Codes {
 };
 
 template <int D>
-__device__ __forceinline__ void load_codes(const HeadCache &c, const BlockAt (&at)[2], uint32_t koff, uint32_t voff, uint32_t none, Codes<D> &t)
+__device__ __forceinline__ void load_codes(const HeadCache &c, const BlockAt (&at)[2], uint32_t koff, uint32_t voff,
+                                           uint32_t none, Codes<D> &t)
 {
     const uint32_t ld = c.ld_token;
 #pragma unroll
@@ -754,7 +757,8 @@ template <int D, int NT> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_ro
 // Partial sums of one row from `count` slots, slot i's row at index at(i) of ml and acc: groups of
 // D / 4 threads take slots in turn and meet in LDS.
 template <int D, typename F>
-__device__ __forceinline__ void join_row(const KvQueries &q, const KvPlan &plan, int32_t count, F at, int64_t token, int32_t head)
+__device__ __forceinline__ void join_row(const KvQueries &q, const KvPlan &plan, int32_t count, F at, int64_t token,
+                                         int32_t head)
 {
     constexpr int LANES = D / 4, GROUPS = KVA_THREADS / LANES;
     __shared__ float lds_l[GROUPS], lds_m[GROUPS];
@@ -873,7 +877,8 @@ template <int D> struct TileState {
 // Values that may not be finite are left out of a step that some row does not see whole (a weight of 0 would not keep
 // them out of its sum); odd_values adds them, position by position, to the rows that see them.
 template <int D>
-__device__ __forceinline__ void odd_values(const HeadCache &c, TileState<D> &r, const Frag (&p)[4], int32_t t0, int32_t kv_len)
+__device__ __forceinline__ void odd_values(const HeadCache &c, TileState<D> &r, const Frag (&p)[4], int32_t t0,
+                                           int32_t kv_len)
 {
     const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
 #pragma unroll 1
@@ -1036,12 +1041,13 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
     };
     auto stage = [&](uint32_t buf) {
         const float kf = cvt_scale(ks), vf = cvt_scale(vs);
+        auto eight = [](uint32_t a, uint32_t b, float s) {
+            return make_uint4(e4m3_bf16<false>(a, s), e4m3_bf16<true>(a, s), e4m3_bf16<false>(b, s), e4m3_bf16<true>(b, s));
+        };
 #pragma unroll
         for (int j = 0; j < KW; j++) {
-            *reinterpret_cast<uint4 *>(lds + ((buf + kst) ^ (32 * j))) = make_uint4(e4m3_bf16<false>(kc[j].x, kf), e4m3_bf16<true>(kc[j].x, kf),
-                                                                     e4m3_bf16<false>(kc[j].y, kf), e4m3_bf16<true>(kc[j].y, kf));
-            *reinterpret_cast<uint4 *>(lds + ((buf + kst) ^ (32 * j + 16))) = make_uint4(e4m3_bf16<false>(kc[j].z, kf), e4m3_bf16<true>(kc[j].z, kf),
-                                                                         e4m3_bf16<false>(kc[j].w, kf), e4m3_bf16<true>(kc[j].w, kf));
+            *reinterpret_cast<uint4 *>(lds + ((buf + kst) ^ (32 * j))) = eight(kc[j].x, kc[j].y, kf);
+            *reinterpret_cast<uint4 *>(lds + ((buf + kst) ^ (32 * j + 16))) = eight(kc[j].z, kc[j].w, kf);
         }
         uint32_t x[VB][4];
 #pragma unroll
@@ -1090,8 +1096,8 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
 #pragma unroll
             for (int k = 0; k < D / 16; k++) {
                 const uint4 a = *reinterpret_cast<const uint4 *>(lds + ((buf + ka) ^ (32 * k)) + 32 * D * 2 * j);
-                x[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, r.q[k]),
-                                                               x[j], 0, 0, 0);
+                x[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                               __builtin_bit_cast(bf16x8_t, r.q[k]), x[j], 0, 0, 0);
             }
         }
         stage(buf ^ BUF);
@@ -1137,7 +1143,8 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
         for (int k = 0; k < 4; k++)
 #pragma unroll
             for (int j = 0; j < D / 32; j++) {
-                const uint4 a = *reinterpret_cast<const uint4 *>(lds + ((buf + va) ^ (32 * k) ^ (j & 1 ? ODD : 0)) + 32 * KVA_STEP * 2 * j);
+                const uint32_t from = ((buf + va) ^ (32 * k) ^ (j & 1 ? ODD : 0)) + 32 * KVA_STEP * 2 * j;
+                const uint4 a = *reinterpret_cast<const uint4 *>(lds + from);
                 r.o[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), p[k].f, r.o[j], 0, 0, 0);
             }
         if (flags & 0x01010101u)
@@ -1175,7 +1182,8 @@ template <int D> __global__ __launch_bounds__(KVA_THREADS, 2) void kv_tiles_kern
     for (int j = 0; j < D / 32; j++)
 #pragma unroll
         for (int k = 0; k < 16; k += 4)
-            *reinterpret_cast<float4 *>(acc + 32 * j + 2 * k + 4 * half) = make_float4(r.o[j][k], r.o[j][k + 1], r.o[j][k + 2], r.o[j][k + 3]);
+            *reinterpret_cast<float4 *>(acc + 32 * j + 2 * k + 4 * half) =
+                make_float4(r.o[j][k], r.o[j][k + 1], r.o[j][k + 2], r.o[j][k + 3]);
 }
 
 // The ranges of a tile's rows together: blockIdx as kv_tiles_kernel's, y the row.
@@ -1250,7 +1258,8 @@ static KvSpace space_of(int64_t tokens, int64_t batch, int64_t q_heads, int64_t 
     return s;
 }
 
-int64_t kv_attention_workspace_bytes(int64_t tokens, int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t max_new)
+int64_t kv_attention_workspace_bytes(int64_t tokens, int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t dim,
+                                     int64_t max_new)
 {
     return space_of(tokens, batch, q_heads, kv_heads, dim, max_new).bytes;
 }

@@ -13,8 +13,8 @@ def bf16(rng, *shape, std=1.0):
 
 class Batch:
     """Sequences of new[b] rows behind ctx[b] positions, pages dealt out of order, the rest
-    of the table -1 (room: positions that it has places for at least).  Cells that no position holds are filled with any bytes, NaN codes and
-    scales among them."""
+    of the table -1 (room: positions that it has places for at least).  Cells that no
+    position holds are filled with any bytes, NaN codes and scales among them."""
 
     def __init__(self, seed, new, ctx, heads, dim, page, layout="hnd", spare=2, behind=0, filled=True, std=1.0, room=0):
         self.rng = rng = np.random.default_rng(seed)

@@ -430,6 +430,9 @@ __device__ __forceinline__ void masked_step(RowState<D, NT> &r, Codes<D> &t, int
             }
         }
         odd = odd || t.vs[j] >= KVA_BIG_SCALE;
+        // (the codes say it now: zeros at the NaN scale are converted to NaN, in products of the other block's
+        // positions too)
+        t.vs[j] = t.vs[j] == 0xFFu ? 127u : t.vs[j];
     }
     if (!__any(odd)) {
         add_values<D, NT>(r, t, p);

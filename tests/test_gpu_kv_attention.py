@@ -259,3 +259,20 @@ def test_binding_refusals(gpu_lib):
         with pytest.raises(gpu_lib.MxError):
             gpu_lib.mx_kv_attention(**dict(good, **bad))
     assert gpu_lib.mx_kv_attention(q[:0], kv, scale, table, lens, starts * 0).shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("room", ROOM)
+@pytest.mark.parametrize("rows", [12, 70])
+def test_nan_value_scales(gpu_lib, rows, room):
+    """A block of values whose scale is NaN, beside blocks that are none: rows that see only those get numbers."""
+    clean = 0
+    for dim, at in ((64, 16), (128, 16), (64, 32), (128, 32), (64, 48)):
+        if at >= 33 + rows:
+            continue
+        B = Batch(40 + rows + at, [rows, 3], [33, 20], 2, dim, 16, room=room)
+        B.ref.scale[1, B.table[0, at // 16], 0, 0] = 255
+        B.scale.copy_(torch.from_numpy(B.ref.scale))
+        for kw in (dict(), dict(window=10), dict(window=3), dict(max_new=rows)):
+            out, _, _ = _run(gpu_lib, B, 4, **kw)
+            clean += int(torch.isfinite(out[:rows, :2].float()).all(-1).all(-1).sum())
+    assert clean  # (some row sees nothing of the block)

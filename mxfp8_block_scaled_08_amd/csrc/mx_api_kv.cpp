@@ -356,7 +356,8 @@ mx_status mx_kv_attention(const mx_kv_cache *cache, const void *q, int64_t ld_qt
     if ((st = check_workspace(fn, workspace, workspace_bytes, need, 16, all, lens, 10)) != MX_OK ||
         (st = check_starts(fn, cache, tokens, stream)) != MX_OK)
         return st;
-    const int64_t far = (int64_t)1 << 30;  // no position reaches it
+    // a row's position is below 2^31 - 1 (past the table too): a window of that many positions hides none
+    const int64_t far = ((int64_t)1 << 31) - 1;
     const mx::KvQueries a{(const uint16_t *)q, ld_qt, ld_qh, (uint16_t *)out, ld_ot, ld_oh, lse, (int32_t)q_heads,
                           (int32_t)(q_heads / cache->kv_heads), scale, window >= far ? 0 : (int32_t)window, causal != 0,
                           max_new};

@@ -276,3 +276,15 @@ def test_nan_value_scales(gpu_lib, rows, room):
             out, _, _ = _run(gpu_lib, B, 4, **kw)
             clean += int(torch.isfinite(out[:rows, :2].float()).all(-1).all(-1).sum())
     assert clean  # (some row sees nothing of the block)
+
+
+def test_windows_that_reach_far(gpu_lib):
+    """Windows from 2^30 on, rows as far: positions are numbers below 2^31, whatever the table holds."""
+    B = Batch(41, [2, 70], [30, 0], 1, 64, 16, room=1100)
+    cap = B.table.shape[1] * 16
+    for lens in ([2 ** 31 - 1, 2 ** 31 - 1], [2 ** 30 + 40, 2 ** 30 + 71]):
+        B.lens = np.array(lens, np.int32)
+        for window in (2 ** 30 - 1, 2 ** 30, 2 ** 30 + 20, 2 ** 31 - 40, 2 ** 31 - 2, 2 ** 31 - 1, 2 ** 31, 2 ** 62):
+            _run(gpu_lib, B, 2, window=window)
+            _run(gpu_lib, B, 2, window=window, max_new=70)
+    assert cap < 2 ** 30

@@ -79,25 +79,48 @@ struct CacheBufs {
     int64_t len[7];
 };
 
+// The sizes of a call that its workspace depends on too.
+static mx_status check_sizes(const char *fn, int64_t tokens, int64_t batch, int64_t kv_heads, int64_t head_dim)
+{
+    if (tokens < 0 || batch < 0 || kv_heads < 1 || head_dim < 1)
+        return fail(MX_ERR_INVALID_ARG, "%s: need tokens, batch >= 0 and kv_heads, head_dim >= 1", fn);
+    if (head_dim != 64 && head_dim != 128)
+        return fail(MX_ERR_UNSUPPORTED, "%s: head_dim=%lld is neither 64 nor 128", fn, (long long)head_dim);
+    if (kv_heads > 1024 || batch > 65536 || batch * kv_heads >= (int64_t)1 << 23 || tokens >= (int64_t)1 << 27)
+        return fail(MX_ERR_UNSUPPORTED,
+                    "%s: kv_heads must be at most 1024, batch 65536, batch * kv_heads below 2^23, tokens below 2^27", fn);
+    return MX_OK;
+}
+
+// The attention's likewise, behind check_sizes.
+static mx_status check_queries(const char *fn, int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t max_new)
+{
+    if (q_heads < kv_heads || q_heads % kv_heads != 0)
+        return fail(MX_ERR_INVALID_ARG, "%s: q_heads=%lld is no multiple of kv_heads=%lld", fn, (long long)q_heads,
+                    (long long)kv_heads);
+    if (max_new < 0)
+        return fail(MX_ERR_INVALID_ARG, "%s: max_new=%lld is negative", fn, (long long)max_new);
+    if (q_heads / kv_heads > 1024 || tokens * q_heads >= (int64_t)1 << 27)
+        return fail(MX_ERR_UNSUPPORTED, "%s: more than 1024 query heads a key/value head, or tokens * q_heads from 2^27",
+                    fn);
+    return MX_OK;
+}
+
 static mx_status check_cache(const char *fn, const mx_kv_cache *c, int64_t tokens, mx::KvView &view, CacheBufs &bufs,
                              bool &empty)
 {
     if (!c)
         return fail(MX_ERR_INVALID_ARG, "%s: null pointer cache", fn);
-    if (tokens < 0 || c->batch < 0 || c->num_pages < 1 || c->kv_heads < 1 || c->max_pages < 1 || c->page_size < 1 ||
-        c->head_dim < 1)
-        return fail(MX_ERR_INVALID_ARG,
-                    "%s: need tokens, batch >= 0 and num_pages, kv_heads, page_size, head_dim, max_pages >= 1", fn);
-    if (c->head_dim != 64 && c->head_dim != 128)
-        return fail(MX_ERR_UNSUPPORTED, "%s: head_dim=%lld is neither 64 nor 128", fn, (long long)c->head_dim);
+    if (c->num_pages < 1 || c->max_pages < 1 || c->page_size < 1)
+        return fail(MX_ERR_INVALID_ARG, "%s: need num_pages, page_size, max_pages >= 1", fn);
+    const mx_status st = check_sizes(fn, tokens, c->batch, c->kv_heads, c->head_dim);
+    if (st != MX_OK)
+        return st;
     if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)))
         return fail(MX_ERR_UNSUPPORTED, "%s: page_size=%lld is no power of two in 16..1024", fn, (long long)c->page_size);
     const int64_t lim = (int64_t)1 << 30;
-    if (c->num_pages >= lim || c->max_pages >= lim / c->page_size || c->kv_heads > 1024 || c->batch > 65536 ||
-        c->batch * c->kv_heads >= (int64_t)1 << 23 || tokens >= (int64_t)1 << 27)
-        return fail(MX_ERR_UNSUPPORTED,
-                    "%s: num_pages, max_pages * page_size must be below 2^30, kv_heads at most 1024, batch 65536, batch * "
-                    "kv_heads below 2^23, tokens below 2^27", fn);
+    if (c->num_pages >= lim || c->max_pages >= lim / c->page_size)
+        return fail(MX_ERR_UNSUPPORTED, "%s: num_pages and max_pages * page_size must be below 2^30", fn);
     const int64_t most = (int64_t)1 << 46;
     if (c->ld_token < 0 || c->ld_head < 0 || c->ld_page < 0 || c->ld_token >= (int64_t)1 << 20 ||
         (c->num_pages > 1 && c->ld_page >= (int64_t)1 << 32) || (c->kv_heads > 1 && c->ld_head >= most / c->kv_heads) ||
@@ -304,10 +327,14 @@ mx_status mx_kv_read(const mx_kv_cache *cache, int64_t tokens, void *k, void *v,
 int64_t mx_kv_attention_workspace_bytes(int64_t tokens, int64_t batch, int64_t q_heads, int64_t kv_heads,
                                         int64_t head_dim, int64_t max_new)
 {
-    if (tokens < 1 || batch < 1 || kv_heads < 1 || q_heads < kv_heads || head_dim < 1 || max_new < 0 ||
-        tokens >= (int64_t)1 << 27 || q_heads > (int64_t)1 << 20 || batch > 65536 || tokens * q_heads >= (int64_t)1 << 27)
+    const char *fn = "mx_kv_attention_workspace_bytes";
+    if (check_sizes(fn, tokens, batch, kv_heads, head_dim) != MX_OK ||
+        check_queries(fn, tokens, q_heads, kv_heads, max_new) != MX_OK)
         return 0;
-    return mx::kv_attention_workspace_bytes(tokens, batch, q_heads, kv_heads, head_dim, max_new);
+    ok();
+    return tokens == 0 || batch == 0
+               ? 0
+               : mx::kv_attention_workspace_bytes(tokens, batch, q_heads, kv_heads, head_dim, max_new);
 }
 
 mx_status mx_kv_attention(const mx_kv_cache *cache, const void *q, int64_t ld_qt, int64_t ld_qh, int64_t tokens,
@@ -322,16 +349,12 @@ mx_status mx_kv_attention(const mx_kv_cache *cache, const void *q, int64_t ld_qt
     mx_status st = check_cache(fn, cache, tokens, view, bufs, empty);
     if (st != MX_OK)
         return st;
-    if (q_heads < cache->kv_heads || q_heads % cache->kv_heads != 0)
-        return fail(MX_ERR_INVALID_ARG, "%s: q_heads=%lld is no multiple of kv_heads=%lld", fn, (long long)q_heads,
-                    (long long)cache->kv_heads);
+    if ((st = check_queries(fn, tokens, q_heads, cache->kv_heads, max_new)) != MX_OK)
+        return st;
     if (!std::isfinite(scale) || scale < 0.0f)
         return fail(MX_ERR_INVALID_ARG, "%s: scale must be finite and not negative", fn);
-    if (window < 0 || (window > 0 && !causal) || max_new < 0)
-        return fail(MX_ERR_INVALID_ARG, "%s: need window, max_new >= 0, and no window unless causal", fn);
-    if (q_heads / cache->kv_heads > 1024 || tokens >= ((int64_t)1 << 27) / q_heads)
-        return fail(MX_ERR_UNSUPPORTED, "%s: more than 1024 query heads a key/value head, or tokens * q_heads from 2^27",
-                    fn);
+    if (window < 0 || (window > 0 && !causal))
+        return fail(MX_ERR_INVALID_ARG, "%s: need window >= 0, and no window unless causal", fn);
     if (empty)
         return ok();
     const int64_t dim = cache->head_dim;

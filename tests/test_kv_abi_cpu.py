@@ -354,3 +354,35 @@ def test_limits_of_the_cache(name, base):
     r(mx.MX_OK, ld_page=64 * 128, ld_head=10 * 64 * 128)
     r(mx.MX_OK, ld_page=128, ld_head=1280, ld_token=2560)
     r(INV, ld_page=128, ld_head=1280, ld_token=2432)
+
+
+def test_workspace_query_and_call_take_the_same_sizes():
+    """Both sides of each limit: the query is above 0 just where the call takes the sizes (asked of a call without a
+    workspace, which says so last)."""
+    def take(tokens, batch, q_heads, kv_heads, dim, max_new=0):
+        need = mx.mx_kv_attention_workspace_bytes(tokens, batch, q_heads, kv_heads, dim, max_new)
+        c = _cache(kv_heads=kv_heads, head_dim=dim, batch=batch, num_pages=2, page_size=16, ld_token=128, ld_head=16 * 128,
+                   ld_page=1 << 22)
+        args = dict(ATTENTION, tokens=tokens, q_heads=q_heads, max_new=max_new, ws=None, ws_bytes=0, lse=None, q=1 << 51,
+                    out=1 << 52, ld_qt=q_heads * 128, ld_ot=q_heads * 128)
+        st = kv._fn("mx_kv_attention")(c, *args.values(), None)
+        if need:
+            assert st == INV and "workspace" in mx.mx_last_error(), (st, mx.mx_last_error())
+        else:
+            assert st in (INV, UNSUP) and "workspace" not in mx.mx_last_error(), (st, mx.mx_last_error())
+        return need > 0
+
+    assert take(5, 3, 8, 2, 128) and take(5, 3, 8, 2, 64) and take(5, 3, 2, 2, 64, 1)
+    assert not take(5, 3, 7, 2, 128) and not take(5, 3, 1, 2, 128) and not take(5, 3, 8, 2, 128, -1)
+    for dim in (32, 96, 192, 256, 1 << 40, 1 << 62):
+        assert not take(5, 3, 8, 2, dim)
+    assert take(5, 3, 1024, 1024, 64) and not take(5, 3, 1025, 1025, 64) and not take(5, 3, 2048, 2048, 64)
+    assert take(5, 3, 1024, 1, 64) and not take(5, 3, 1025, 1, 64) and take(5, 3, 2048, 2, 64) and not take(5, 3, 2050, 2, 64)
+    assert take(5, 65536, 127, 127, 64) and not take(5, 65536, 128, 128, 64) and not take(5, 65537, 1, 1, 64)
+    assert not take(-1, 3, 8, 2, 128) and not take(5, -1, 8, 2, 128) and not take(5, 3, 8, 0, 128) and not take(5, 3, 8, -2, 128)
+    # tokens * q_heads below 2^27, the whole quotient's remainder too
+    for heads in (1, 3, 5, 8, 1000):
+        last = ((1 << 27) - 1) // heads
+        assert take(last, 3, heads, 1, 64) and not take(last + 1, 3, heads, 1, 64), heads
+    assert take((1 << 27) - 1, 1, 1, 1, 128) and not take(1 << 27, 1, 1, 1, 128) and not take(1 << 62, 1, 1, 1, 128)
+    assert not take(5, 3, 1 << 62, 2, 128)

@@ -169,9 +169,9 @@ mx_status mx_kv_read(const mx_kv_cache *cache, int64_t tokens, void *k, void *v,
  * Keys and values a row does not see take no part, NaN among them.
  *   q, out   BF16 [tokens][q_heads][head_dim], strides ld_qt, ld_qh / ld_ot, ld_oh
  *   lse      DEVICE float [tokens][q_heads] out, or null
- *   max_new  no sequence has more than max_new rows in this call (0: not known).  Rows
- *            of a sequence with more are unspecified.  Given, a step of few rows saves
- *            launches and workspace.
+ *   max_new  no sequence has more than max_new rows in this call (0: not known).  Output
+ *            rows of a sequence with more are unspecified, also left as they were (MX_DEBUG
+ *            checks it).  Given, a step of few rows saves launches and workspace.
  *   workspace  DEVICE scratch of mx_kv_attention_workspace_bytes(...) bytes, 16-byte
  *            aligned (partial sums where the cache is split over workgroups; null if 0)
  * The cache's values enter as BF16: exact but beyond its range (scales from 2^120 on),

@@ -159,6 +159,21 @@ static mx_status check_starts(const char *fn, const mx_kv_cache *c, int64_t toke
                           : MX_OK;
 }
 
+// MX_DEBUG: no sequence has more rows than the call was told (0: it was not).
+static mx_status check_most(const char *fn, const mx_kv_cache *c, int64_t tokens, int64_t max_new, void *stream)
+{
+    if (max_new == 0 || !debug_checks())
+        return MX_OK;
+    int64_t bad = -1;
+    const hipError_t e = mx::check_longest(c->seq_starts, c->batch, tokens, max_new, (hipStream_t)stream, &bad);
+    if (e != hipSuccess)
+        return fail(MX_ERR_HIP, "%s: MX_DEBUG check of max_new failed: %s", fn, hipGetErrorString(e));
+    if (bad >= 0)
+        return fail(MX_ERR_INVALID_ARG, "%s: more than max_new=%lld rows from seq_starts[%lld] on (MX_DEBUG check)", fn,
+                    (long long)max_new, (long long)bad);
+    return MX_OK;
+}
+
 // n outputs against the cache's buffers and each other.
 static mx_status check_outputs(const char *fn, const CacheBufs &cache, const void *const *in, const int64_t *in_len, int ins,
                                const void *const *out, const int64_t *out_len, int outs)
@@ -377,7 +392,8 @@ mx_status mx_kv_attention(const mx_kv_cache *cache, const void *q, int64_t ld_qt
     }
     const int64_t need = mx::kv_attention_workspace_bytes(tokens, cache->batch, q_heads, cache->kv_heads, dim, max_new);
     if ((st = check_workspace(fn, workspace, workspace_bytes, need, 16, all, lens, 10)) != MX_OK ||
-        (st = check_starts(fn, cache, tokens, stream)) != MX_OK)
+        (st = check_starts(fn, cache, tokens, stream)) != MX_OK ||
+        (st = check_most(fn, cache, tokens, max_new, stream)) != MX_OK)
         return st;
     // a row's position is below 2^31 - 1 (past the table too): a window of that many positions hides none
     const int64_t far = ((int64_t)1 << 31) - 1;

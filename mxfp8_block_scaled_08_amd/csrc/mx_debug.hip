@@ -13,6 +13,7 @@
 
 #include <atomic>
 #include <climits>
+#include <cstdint>
 
 namespace mx {
 
@@ -25,10 +26,10 @@ static __device__ __align__(256) int debug_flags[DEBUG_SLOTS];
 // One workgroup: entry g of off[0..G] fails when it is outside [0, total],
 // not a multiple of align, (first_zero) g == 0 and nonzero, (exact_end)
 // g == G and not total, or (g < G) the range [off[g], off[g+1]) is shorter
-// than min_len (negative included).  *flag = the first failing g + 1, or 0.
+// than min_len (negative included) or longer than max_len.  *flag = the first failing g + 1, or 0.
 __global__ __launch_bounds__(256) void check_offsets_kernel(const int64_t *__restrict__ off, int64_t G,
                                                             int64_t total, int64_t align, int64_t min_len,
-                                                            int first_zero, int exact_end, int *flag)
+                                                            int64_t max_len, int first_zero, int exact_end, int *flag)
 {
     __shared__ int s_bad;
     if (threadIdx.x == 0)
@@ -43,7 +44,7 @@ __global__ __launch_bounds__(256) void check_offsets_kernel(const int64_t *__res
         if (g == G && exact_end)
             ok = ok && v == total;
         if (g < G)
-            ok = ok && off[g + 1] - v >= min_len;
+            ok = ok && off[g + 1] - v >= min_len && off[g + 1] - v <= max_len;
         if (!ok)
             bad = min(bad, (int)g);
     }
@@ -53,8 +54,8 @@ __global__ __launch_bounds__(256) void check_offsets_kernel(const int64_t *__res
         *flag = s_bad == INT_MAX ? 0 : s_bad + 1;
 }
 
-hipError_t check_offsets(const int64_t *off, int64_t G, int64_t total, int64_t align, int64_t min_len,
-                         bool first_zero, bool exact_end, hipStream_t stream, int64_t *first_bad)
+static hipError_t check(const int64_t *off, int64_t G, int64_t total, int64_t align, int64_t min_len,
+                        int64_t max_len, bool first_zero, bool exact_end, hipStream_t stream, int64_t *first_bad)
 {
     *first_bad = -1;
     void *base = nullptr;
@@ -64,7 +65,7 @@ hipError_t check_offsets(const int64_t *off, int64_t G, int64_t total, int64_t a
     static std::atomic<unsigned> next{0};
     int *flag = (int *)base + next.fetch_add(1) % DEBUG_SLOTS;
     hipLaunchKernelGGL(check_offsets_kernel, dim3(1), dim3(256), 0, stream, off, G, total, align, min_len,
-                       (int)first_zero, (int)exact_end, flag);
+                       max_len, (int)first_zero, (int)exact_end, flag);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
@@ -77,6 +78,18 @@ hipError_t check_offsets(const int64_t *off, int64_t G, int64_t total, int64_t a
         return e;
     *first_bad = h - 1;
     return hipSuccess;
+}
+
+hipError_t check_offsets(const int64_t *off, int64_t G, int64_t total, int64_t align, int64_t min_len,
+                         bool first_zero, bool exact_end, hipStream_t stream, int64_t *first_bad)
+{
+    return check(off, G, total, align, min_len, INT64_MAX, first_zero, exact_end, stream, first_bad);
+}
+
+hipError_t check_longest(const int64_t *off, int64_t G, int64_t total, int64_t max_len, hipStream_t stream,
+                         int64_t *first_bad)
+{
+    return check(off, G, total, 1, 0, max_len, false, false, stream, first_bad);
 }
 
 }  // namespace mx

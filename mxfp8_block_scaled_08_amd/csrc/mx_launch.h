@@ -266,5 +266,8 @@ hipError_t launch_kv_attention(const KvView &c, const KvQueries &q, void *ws, hi
 // off[0] == 0 if first_zero, off[G] == total if exact_end), or -1.
 hipError_t check_offsets(const int64_t *off, int64_t G, int64_t total, int64_t align, int64_t min_len,
                          bool first_zero, bool exact_end, hipStream_t stream, int64_t *first_bad);
+// Likewise: *first_bad = the first range that is longer than max_len (or decreasing, or outside [0, total]).
+hipError_t check_longest(const int64_t *off, int64_t G, int64_t total, int64_t max_len, hipStream_t stream,
+                         int64_t *first_bad);
 
 }  // namespace mx

@@ -219,3 +219,16 @@ def test_binding_refusals(gpu_lib):
     empty = Batch(19, [0, 0], [3, 4], 2, 64, 16)
     gpu_lib.mx_kv_append(k[:0], k[:0], *empty.args)
     assert gpu_lib.mx_kv_read(*empty.args, 0)[0].shape == (0, 2, 64)
+
+
+def test_debug_checks_the_most_rows(gpu_lib, monkeypatch):
+    """MX_DEBUG finds a sequence with more rows than max_new says."""
+    B = Batch(22, [3, 4, 0], [0, 5, 9], 1, 64, 16)
+    q = bf16(B.rng, 7, 1, 64).cuda()
+    monkeypatch.setenv("MX_DEBUG", "1")
+    for most in (0, 4, 5, 1 << 40):
+        gpu_lib.mx_kv_attention(q, *B.args, max_new=most)
+    for most, at in ((3, 1), (2, 0), (1, 0)):
+        with pytest.raises(gpu_lib.MxError, match=rf"max_new.*seq_starts\[{at}\]") as e:
+            gpu_lib.mx_kv_attention(q, *B.args, max_new=most)
+        assert e.value.status == gpu_lib.MX_ERR_INVALID_ARG

@@ -43,7 +43,8 @@ typedef enum mx_rope_scaling {
     MX_ROPE_PLAIN = 0,
     MX_ROPE_LINEAR = 1,
     MX_ROPE_NTK = 2,
-    MX_ROPE_YARN = 3
+    MX_ROPE_YARN = 3,
+    MX_ROPE_YARN_PAIRS = 4
 } mx_rope_scaling;
 
 /*
@@ -56,11 +57,20 @@ typedef enum mx_rope_scaling {
  *           pair as LINEAR, the fastest as PLAIN
  *   YARN    f_i (g_i + (1 - g_i) / factor), g_i = (original_len f_i / (2 pi) - 1) / 31
  *           clamped to [0, 1]: pairs that turn less than once in original_len
- *           positions are interpolated, those over 32 times are kept;
- *           amplitude = 1 + 0.1 ln(factor)
+ *           positions are interpolated, those over 32 times are kept, with a ramp over
+ *           the turns between; amplitude = 1 + 0.1 ln(factor)
+ *   YARN_PAIRS  as YARN, with a ramp over the pairs' numbers: g_i = (hi - i) / (hi - lo)
+ *           clamped to [0, 1], lo = max(floor d(32), 0), hi = min(ceil d(1), rot_dim - 1)
+ *           and at least lo + 0.001, d(r) = rot_dim ln(original_len / (2 pi r)) / (2 ln
+ *           base) the (fractional) pair that turns r times in original_len positions
  * (amplitude 1 for the others; "YaRN: Efficient Context Window Extension", 2023.)
- * Requirements: rot_dim even and >= 2 (4 for NTK), base finite and > 0, factor
- * finite and >= 1, original_len >= 1 for YARN (else MX_ERR_INVALID_ARG).
+ * YARN is the formula that the paper prints.  Checkpoints whose configuration names yarn
+ * scaling are trained and served with YARN_PAIRS' frequencies, and those of the pairs on the
+ * ramp differ: base 10^6, rot_dim 128, factor 4, original_len 32768 keep 0.53 of pair
+ * 31's there and 0.18 by YARN.  For such a checkpoint take YARN_PAIRS.
+ * Requirements: rot_dim even and >= 2 (4 for NTK), at most 2^20, base finite and > 0 (> 1
+ * for YARN_PAIRS), factor finite and >= 1, original_len >= 1 for YARN and YARN_PAIRS
+ * (else MX_ERR_INVALID_ARG).
  */
 mx_status mx_rope_frequencies(int64_t rot_dim, double base, int scaling, double factor, int64_t original_len,
                               double *freqs, float *amplitude);

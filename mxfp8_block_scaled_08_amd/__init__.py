@@ -39,7 +39,7 @@ __all__ = [
     "mx_grouped_gemm_fp4", "MX_SCORE_SOFTMAX", "MX_SCORE_SIGMOID",
     "mx_rope_frequencies", "mx_rope", "mx_rope_bwd", "mx_kv_append", "mx_kv_read", "mx_kv_attention",
     "mx_kv_attention_workspace_bytes", "MX_KV_BLOCK", "MX_ROPE_HALF", "MX_ROPE_INTERLEAVED", "MX_ROPE_PLAIN",
-    "MX_ROPE_LINEAR", "MX_ROPE_NTK", "MX_ROPE_YARN",
+    "MX_ROPE_LINEAR", "MX_ROPE_NTK", "MX_ROPE_YARN", "MX_ROPE_YARN_PAIRS",
 ]
 
 MX_OK, MX_ERR_INVALID_ARG, MX_ERR_SHAPE, MX_ERR_ALIGN = 0, 1, 2, 3
@@ -795,5 +795,5 @@ from .moe_fp4 import (MX_SCORE_SIGMOID, MX_SCORE_SOFTMAX, mx_dequantize_fp4, mx_
 
 # rotary positions, the 8-bit paged cache and its attention (include/mxfp8_kv.h)
 from .kv import (MX_KV_BLOCK, MX_ROPE_HALF, MX_ROPE_INTERLEAVED, MX_ROPE_LINEAR, MX_ROPE_NTK, MX_ROPE_PLAIN,  # noqa: E402
-                 MX_ROPE_YARN, mx_kv_append, mx_kv_attention, mx_kv_attention_workspace_bytes, mx_kv_read, mx_rope,
-                 mx_rope_bwd, mx_rope_frequencies)
+                 MX_ROPE_YARN, MX_ROPE_YARN_PAIRS, mx_kv_append, mx_kv_attention, mx_kv_attention_workspace_bytes,
+                 mx_kv_read, mx_rope, mx_rope_bwd, mx_rope_frequencies)

@@ -203,30 +203,41 @@ mx_status mx_rope_frequencies(int64_t rot_dim, double base, int scaling, double 
                               double *freqs, float *amplitude)
 {
     const char *fn = "mx_rope_frequencies";
-    if (scaling < MX_ROPE_PLAIN || scaling > MX_ROPE_YARN)
+    if (scaling < MX_ROPE_PLAIN || scaling > MX_ROPE_YARN_PAIRS)
         return fail(MX_ERR_INVALID_ARG, "%s: scaling=%d is no mx_rope_scaling", fn, scaling);
     if (rot_dim < (scaling == MX_ROPE_NTK ? 4 : 2) || rot_dim % 2 != 0 || rot_dim > (int64_t)1 << 20)
         return fail(MX_ERR_INVALID_ARG, "%s: rot_dim=%lld must be even, at least 2 (4 for MX_ROPE_NTK) and at most 2^20", fn,
                     (long long)rot_dim);
     if (!std::isfinite(base) || base <= 0.0 || !std::isfinite(factor) || factor < 1.0)
         return fail(MX_ERR_INVALID_ARG, "%s: base must be finite and positive, factor finite and at least 1", fn);
-    if (scaling == MX_ROPE_YARN && original_len < 1)
+    const bool yarn = scaling == MX_ROPE_YARN || scaling == MX_ROPE_YARN_PAIRS;
+    if (scaling == MX_ROPE_YARN_PAIRS && base <= 1.0)
+        return fail(MX_ERR_INVALID_ARG, "%s: base must be above 1 for MX_ROPE_YARN_PAIRS", fn);
+    if (yarn && original_len < 1)
         return fail(MX_ERR_INVALID_ARG, "%s: original_len=%lld must be at least 1", fn, (long long)original_len);
     if (!freqs || !amplitude)
         return fail(MX_ERR_INVALID_ARG, "%s: null pointer", fn);
     const double r = (double)rot_dim;
     const double b = scaling == MX_ROPE_NTK ? base * std::pow(factor, r / (r - 2.0)) : base;
+    const double len = (double)original_len;
+    double lo = 0.0, hi = 0.0;  // MX_ROPE_YARN_PAIRS: pairs up to lo are kept, from hi on interpolated
+    if (scaling == MX_ROPE_YARN_PAIRS) {
+        const auto pair = [&](double rounds) { return r * std::log(len / (TWO_PI * rounds)) / (2.0 * std::log(base)); };
+        lo = std::max(std::floor(pair(32.0)), 0.0);
+        hi = std::max(std::min(std::ceil(pair(1.0)), r - 1.0), lo + 0.001);
+    }
     for (int64_t i = 0; i < rot_dim / 2; i++) {
         double f = std::pow(b, -2.0 * (double)i / r);
         if (scaling == MX_ROPE_LINEAR) {
             f /= factor;
-        } else if (scaling == MX_ROPE_YARN) {
-            const double g = std::min(std::max(((double)original_len * f / TWO_PI - 1.0) / 31.0, 0.0), 1.0);
+        } else if (yarn) {
+            const double at = scaling == MX_ROPE_YARN ? (len * f / TWO_PI - 1.0) / 31.0 : (hi - (double)i) / (hi - lo);
+            const double g = std::min(std::max(at, 0.0), 1.0);
             f = f * g + f / factor * (1.0 - g);
         }
         freqs[i] = f;
     }
-    *amplitude = scaling == MX_ROPE_YARN ? (float)(1.0 + 0.1 * std::log(factor)) : 1.0f;
+    *amplitude = yarn ? (float)(1.0 + 0.1 * std::log(factor)) : 1.0f;
     return ok();
 }
 

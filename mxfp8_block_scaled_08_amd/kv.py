@@ -26,11 +26,12 @@ from . import MX_BF16, MX_F32, _check, load
 from .moe_fp4 import _at, _current, _elsewhere, _one_of, _out_at, _scratch
 
 MX_ROPE_HALF, MX_ROPE_INTERLEAVED = 0, 1
-MX_ROPE_PLAIN, MX_ROPE_LINEAR, MX_ROPE_NTK, MX_ROPE_YARN = 0, 1, 2, 3
+MX_ROPE_PLAIN, MX_ROPE_LINEAR, MX_ROPE_NTK, MX_ROPE_YARN, MX_ROPE_YARN_PAIRS = 0, 1, 2, 3, 4
 MX_KV_BLOCK = 16
 
 _STYLES = {"half": MX_ROPE_HALF, "interleaved": MX_ROPE_INTERLEAVED}
-_SCALINGS = {"plain": MX_ROPE_PLAIN, "linear": MX_ROPE_LINEAR, "ntk": MX_ROPE_NTK, "yarn": MX_ROPE_YARN}
+_SCALINGS = {"plain": MX_ROPE_PLAIN, "linear": MX_ROPE_LINEAR, "ntk": MX_ROPE_NTK, "yarn": MX_ROPE_YARN,
+             "yarn_pairs": MX_ROPE_YARN_PAIRS}
 _TYPES = {torch.bfloat16: MX_BF16, torch.float32: MX_F32}
 _BF, _U8, _I32, _I64, _F64 = torch.bfloat16, torch.uint8, torch.int32, torch.int64, torch.float64
 _i, _l, _f, _d, _p = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_double, ctypes.c_void_p
@@ -118,7 +119,10 @@ def _cache(kv, kv_scale, page_table, kv_lens, seq_starts, dev) -> Tuple[bytes, i
 def mx_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
                         original_len: int = 0, device="cuda") -> Tuple[torch.Tensor, float]:
     """(freqs float64 [rot_dim / 2] on device, amplitude): radians a position of
-    every rotary pair, scaling 'plain', 'linear', 'ntk' or 'yarn' (include/mxfp8_kv.h)."""
+    every rotary pair, scaling 'plain', 'linear', 'ntk', 'yarn' or 'yarn_pairs'
+    (include/mxfp8_kv.h).  For a checkpoint whose configuration names yarn scaling take
+    'yarn_pairs', which ramps over the pairs' numbers; 'yarn' is the paper's formula,
+    which ramps over the turns and gives other frequencies in between."""
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling must be one of {', '.join(_SCALINGS)}, got {scaling!r}")
     freqs = torch.empty(max(rot_dim // 2, 1), dtype=_F64)

@@ -386,3 +386,43 @@ def test_workspace_query_and_call_take_the_same_sizes():
         assert take(last, 3, heads, 1, 64) and not take(last + 1, 3, heads, 1, 64), heads
     assert take((1 << 27) - 1, 1, 1, 1, 128) and not take(1 << 27, 1, 1, 1, 128) and not take(1 << 62, 1, 1, 1, 128)
     assert not take(5, 3, 1 << 62, 2, 128)
+
+
+def test_yarn_over_the_pairs():
+    """The ramp over the pairs' numbers.  Base 10^6, 128 elements, 32768 positions: pair 23.6 turns 32 times, pair 39.7 once
+    (64 ln(32768 / (64 pi)) / ln 10^6 and 64 ln(32768 / (2 pi)) / ln 10^6), so pairs up to 23 are kept, from 40 on
+    interpolated, pair 31 keeps 9 parts of 17."""
+    near = dict(rtol=1e-13, atol=0)
+    f = 1e6 ** (-2.0 * np.arange(64) / 128)
+    got, amp = mx.mx_rope_frequencies(128, 1e6, "yarn_pairs", 4.0, 32768, device="cpu")
+    got = got.numpy()
+    assert amp == np.float32(1 + 0.1 * math.log(4.0))
+    np.testing.assert_allclose(got[:24], f[:24], **near)
+    np.testing.assert_allclose(got[40:], f[40:] / 4, **near)
+    keep = (40 - np.arange(24, 40)) / 17
+    assert keep[31 - 24] == 9 / 17
+    np.testing.assert_allclose(got[24:40], f[24:40] * keep + f[24:40] / 4 * (1 - keep), **near)
+    # the paper's ramp over the turns keeps less of it
+    other, _ = mx.mx_rope_frequencies(128, 1e6, "yarn", 4.0, 32768, device="cpu")
+    assert other.numpy()[31] < 0.65 * got[31]
+    # nothing to scale; all pairs fast; all pairs slow but the first; a ramp that starts before the first pair
+    np.testing.assert_allclose(mx.mx_rope_frequencies(128, 1e6, "yarn_pairs", 1.0, 32768, device="cpu")[0].numpy(), f, **near)
+    np.testing.assert_allclose(mx.mx_rope_frequencies(128, 1e6, "yarn_pairs", 4.0, 1 << 40, device="cpu")[0].numpy(), f, **near)
+    got = mx.mx_rope_frequencies(128, 1e6, "yarn_pairs", 4.0, 1, device="cpu")[0].numpy()
+    np.testing.assert_allclose(got[1:], f[1:] / 4, **near)
+    # 64 ln(64 / (2 pi)) / ln 10^6 = 10.75: from pair 11 on interpolated, the ramp from pair 0
+    got = mx.mx_rope_frequencies(128, 1e6, "yarn_pairs", 8.0, 64, device="cpu")[0].numpy()
+    keep = np.clip((11 - np.arange(64)) / 11, 0, 1)
+    np.testing.assert_allclose(got, f * keep + f / 8 * (1 - keep), **near)
+    assert mx.mx_rope_frequencies(2, 1e4, "yarn_pairs", 4.0, 4096, device="cpu")[0].shape == (1,)
+
+
+def test_yarn_over_the_pairs_refusals():
+    buf = (ctypes.c_double * 64)()
+    amp = ctypes.c_float()
+    f = lambda *a: kv._fn("mx_rope_frequencies")(*a, ctypes.addressof(buf), ctypes.addressof(amp))  # noqa: E731
+    assert f(64, 1e4, mx.MX_ROPE_YARN_PAIRS, 4.0, 4096) == mx.MX_OK
+    for bad in ((64, 1.0, 4, 4.0, 4096), (64, 0.5, 4, 4.0, 4096), (64, 1e4, 4, 4.0, 0), (64, 1e4, 4, 0.9, 4096), (63, 1e4, 4, 4.0, 4096),
+                (64, 1e4, 5, 4.0, 4096)):
+        assert f(*bad) == INV, bad
+        assert "mx_rope_frequencies" in mx.mx_last_error()

@@ -85,8 +85,9 @@ mx_status mx_rope_frequencies(int64_t rot_dim, double base, int scaling, double 
  *              (t, h, d) at t * ld_t + h * ld_h + d (ld_xt, ld_xh; ld_yt, ld_yh)
  *   positions  DEVICE int32 [tokens], any sign
  *   freqs      DEVICE double [rot_dim / 2] (mx_rope_frequencies')
- * The angle is reduced in 64 bits, so far positions lose nothing; products in
- * FP32, the result rounded once.
+ * The angle is formed and reduced in 64 bits, off by at most 3 * 2^-53 of itself (less than
+ * half an FP32 step of its sine up to 2^26 radians, 2^-20 at 2^31), sine and cosine by
+ * 2^-41 more; both rounded to FP32, products in FP32, the result rounded once.
  * y may be x itself (same pointer and strides).  Requirements: tokens, heads >= 0,
  * head_dim >= 1, style one of the two, amplitude finite, strides that leave the
  * (t, h) rows apart, tokens outside or heads outside (else MX_ERR_INVALID_ARG);
@@ -142,11 +143,14 @@ typedef struct mx_kv_cache {
  * otherwise.  New values are rounded to the nearest E4M3 (ties to even) of that scale;
  * NaN and infinities become the code 0x7F; where c > c_old the older positions' codes of
  * the block are rounded anew.  Other than the MX rule's floor(log2 amax) - 8, c_new
- * clamps nothing, so a block that grows never holds a clamped value.
+ * clamps nothing, so a block that grows never holds a clamped value.  (At c = 247, the
+ * largest that finite values need, those from 248 * 2^120 on round to 2^128 and are read
+ * back infinite.)
  *   k, v   BF16 [tokens][kv_heads][head_dim], strides ld_kt, ld_kh / ld_vt, ld_vh
  *   freqs  DEVICE double [rot_dim / 2]: keys are turned first, by their position in the
- *          cache (mx_rope's formula), in 64 bits: the rounding to E4M3 is the only one
- *          (beyond FP32's range they count as infinite);
+ *          cache (mx_rope's formula, angles and their sines as there), in 64-bit products:
+ *          the rounding to E4M3 is the only one (beyond FP32's range they count as
+ *          infinite);
  *          null: keys as they are (rot_dim, style, amplitude not used)
  * A block that is written may stand at one place of the call's tables only (pages that
  * several sequences read, as a shared prefix, are not written).  Deterministic.
@@ -164,7 +168,10 @@ mx_status mx_kv_append(const mx_kv_cache *cache, const void *k, int64_t ld_kt, i
  * The values that the cache holds for the call's rows: what mx_kv_append with the same
  * sequences wrote (n_b = kv_lens[b] gives a sequence whole).
  *   k, v  [tokens][kv_heads][head_dim] contiguous, of dtype (MX_BF16 or MX_F32), out;
- *         either may be null.  Exact in both; rows that the cache does not hold are zeros.
+ *         either may be null.  Rows that the cache does not hold are zeros.
+ * FP32 holds every value exactly, infinities for those of 2^128 and more (finite codes of
+ * scale codes from 247 on); BF16 does from scale code 3 on, smaller values are rounded to
+ * nearest even where they pass its last bit, 2^-133.
  * Requirements beyond the cache's: dtype one of the two (else MX_ERR_INVALID_ARG); k and v
  * 16-byte aligned (else MX_ERR_ALIGN); they overlap nothing (else MX_ERR_OVERLAP).
  */
@@ -184,12 +191,14 @@ mx_status mx_kv_read(const mx_kv_cache *cache, int64_t tokens, void *k, void *v,
  *            checks it).  Given, a step of few rows saves launches and workspace.
  *   workspace  DEVICE scratch of mx_kv_attention_workspace_bytes(...) bytes, 16-byte
  *            aligned (partial sums where the cache is split over workgroups; null if 0)
- * The cache's values enter as BF16: exact but beyond its range (scales from 2^120 on),
- * where they are infinite.  Products of queries and keys are exact; scores, exponentials,
- * sums and outputs are formed in FP32, the weights exp(s_j - max) rounded to BF16 for the
- * product with the values; one rounding of the output.  A score beyond FP32's range gives
- * NaN.  The order of the sums depends on the sizes, the tables' contents and the device's
- * compute-unit count: the same call gives the same bytes.
+ * The cache's values enter as the BF16 that mx_kv_read gives: exact but at the ends of the
+ * range (scale codes 0..2 and from 247 on).  Products of queries and keys are exact;
+ * scores, exponentials, sums and outputs are formed in FP32, the weights exp(s_j - max)
+ * rounded to BF16 for the product with the values; one rounding of the output.  A score or
+ * a scale that passes FP32's range when it is multiplied by log2(e) gives NaN.  Weights may
+ * stay up to 2^8 until the end, so values whose sum times 2^8 passes FP32's range may give
+ * infinities.  The order of the sums depends on the sizes, the tables' contents and the
+ * device's compute-unit count: the same call gives the same bytes.
  * mx_kv_attention_workspace_bytes is host-only (0 for sizes that the call refuses too).
  * Requirements beyond the cache's: q_heads a multiple of kv_heads, scale finite and >= 0,
  * window >= 0 and 0 unless causal, max_new >= 0, the workspace large enough (else

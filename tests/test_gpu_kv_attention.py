@@ -288,3 +288,25 @@ def test_windows_that_reach_far(gpu_lib):
             _run(gpu_lib, B, 2, window=window)
             _run(gpu_lib, B, 2, window=window, max_new=70)
     assert cap < 2 ** 30
+
+
+def test_values_at_the_ends_of_the_scales(gpu_lib):
+    """One visible position: the value comes back as mx_kv_read's BF16, subnormal and infinite ones too."""
+    codes = [0, 1, 2, 3, 5, 8, 246, 247, 248, 254]
+    n = len(codes)
+    for rows, kv_heads in ((1, 4), (70, 4)):
+        B = Batch(42, [1] * n, [0] * n, kv_heads, 64, 16, filled=False)
+        flat = np.arange(kv_heads * 64) % 256
+        flat[(flat & 127) == 127] = 0x31
+        B.ref.scale[0] = 120
+        B.ref.kv[0] = 0x38
+        for b, c in enumerate(codes):
+            B.ref.kv[1, B.table[b, 0], :, 0] = flat.reshape(kv_heads, 64)
+            B.ref.scale[1, B.table[b, 0]] = c
+        B.kv.copy_(torch.from_numpy(B.ref.kv))
+        B.scale.copy_(torch.from_numpy(B.ref.scale))
+        _, v = gpu_lib.mx_kv_read(*B.args, n)
+        q = bf16(B.rng, n, kv_heads * rows, 64).cuda()
+        out = gpu_lib.mx_kv_attention(q, *B.args)
+        assert torch.isinf(v).any() and (v[v != 0].abs().min() < 2.0 ** -130)
+        assert torch.equal(out, v.repeat_interleave(rows, 1)), rows

@@ -232,3 +232,50 @@ def test_debug_checks_the_most_rows(gpu_lib, monkeypatch):
         with pytest.raises(gpu_lib.MxError, match=rf"max_new.*seq_starts\[{at}\]") as e:
             gpu_lib.mx_kv_attention(q, *B.args, max_new=most)
         assert e.value.status == gpu_lib.MX_ERR_INVALID_ARG
+
+
+def test_reading_at_the_ends_of_the_scales(gpu_lib):
+    """Every finite code at the smallest and the largest scales: FP32 holds the value, or is infinite beyond its range;
+    BF16 rounds to nearest where its last bit (2^-133) does not reach."""
+    codes = [0, 1, 2, 3, 4, 7, 8, 120, 127, 200, 246, 247, 248, 250, 254]
+    B = Batch(23, [0], [16 * len(codes)], 1, 64, 16, filled=False)
+    B.starts[1] = B.lens[0]
+    flat = np.arange(16 * 64) % 256
+    flat[(flat & 127) == 127] = 0x31
+    for i, c in enumerate(codes):
+        B.ref.kv[:, B.table[0, i], 0] = flat.reshape(16, 64)
+        B.ref.scale[:, B.table[0, i], 0, 0] = c
+    B.kv.copy_(torch.from_numpy(B.ref.kv))
+    B.scale.copy_(torch.from_numpy(B.ref.scale))
+    rows = int(B.lens[0])
+    want = B.ref.read(B.starts, B.lens, rows)
+    with np.errstate(over="ignore"):
+        f32 = want.astype(np.float32)  # exact, or infinite
+    assert (np.isinf(f32) | (f32 == want)).all() and np.isinf(f32).any()
+    # to nearest even by hand: the step of a BF16 value is 2^(exponent - 7), 2^-133 at least; beyond FP32's range infinite
+    with np.errstate(divide="ignore"):
+        step = 2.0 ** np.maximum(np.floor(np.log2(np.abs(want))) - 7, -133)
+    near = np.where(np.isinf(f32), f32, np.rint(want / step) * step)
+    assert (near != want)[:, :48].any() and (near == want)[:, 48:][np.isfinite(f32[:, 48:])].all()
+    for dtype, w in ((torch.float32, f32), (BF, near)):
+        k, v = gpu_lib.mx_kv_read(*B.args, rows, out_dtype=dtype)
+        for got, x in ((k, w[0]), (v, w[1])):
+            assert np.array_equal(got.double().cpu().numpy(), x.astype(np.float64)), dtype
+
+
+def test_the_largest_values_come_back_infinite(gpu_lib):
+    """A finite value that rounds to 2^128 is beyond FP32 when it is read: from 248 * 2^120 on, whose tie goes to the even
+    code."""
+    B = Batch(24, [4], [0], 1, 64, 16)
+    x = torch.zeros(4, 1, 64)
+    for i, m in enumerate((240, 247, 248, 255)):
+        x[i] = m * 2.0 ** 120
+        x[i, :, 1::2] *= -1
+    k = x.to(BF)
+    assert torch.equal(k.float(), x)
+    _append(gpu_lib, B, k.cuda(), (-k).cuda())
+    gk, gv = gpu_lib.mx_kv_read(*B.args, 4)
+    want = x.double()
+    want[1] = want[0]
+    want[2:] *= float("inf")
+    assert torch.equal(gk.double().cpu(), want) and torch.equal(gv.double().cpu(), -want)

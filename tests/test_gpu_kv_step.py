@@ -200,3 +200,64 @@ def test_after_a_projection(gpu_lib):
     S.run()
     torch.cuda.synchronize()
     _check(mx, S, B, _pos(B))
+
+
+def _fresh(S, before, qkv):
+    """The step's buffers as before its append, with other rows; whatever a step leaves is garbage."""
+    S.kv.copy_(before[0])
+    S.scale.copy_(before[1])
+    S.qkv.copy_(qkv)
+    S.q.fill_(9.0)
+    S.out.fill_(5.0)
+    S.lse.fill_(float("nan"))
+    S.ws.fill_(255)
+
+
+def _left(S):
+    return [t.clone() for t in (S.q, S.kv, S.scale, S.out, S.lse)]
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_two_steps_at_once_from_fresh_buffers(gpu_lib, captured):
+    """Two steps on two streams, eager or replayed, on other rows every time and from the cache as it was: each of their
+    three calls has to run, in its order, for the bytes of the same steps one after the other."""
+    mx = gpu_lib
+    B = [Batch(90 + i, [1, 1, 70], [200, 5, 33], HK, D, 64, room=1500) for i in range(2)]
+    S = [Step(mx, b, bf16(b.rng, b.rows, HQ + 2 * HK, D).cuda()) for b in B]
+    before = [(s.kv.clone(), s.scale.clone()) for s in S]
+    for s, b in zip(S, B):
+        s.pos.copy_(torch.from_numpy(_pos(b)))
+    st = [torch.cuda.Stream(), torch.cuda.Stream()]
+    graphs = []
+    if captured:
+        for s, stream in zip(S, st):
+            g = torch.cuda.CUDAGraph()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(g, stream=stream):
+                s.run()
+            graphs.append(g)
+    last = None
+    for rep in range(3):
+        rows = [bf16(b.rng, b.rows, HQ + 2 * HK, D).cuda() for b in B]
+        want = []
+        for s, w, x in zip(S, before, rows):
+            _fresh(s, w, x)
+            s.run()
+            torch.cuda.synchronize()
+            want.append(_left(s))
+        assert last is None or not torch.equal(want[0][3], last)
+        last = want[0][3]
+        for s, w, x in zip(S, before, rows):
+            _fresh(s, w, x)
+        torch.cuda.synchronize()
+        for i in range(2):
+            if captured:
+                with torch.cuda.stream(st[i]):
+                    graphs[i].replay()
+            else:
+                S[i].run(stream=st[i])
+        torch.cuda.synchronize()
+        for s, w in zip(S, want):
+            for a, b in zip(_left(s), w):
+                assert torch.equal(a, b)
+        assert all(torch.isfinite(w[3].float()).all() and torch.isfinite(w[4]).all() for w in want)

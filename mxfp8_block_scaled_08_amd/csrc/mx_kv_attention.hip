@@ -12,8 +12,12 @@
 //
 // One pass with a running maximum m and sum l per row.  The maximum is raised only where a
 // score passes it by more than 2^8 (weights stay below 2^8: neither FP32 nor BF16 minds), so the
-// accumulators are rarely rescaled.  Weights are rounded to BF16 for the product with V, the
-// sum takes them unrounded.
+// accumulators are rarely rescaled.  The product with V takes weights as BF16, the type in which the
+// matrix cores hold V exactly (FP16 has the bits, but not the range of the blocks' scales); the sum
+// takes them unrounded.  Where a head has up to 16 rows a second product adds what BF16 loses, for
+// nothing (see REST): the outputs' error is then that of their own rounding (norm of the difference
+// over norm, 64 sequences of up to 16 k positions: 2.0e-3 without, 1.7e-3 with it).  Prompts do
+// without it (2.2e-3): it would take them from 873 to 1151 us (the four below).
 //
 // Few rows (up to 64 a sequence and head; a sampler's step): kv_rows_kernel.  Bound by reading the
 // cache.  A wave reads 32 positions' codes straight into registers in the matrix cores' layout, V
@@ -271,9 +275,9 @@ union Frag {
 };
 
 // V^T, 16 elements by the wave's 32 positions at a time: into(j, fragment) for the D / 16 tiles of elements
-// (D / 16) m + j; V's words as in Codes.
-template <int D, typename F>
-__device__ __forceinline__ void value_tiles(const uint32_t (&v)[8][D / 64], const uint32_t (&vs)[2], F into)
+// (D / 16) m + j (several: one after the other for every four tiles); V's words as in Codes.
+template <int D, typename... F>
+__device__ __forceinline__ void value_tiles(const uint32_t (&v)[8][D / 64], const uint32_t (&vs)[2], F... into)
 {
     const float s0 = cvt_scale(vs[0]), s1 = cvt_scale(vs[1]);
 #pragma unroll
@@ -290,9 +294,12 @@ __device__ __forceinline__ void value_tiles(const uint32_t (&v)[8][D / 64], cons
             a[2].w[e] = e4m3_bf16<false>(hi, s);
             a[3].w[e] = e4m3_bf16<true>(hi, s);
         }
+        const auto four = [&](auto &f) {
 #pragma unroll
-        for (int j = 0; j < 4; j++)
-            into(4 * w + j, a[j]);
+            for (int j = 0; j < 4; j++)
+                f(4 * w + j, a[j]);
+        };
+        (four(into), ...);
     }
 }
 
@@ -332,10 +339,16 @@ __device__ __forceinline__ void scores(const RowState<D, NT> &r, const Codes<D> 
     }
 }
 
-// The weights of the positions that vis has bits for (4 j + i; all if !MASKED), the running maxima and sums.
+// Whether what a weight loses as BF16 goes through the matrix cores as well: with one tile of rows they have the time (64
+// sequences of up to 16 k positions 224 us either way, two long ones 36, one of 701 12.2 -> 12.5); with two it costs 8 %
+// (heads of 64) to 16 % (of 128, whose registers spill: 32 sequences of 16 rows a head 140 -> 163 us).
+template <int NT> constexpr bool REST = NT == 1;
+
+// The weights of the positions that vis has bits for (4 j + i; all if !MASKED) and what they lose as BF16, the running
+// maxima and sums.
 template <int D, int NT, bool MASKED>
 __device__ __forceinline__ void weights(RowState<D, NT> &r, const f32x4_t (&s)[2][NT], const uint32_t (&vis)[NT], float c2,
-                                        Frag (&p)[NT])
+                                        Frag (&p)[NT], Frag (&rest)[NT])
 {
 #pragma unroll
     for (int n = 0; n < NT; n++) {
@@ -361,36 +374,47 @@ __device__ __forceinline__ void weights(RowState<D, NT> &r, const f32x4_t (&s)[2
         }
         r.l[n] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            p[n].w[i] = pack_bf16(e[2 * i], e[2 * i + 1]);
+        for (int i = 0; i < 4; i++) {
+            const uint32_t w = pack_bf16(e[2 * i], e[2 * i + 1]);
+            p[n].w[i] = w;
+            if (REST<NT>)
+                rest[n].w[i] = pack_bf16(e[2 * i] - bf16_lo(w), e[2 * i + 1] - bf16_hi(w));
+        }
     }
 }
 
 template <int D, int NT>
-__device__ __forceinline__ void add_values(RowState<D, NT> &r, const Codes<D> &t, const Frag (&p)[NT])
+__device__ __forceinline__ void add_values(RowState<D, NT> &r, const Codes<D> &t, const Frag (&p)[NT],
+                                           const Frag (&rest)[NT])
 {
-    value_tiles<D>(t.v, t.vs, [&](int j, const Frag &a) {
+    const auto add = [&](const Frag (&x)[NT]) {
+        return [&](int j, const Frag &a) {
 #pragma unroll
-        for (int n = 0; n < NT; n++)
-            r.o[n][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.f, p[n].f, r.o[n][j], 0, 0, 0);
-    });
+            for (int n = 0; n < NT; n++)
+                r.o[n][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.f, x[n].f, r.o[n][j], 0, 0, 0);
+        };
+    };
+    if constexpr (REST<NT>)
+        value_tiles<D>(t.v, t.vs, add(p), add(rest));
+    else
+        value_tiles<D>(t.v, t.vs, add(p));
 }
 
-// Whether a wave's 32 positions need masked_step: a page is not there, or a scale is NaN.
+// Whether a wave's 32 positions need masked_step: a page is not there, a scale is NaN, or values may be infinite.
 template <int D> __device__ __forceinline__ bool irregular(const Codes<D> &t)
 {
-    return !t.ok[0] || !t.ok[1] || __any(max(max(t.ks[0], t.ks[1]), max(t.vs[0], t.vs[1])) == 0xFFu);
+    return !t.ok[0] || !t.ok[1] || __any(max(t.ks[0], t.ks[1]) == 0xFFu || max(t.vs[0], t.vs[1]) >= KVA_BIG_SCALE);
 }
 
 // 32 positions that every row sees.
 template <int D, int NT> __device__ __forceinline__ void plain_step(RowState<D, NT> &r, const Codes<D> &t, float c2)
 {
     f32x4_t s[2][NT];
-    Frag p[NT];
+    Frag p[NT], rest[NT];
     scores<D, NT>(r, t, s);
     const uint32_t vis[NT] = {};
-    weights<D, NT, false>(r, s, vis, c2, p);
-    add_values<D, NT>(r, t, p);
+    weights<D, NT, false>(r, s, vis, c2, p, rest);
+    add_values<D, NT>(r, t, p, rest);
 }
 
 // 32 positions from t0 on, of which a row sees what it sees.
@@ -399,7 +423,7 @@ __device__ __forceinline__ void masked_step(RowState<D, NT> &r, Codes<D> &t, int
 {
     const int g = (threadIdx.x & 63) >> 4;
     f32x4_t s[2][NT];
-    Frag p[NT];
+    Frag p[NT], rest[NT];
     scores<D, NT>(r, t, s);
     uint32_t vis[NT] = {};  // bit 4 j + i: the row sees position t0 + 16 j + 4 g + i
 #pragma unroll
@@ -413,7 +437,7 @@ __device__ __forceinline__ void masked_step(RowState<D, NT> &r, Codes<D> &t, int
                 vis[n] |= y ? 1u << (4 * j + i) : 0u;
                 s[j][n][i] = !y ? KVA_NEG : t.ks[j] == 0xFFu ? __builtin_nanf("") : s[j][n][i];
             }
-    weights<D, NT, true>(r, s, vis, c2, p);
+    weights<D, NT, true>(r, s, vis, c2, p, rest);
     bool odd = false;
 #pragma unroll
     for (int j = 0; j < 2; j++) {
@@ -435,7 +459,7 @@ __device__ __forceinline__ void masked_step(RowState<D, NT> &r, Codes<D> &t, int
         t.vs[j] = t.vs[j] == 0xFFu ? 127u : t.vs[j];
     }
     if (!__any(odd)) {
-        add_values<D, NT>(r, t, p);
+        add_values<D, NT>(r, t, p, rest);
         return;
     }
     // NaN or infinite values that some row may not see: a weight of 0 does not keep them out of a
@@ -444,8 +468,10 @@ __device__ __forceinline__ void masked_step(RowState<D, NT> &r, Codes<D> &t, int
     for (int at = 0; at < 32; at++) {
         const int mine = (at & 15) >> 2 == g ? 4 * (at >> 4) + (at & 3) : -1;
         const bool there = at < 16 ? t.ok[0] : t.ok[1];
+        // (infinite values go without the remainders: zero, or of the other sign, they would make NaN of them)
+        const bool far = __any((at < 16 ? t.vs[0] : t.vs[1]) >= KVA_BIG_SCALE);
         uint32_t v[8][D / 64];
-        Frag one[NT];
+        Frag one[NT], one_rest[NT];
 #pragma unroll
         for (int e = 0; e < 8; e++)
 #pragma unroll
@@ -454,13 +480,18 @@ __device__ __forceinline__ void masked_step(RowState<D, NT> &r, Codes<D> &t, int
 #pragma unroll
         for (int n = 0; n < NT; n++)
 #pragma unroll
-            for (int i = 0; i < 4; i++)
-                one[n].w[i] = mine == 2 * i ? p[n].w[i] & 0xFFFFu : mine == 2 * i + 1 ? p[n].w[i] & 0xFFFF0000u : 0u;
+            for (int i = 0; i < 4; i++) {
+                const uint32_t keep = mine == 2 * i ? 0xFFFFu : mine == 2 * i + 1 ? 0xFFFF0000u : 0u;
+                one[n].w[i] = p[n].w[i] & keep;
+                one_rest[n].w[i] = REST<NT> ? rest[n].w[i] & keep : 0u;
+            }
         value_tiles<D>(v, t.vs, [&](int j, const Frag &a) {
 #pragma unroll
             for (int n = 0; n < NT; n++) {
                 const bool y = there && t0 + at >= r.see[n].lo && t0 + at <= r.see[n].hi;
-                const f32x4_t o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.f, one[n].f, f32x4_t{0, 0, 0, 0}, 0, 0, 0);
+                f32x4_t o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.f, one[n].f, f32x4_t{0, 0, 0, 0}, 0, 0, 0);
+                if (REST<NT> && !far)
+                    o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.f, one_rest[n].f, o, 0, 0, 0);
                 r.o[n][j] += y ? o : f32x4_t{0, 0, 0, 0};
             }
         });

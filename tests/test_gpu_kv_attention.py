@@ -310,3 +310,26 @@ def test_values_at_the_ends_of_the_scales(gpu_lib):
         out = gpu_lib.mx_kv_attention(q, *B.args)
         assert torch.isinf(v).any() and (v[v != 0].abs().min() < 2.0 ** -130)
         assert torch.equal(out, v.repeat_interleave(rows, 1)), rows
+
+
+@pytest.mark.parametrize("room", ROOM)
+@pytest.mark.parametrize("dim,group", [(64, 1), (64, 16), (128, 7)])
+def test_single_tokens_keep_their_weights(gpu_lib, dim, group, room):
+    """Up to 16 rows a head: a weight reaches the product with the values as two BF16 numbers, off by 2^-8 of 2^-8 of
+    itself, so the outputs are as near as their own rounding and the FP32 sums let them (attention_bounds without the 2^-8 of
+    the weights).  With a NaN outside a window too, where positions go one by one."""
+    kv_heads = 2
+    ctx = [int(c) for c in np.random.default_rng(43).integers(14, 60, 8)]
+    B = Batch(43 + dim + group, [1] * 8, ctx, kv_heads, dim, 16, room=room)
+    q = bf16(B.rng, 8, kv_heads * group, dim, std=0.1)
+    for window in (0, 12):
+        if window:
+            for b in range(8):
+                B.ref.kv[1, B.table[b, 0], :, 1] = 0x7F
+            B.kv.copy_(torch.from_numpy(B.ref.kv))
+        out = gpu_lib.mx_kv_attention(q.cuda(), *B.args, window=window, max_new=1).double().cpu().numpy()
+        want, _, mag, reach = ref = B.ref.attention(q.double().numpy(), B.starts, B.lens, dim ** -0.5, True, window)
+        assert np.isfinite(want).all()
+        bound = attention_bounds(*ref, dim, int(B.lens.max()))[0] - 2.0 ** -8 * mag + 2.0 ** -16 * mag
+        err = np.abs(out - want)
+        assert (err <= bound).all(), ((err > bound).sum(), (err / bound).max())

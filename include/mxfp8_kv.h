@@ -188,7 +188,9 @@ mx_status mx_kv_read(const mx_kv_cache *cache, int64_t tokens, void *k, void *v,
  *   lse      DEVICE float [tokens][q_heads] out, or null
  *   max_new  no sequence has more than max_new rows in this call (0: not known).  Output
  *            rows of a sequence with more are unspecified, also left as they were (MX_DEBUG
- *            checks it).  Given, a step of few rows saves launches and workspace.
+ *            checks it).  Given, a step of few rows saves launches and workspace, and up to
+ *            half its time (64 sequences of up to 16 k positions, 32 heads over 8: 223 us
+ *            against 285; 32 of up to 4 k, 32 over 4: 29 against 57).
  *   workspace  DEVICE scratch of mx_kv_attention_workspace_bytes(...) bytes, 16-byte
  *            aligned (partial sums where the cache is split over workgroups; null if 0)
  * The cache's values enter as the BF16 that mx_kv_read gives: exact but at the ends of the

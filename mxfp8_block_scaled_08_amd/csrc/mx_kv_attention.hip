@@ -25,7 +25,7 @@
 // positions of every (sequence, head, tile of rows), lies on one line that is cut into equal pieces,
 // one a workgroup, so uneven sequences load the chip evenly; pieces of one item meet in
 // kv_join_kernel.  64 sequences of up to 16 k positions, 32 heads over 8 (1.23 GB): 222-229 us, 5.4
-// TB/s, a large copy's 5.0-5.2; two of up to 131 k, 32 heads over 4 (106 MB): 29 us and 6 for the
+// TB/s, a large copy's 5.0-5.2; two of 38 k and 66 k, 32 heads over 4 (106 MB): 27 us and 6 for the
 // join, most of both the start of a launch and the tail's.  Two pieces a compute unit are as many
 // as run at once (two waves a SIMD of 256 registers); one, three or four, and workgroups of eight
 // waves, were slower.
@@ -1302,8 +1302,10 @@ template <int D> static hipError_t launch(const KvView &c, const KvQueries &q, K
 {
     const dim3 block(KVA_THREADS);
     const int64_t positions = (int64_t)c.max_pages << c.page_shift;
-    // A cache of few positions: whole items save the join's launch (one sequence of 701, 32 heads over 8: a call 12.2 us
-    // instead of 14.2, on the GPU 12.0 against 11.4), and beside prompts the few-row kernel's own.
+    // A cache of few positions: whole items save the join's launch, and beside prompts the few-row kernel's own.  32 heads
+    // over 8, every sequence of 701, captured, whole against cut: 1 sequence 12.6 against 11.5 us (a call of its own 12.7
+    // against 14.3, the host's), 8 14.1 either way, 32 16.4 against 20.9, 64 23.6 against 27.8, 65 33 against 33, 128 48
+    // against 55, 256 85 against 95; uneven lengths up to that 8 11.9 either way, 64 19.7 against 31.4, 256 67 against 98.
     s.plan.whole = positions <= KVA_WHOLE;
     if (s.tiles) {
         if (s.plan.whole)

@@ -233,7 +233,7 @@ def mx_kv_attention(q: torch.Tensor, kv: torch.Tensor, kv_scale: torch.Tensor, p
     scale: head_dim^-0.5 if None.  causal: a row sees positions up to its own;
     window > 0: only the last `window` of them.  max_new: the most rows that a
     sequence has in this call (0: not known; a step of few rows then takes more
-    launches).  Rows behind the last sequence are not written; a row that sees
+    launches and up to twice its time, and a single token's weights fewer bits).  Rows behind the last sequence are not written; a row that sees
     nothing gets zeros and -inf.  workspace: device scratch of
     mx_kv_attention_workspace_bytes bytes (a new tensor if None)."""
     dev = q.device

@@ -196,9 +196,9 @@ mx_status mx_kv_read(const mx_kv_cache *cache, int64_t tokens, void *k, void *v,
  * The cache's values enter as the BF16 that mx_kv_read gives: exact but at the ends of the
  * range (scale codes 0..2 and from 247 on).  Products of queries and keys are exact;
  * scores, exponentials, sums and outputs are formed in FP32; the weights exp(s_j - max) are
- * rounded to BF16 for the product with the values, or, where max_new (tokens if it is 0 or
- * more) times q_heads / kv_heads is at most 16, to two BF16 numbers, 16 bits; one rounding
- * of the output.  A score or a scale that passes FP32's range when it is multiplied by
+ * rounded to BF16 for the product with the values, or, where tokens (max_new, if that is
+ * known and less) times q_heads / kv_heads is at most 16, to two BF16 numbers, 16 bits; one
+ * rounding of the output.  A score or a scale that passes FP32's range when it is multiplied by
  * log2(e) gives NaN.  Weights may stay up to 2^8 until the end, so values whose sum times
  * 2^8 passes FP32's range may give infinities.  The order of the sums depends on the sizes,
  * the tables' contents and the device's compute-unit count: the same call gives the same
